@@ -258,6 +258,53 @@ rudder_status_t rudder_linear(const void* Xq, const float* row_scale, const uint
                               uint16_t* Y, int32_t* acc_out, void* stream);
 
 /*
+ * Few-row products with 4-bit weights and group scales (W4A16): the form of a
+ * layer for single tokens and small action sets, where the weights' bytes are
+ * the cost.  Activations stay bf16; each (group of input channels, output
+ * channel) has a bf16 scale of its own.
+ *   s[g][n]   = bf16_rne(fl32(max_{k in g} |W[k][n]| / 7))     (formed in fp64)
+ *   q[k][n]   = rne(clamp(W[k][n] * fl32(1 / s[g][n]), -7, 7))
+ *   t[m][n]   = sum_g s[g][n] * sum_{k in g} q[k][n] * X[m][k]  (fp32 sums)
+ *   Y[m][n]   = bf16_rne(fmaf(a[st][n], t, b[st][n])), st = stream_id[m]
+ * (Y = bf16_rne(t) without compensation).  A zero scale gives codes 0.
+ *
+ * rudder_quantize_weights_grouped prepares a layer once:
+ *   W        bf16 bits [K][N], row-major
+ *   K, N     > 0; K a multiple of group, N any
+ *   group    32, 64 or 128 input channels
+ *   Wq       out: rudder_grouped_weight_bytes(K, N) bytes.  With n and k
+ *            padded to multiples of 16 and 128 (code 0), tile (n / 16, k / 128)
+ *            is 1024 bytes at tile index (n / 16) * (Kpad / 128) + k / 128;
+ *            lane l = n % 16 + 16 * ((k % 32) / 8) has 16 bytes at 16 * l, whose
+ *            little-endian word (k % 128) / 32 holds code k as the nibble q + 8
+ *            at nibble (k % 8) / 2 + 4 * (k % 2)
+ *   g_scale  out: bf16 bits [K / group][ceil(N / 16) * 16], padding 0
+ * Errors: INVALID_ARG for a null pointer, K or N <= 0, a group other than 32,
+ * 64 or 128, K % group != 0, Wq or g_scale not 16-byte aligned; UNSUPPORTED for
+ * K > RUDDER_MAX_K or N > 2^24.
+ *
+ * rudder_matvec_w4 (one launch):
+ *   X          bf16 bits [M][K], row-major
+ *   stream_id  uint8 [M], each < S; NULL with comp_a NULL
+ *   comp_a, comp_b  fp32 [S][N], both or neither (NULL)
+ *   M          >= 0 (M = 0 is a no-op).  Rows go 16 at a time, and every 16
+ *              read the weights once: for many rows use rudder_linear
+ *   Y          out: bf16 bits [M][N], row-major
+ * Errors: INVALID_ARG for a null required pointer, comp_a without comp_b or
+ * stream_id (or comp_b without comp_a), M < 0, K or N <= 0, a bad group,
+ * K % group != 0, S outside 1..8 with compensation, X, Wq or g_scale not
+ * 16-byte aligned; UNSUPPORTED for K > RUDDER_MAX_K, N > 2^24 or M > 2^19.
+ */
+size_t rudder_grouped_weight_bytes(int K, int N);
+size_t rudder_grouped_scale_count(int K, int N, int group);
+rudder_status_t rudder_quantize_weights_grouped(const uint16_t* W, int K, int N, int group,
+                                                uint8_t* Wq, uint16_t* g_scale, void* stream);
+rudder_status_t rudder_matvec_w4(const uint16_t* X, const uint8_t* stream_id, const uint8_t* Wq,
+                                 const uint16_t* g_scale, const float* comp_a,
+                                 const float* comp_b, int M, int N, int K, int group, int S,
+                                 uint16_t* Y, void* stream);
+
+/*
  * MLP up-projection with GELU and the down layer's activation quantizer fused
  * into the epilogue (SteerQuant §4.4: only integer activations and row scales
  * travel between kernels; App. D: GELU stays in BF16).  The bf16 output of

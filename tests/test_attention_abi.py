@@ -1,0 +1,149 @@
+"""Host-side checks of the cache, attention and few-row calls (no GPU
+needed): sizes, and every refusal before anything is launched."""
+import pytest
+import torch
+
+P = 0x1000              # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def r():
+    from w4a4_quantized_gemm_rudder_amd import rudder
+    rudder.load_library()
+    return rudder
+
+
+def _status(r, name, args, kw):
+    args = dict(args)
+    for k in kw:
+        assert k in args, k
+    args.update(kw)
+    return getattr(r.load_library(), name)(*args.values(), None)
+
+
+MATVEC = dict(X=P, sid=P, Wq=P, gs=P, a=P, b=P, M=4, N=48, K=256, group=64, S=3, Y=P)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(X=None), 1), (dict(Wq=None), 1), (dict(gs=None), 1), (dict(Y=None), 1),
+    (dict(a=None), 1), (dict(b=None), 1), (dict(sid=None), 1), (dict(M=-1), 1), (dict(N=0), 1),
+    (dict(K=0), 1), (dict(K=96), 1), (dict(group=16), 1), (dict(group=0), 1), (dict(S=0), 1),
+    (dict(S=9), 1), (dict(X=P + 2), 1), (dict(Wq=P + 8), 1), (dict(gs=P + 2), 1),
+    (dict(K=65536 + 64), 2), (dict(N=(1 << 24) + 1), 2), (dict(M=(1 << 19) + 1), 2),
+    (dict(M=0), 0), (dict(M=0, sid=None, a=None, b=None, S=0), 0),
+])
+def test_matvec_refusals(r, kw, status):
+    assert _status(r, "rudder_matvec_w4", MATVEC, kw) == status
+    assert (r.load_library().rudder_last_error() == b"") == (status == 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(W=None), 1), (dict(Wq=None), 1), (dict(gs=None), 1), (dict(K=100), 1), (dict(N=-1), 1),
+    (dict(group=48), 1), (dict(Wq=P + 4), 1), (dict(K=65536 * 2), 2),
+])
+def test_quantize_weights_grouped_refusals(r, kw, status):
+    args = dict(W=P, K=256, N=48, group=64, Wq=P, gs=P)
+    assert _status(r, "rudder_quantize_weights_grouped", args, kw) == status
+
+
+def test_sizes(r):
+    assert r.grouped_weight_bytes(256, 48) == 256 * 48 // 2
+    assert r.grouped_weight_bytes(96, 17) == 128 * 32 // 2        # padded to 128 and 16
+    assert r.grouped_weight_bytes(0, 17) == 0
+    assert r.grouped_scale_count(96, 17, 32) == 3 * 32
+    assert r.grouped_scale_count(96, 17, 64) == 0
+    assert r.cache_page_bytes(8, 128) == 8 * 2 * 64 * 128
+    assert r.cache_page_bytes(8, 96) == 0 and r.cache_page_bytes(0, 64) == 0
+    # many rows need no pieces; one row of a long cache does, and its workspace grows with T
+    assert r.attention_workspace_bytes(2, 8384, 4192, 4192, 16, 16, 128) == 0
+    one = r.attention_workspace_bytes(1, 1, 1, 40000, 16, 16, 128)
+    assert one > 0 and one % (16 * 130 * 4) == 0
+    assert r.attention_workspace_bytes(1, 3, 1, 40000, 16, 16, 128) == 3 * one
+    for bad in ((1, 1, 1, 100, 15, 2, 64), (1, 1, 1, 100, 4, 2, 96), (-1, 1, 1, 100, 4, 2, 64),
+                (1, 1, 1, -1, 4, 2, 64)):
+        assert r.attention_workspace_bytes(*bad) == 0
+
+
+APPEND = dict(K=P, V=P, row_start=P, pos=P, table=P, B=2, T=4, max_rows=2, max_pages=3,
+              num_pages=9, Hkv=2, D=64, ldk=128, ldv=384, codes=P, scales=P)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=None), 1), (dict(V=None), 1), (dict(row_start=None), 1), (dict(pos=None), 1),
+    (dict(table=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(B=-1), 1),
+    (dict(T=-1), 1), (dict(max_rows=-1), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1),
+    (dict(Hkv=0), 1), (dict(ldk=127), 1), (dict(ldk=120), 1), (dict(ldv=132), 1),
+    (dict(K=P + 8), 1), (dict(codes=P + 1), 1), (dict(D=96), 2), (dict(B=65536), 2),
+    (dict(Hkv=5000, ldk=5000 * 64, ldv=5000 * 64), 2), (dict(B=0), 0), (dict(T=0), 0),
+    (dict(max_rows=0), 0),
+])
+def test_append_refusals(r, kw, status):
+    assert _status(r, "rudder_cache_append", APPEND, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(codes=None), 1), (dict(scales=None), 1), (dict(pages=None), 1), (dict(k=None), 1),
+    (dict(v=None), 1), (dict(n=-1), 1), (dict(num_pages=0), 1), (dict(Hkv=-2), 1),
+    (dict(k=P + 4), 1), (dict(D=32), 2), (dict(n=(1 << 23) + 1), 2), (dict(n=0), 0),
+])
+def test_dequant_refusals(r, kw, status):
+    args = dict(codes=P, scales=P, pages=P, n=3, num_pages=9, Hkv=2, D=64, k=P, v=P)
+    assert _status(r, "rudder_cache_dequant", args, kw) == status
+
+
+CACHE = dict(Q=P, row_start=P, kv_len=P, table=P, codes=P, scales=P, B=2, T=4, max_rows=2,
+             max_kv=100, max_pages=3, num_pages=9, Hq=4, Hkv=2, D=64, ldq=256, ldo=256, sm=0.1,
+             causal=1, ws=P, O=P)
+CROSS = dict(Q=P, K=P, V=P, row_start=P, kv_start=P, kv_len=P, B=2, T=4, Tkv=100, max_rows=2,
+             max_kv=50, Hq=4, Hkv=2, D=64, ldq=256, ldk=128, ldv=128, ldo=256, sm=0.1, ws=P, O=P)
+BOTH = [
+    (dict(Q=None), 1), (dict(row_start=None), 1), (dict(kv_len=None), 1), (dict(O=None), 1),
+    (dict(B=-1), 1), (dict(T=-2), 1), (dict(max_rows=-1), 1), (dict(max_kv=-1), 1),
+    (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(ldq=255), 1), (dict(ldq=248), 1),
+    (dict(ldo=260), 1), (dict(sm=float("nan")), 1), (dict(sm=float("inf")), 1),
+    (dict(Q=P + 8), 1), (dict(O=P + 2), 1), (dict(ws=P + 4), 1), (dict(D=80), 2),
+    (dict(B=70000), 2), (dict(max_rows=1 << 25), 2),
+    (dict(B=0), 0), (dict(T=0), 0), (dict(max_rows=0), 0),
+    (dict(max_kv=1 << 20, ws=None), 1),               # these need a workspace
+]
+
+
+@pytest.mark.parametrize("kw,status", BOTH + [
+    (dict(table=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(max_pages=0), 1),
+    (dict(num_pages=-1), 1), (dict(codes=P + 4), 1),
+])
+def test_cache_attention_refusals(r, kw, status):
+    assert _status(r, "rudder_cache_attention", CACHE, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", BOTH + [
+    (dict(K=None), 1), (dict(V=None), 1), (dict(kv_start=None), 1), (dict(Tkv=-1), 1),
+    (dict(ldk=100), 1), (dict(ldv=129), 1), (dict(K=P + 2), 1), (dict(V=P + 4), 1),
+])
+def test_cross_attention_refusals(r, kw, status):
+    assert _status(r, "rudder_cross_attention", CROSS, kw) == status
+
+
+def test_binding_checks_tensors(r):
+    """Types, sizes and layouts of tensors are checked against the sizes passed."""
+    T, H, D = 4, 2, 64
+    i32 = torch.zeros(8, dtype=torch.int32)
+    q = torch.zeros(T, H, D, dtype=torch.bfloat16)
+    codes = torch.zeros(3, H, 2, 64 * D, dtype=torch.int8)
+    scales = torch.zeros(3, H, 2)
+    ok = dict(Q=q, row_start=i32, kv_len=i32, page_table=i32, codes=codes, scales=scales, B=2,
+              T=T, max_rows=2, max_kv=100, max_pages=2, num_pages=3, Hq=H, Hkv=H, D=D, sm=0.1,
+              causal=True, workspace=None, O=q.clone(), stream=0)
+    for kw in (dict(Q=q.float()), dict(Q=q[:3]), dict(Q=q.transpose(0, 1)), dict(Q=q[..., ::2]),
+               dict(row_start=i32.long()), dict(row_start=i32[:2]), dict(kv_len=i32[:1]),
+               dict(page_table=i32[:3]), dict(page_table=i32[::2]), dict(codes=codes[:2]),
+               dict(scales=scales[:2]), dict(scales=scales.double()), dict(O=q[:2]),
+               dict(ldq=2 * H * D)):
+        with pytest.raises(ValueError):
+            r.rudder_cache_attention(**{**ok, **kw})
+    with pytest.raises(ValueError):
+        r.rudder_matvec_w4(q.view(T, -1), None, torch.zeros(100, dtype=torch.uint8), scales, None,
+                           None, T, 32, 128, 64, 1, q, stream=0)
+    with pytest.raises(r.RudderError) as e:
+        r.rudder_cache_attention(**{**ok, "sm": float("nan")})
+    assert e.value.status == r.RUDDER_ERR_INVALID_ARG

@@ -1,0 +1,268 @@
+"""Attention over the 8-bit cache and cross attention against the 64-bit form,
+within bounds that count the kernels' roundings."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+from gpu_harness import log
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module")
+def rudder():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    from w4a4_quantized_gemm_rudder_amd import rudder as r
+    r.load_library()
+    return r
+
+
+def _cache(g, lens, H, D, spread=0.0):
+    """Codes (garbage behind each length), scales and a table with absent pages behind."""
+    need = [(n + PAGE - 1) // PAGE for n in lens]
+    width = max(max(need), 1) + 1
+    P = sum(need) + 2
+    codes = torch.randint(-128, 128, (P, H, 2, PAGE * D), generator=g).to(torch.int8)
+    scales = (torch.rand(P, H, 2, generator=g) + 0.5) * 0.01
+    scales = scales * 2.0 ** (spread * (torch.rand(P, H, 2, generator=g) - 0.5))
+    order = torch.randperm(P, generator=g)
+    table = torch.full((len(lens), width), -5, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n].to(torch.int32)
+        at += n
+    return codes, scales, table
+
+
+def _starts(counts):
+    return torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+
+
+def _run_cache(rudder, q, starts, lens, table, codes, scales, sm, causal, max_rows=None,
+               max_kv=None):
+    counts = (starts[1:] - starts[:-1]).tolist()
+    return rudder.cache_attention(
+        q.cuda(), starts.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(),
+        codes.cuda(), scales.cuda(), max(counts) if max_rows is None else max_rows,
+        max(lens) if max_kv is None else max_kv, sm, causal)
+
+
+CACHE_CASES = [
+    # counts, lens, Hq, Hkv, D, causal
+    ([1], [1], 1, 1, 64, True),
+    ([1], [0], 2, 2, 128, True),                       # an empty cache
+    ([1, 1, 1, 1], [1, 64, 65, 777], 4, 4, 128, True),
+    ([1, 1], [2000, 63], 8, 2, 64, True),              # grouped heads
+    ([1, 1], [300, 129], 6, 2, 128, False),            # a group of three
+    ([1], [9000], 2, 1, 128, True),                    # split over the tokens
+    ([5, 0, 2], [40, 100, 2], 3, 1, 64, True),         # an empty sequence
+    ([7, 3], [4, 0], 2, 2, 64, True),                  # rows in front of the first token
+    ([33, 129], [200, 129], 4, 2, 128, True),
+    ([200], [200], 2, 2, 64, True),
+    ([96, 96], [4100, 4100], 2, 2, 128, False),
+    ([130, 40], [700, 650], 12, 4, 64, False),
+    ([64, 16], [128, 500], 16, 1, 128, True),          # one cached head
+    ([300], [2500], 1, 1, 128, True),
+    ([20], [3000], 4, 4, 64, True),
+]
+
+
+@pytest.mark.parametrize("counts,lens,Hq,Hkv,D,causal", CACHE_CASES)
+def test_cache_attention(rudder, counts, lens, Hq, Hkv, D, causal):
+    log(f"case cache {counts} {lens} Hq={Hq} Hkv={Hkv} D={D} causal={causal}")
+    g = torch.Generator().manual_seed(21)
+    codes, scales, table = _cache(g, lens, Hkv, D)
+    starts = _starts(counts)
+    T = int(starts[-1])
+    q = (torch.randn(T, Hq, D, generator=g) * 2).to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, causal)
+    got = _run_cache(rudder, q, starts, lens, table, codes, scales, sm, causal)
+    ref.assert_within("O", got, want, bound)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,lens", [([1, 1], [500, 1000]), ([70], [400])])
+def test_scales_of_all_sizes(rudder, D, counts, lens):
+    """V scales from 2^-35 to 2^25 (and K scales to match) and blocks of zeros: the pages'
+    shares of the sum stay right however far apart their scales are."""
+    log(f"case scales D={D} {counts} {lens}")
+    g = torch.Generator().manual_seed(22)
+    codes, scales, table = _cache(g, lens, 1, D)
+    P = len(codes)
+    scales[:, :, 1] = 2.0 ** torch.randint(-35, 26, (P, 1), generator=g)
+    for p in table[0, [1, 3]].tolist():                       # zero blocks
+        codes[p, :, 1] = 0
+        scales[p, :, 1] = 0
+    starts = _starts(counts)
+    q = torch.randn(int(starts[-1]), 2, D, generator=g).to(torch.bfloat16)
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, 0.05, False)
+    got = _run_cache(rudder, q, starts, lens, table, codes, scales, 0.05, False)
+    ref.assert_within("O", got, want, bound)
+
+
+def test_zero_and_far_blocks_keep_their_weight(rudder):
+    """A block of zeros beside one of large values: the zeros' tokens still count in the
+    denominator."""
+    log("case zero blocks")
+    D = 64
+    codes = torch.zeros(2, 1, 2, PAGE * D, dtype=torch.int8)
+    scales = torch.zeros(2, 1, 2)
+    codes[1, 0, 1], scales[1, 0, 1] = 100, 2.0 ** 30
+    table = torch.tensor([[0, 1]], dtype=torch.int32)
+    for order in ([0, 1], [1, 0]):
+        t = table[:, order]
+        q = torch.ones(1, 1, D, dtype=torch.bfloat16)
+        got = _run_cache(rudder, q, _starts([1]), [128], t, codes, scales, 1.0, False)
+        # every weight is 1 / 128, half of the tokens have the value 100 * 2^30
+        assert (got == 50 * 2.0 ** 30).all()
+
+
+@pytest.mark.parametrize("D,rows", [(64, 1), (128, 1), (128, 40)])
+def test_sharp_and_large_queries(rudder, D, rows):
+    """Queries of very different magnitudes: near one-hot rows, rows of zeros and rows near the
+    type's ends."""
+    log(f"case sharp D={D} rows={rows}")
+    g = torch.Generator().manual_seed(23)
+    lens = [600]
+    codes, scales, table = _cache(g, lens, 2, D)
+    for scale, sm in ((30.0, 0.3), (1e30, 1e-31), (1e-30, 1e29), (0.0, 0.1)):
+        q = (torch.randn(rows, 4, D, generator=g) * scale).to(torch.bfloat16)
+        starts = _starts([rows])
+        want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, True)
+        got = _run_cache(rudder, q, starts, lens, table, codes, scales, sm, True)
+        ref.assert_within(f"O at {scale}", got, want, bound)
+
+
+@pytest.mark.parametrize("rows", [1, 50])
+def test_absent_pages_and_bounds(rudder, rows):
+    """Pages outside the pool hold no tokens; lengths behind the table or max_kv are cut; rows
+    behind max_rows and behind the last sequence stay as they were."""
+    log(f"case absent pages rows={rows}")
+    g = torch.Generator().manual_seed(24)
+    Hq, Hkv, D = 2, 2, 64
+    lens = [400, 130]
+    codes, scales, table = _cache(g, lens, Hkv, D)
+    P = len(codes)
+    table[0, 0], table[0, 3], table[1, 1] = -1, P, 2 ** 31 - 1
+    starts = _starts([rows, rows])
+    T = 2 * rows + 3
+    q = torch.randn(T, Hq, D, generator=g).to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, True)
+    O = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    n = rudder.attention_workspace_bytes(2, T, rows, 400, Hq, Hkv, D)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+
+    def run(lens, max_rows, max_kv):
+        O.fill_(7.0)
+        rudder.rudder_cache_attention(
+            q.cuda(), starts.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(),
+            codes.cuda(), scales.cuda(), 2, T, max_rows, max_kv, table.shape[1], P, Hq, Hkv, D,
+            sm, True, ws, O)
+        return O.cpu()
+
+    got = run(lens, rows, 400)
+    ref.assert_within("O", got[:2 * rows], want[:2 * rows], bound[:2 * rows])
+    assert (got[2 * rows:] == 7.0).all()
+    # a length beyond max_kv
+    cut, cut_bound = ref.cache_attention(q, starts, [300, 130], table, codes, scales, sm, True)
+    got = run([2 ** 31 - 1, 130], rows, 300)
+    ref.assert_within("O cut", got[:2 * rows], cut[:2 * rows], cut_bound[:2 * rows])
+    # a negative length: no tokens
+    got = run([-5, 130], rows, 400)
+    assert not got[:rows].any()
+    if rows > 1:
+        got = run(lens, rows - 10, 400)
+        assert (got[rows - 10:rows] == 7.0).all()
+        ref.assert_within("O first rows", got[:rows - 10], want[:rows - 10], bound[:rows - 10])
+
+
+def test_rows_are_independent(rudder):
+    """A NaN query stays in its row and head; strided Q and O; other elements stay."""
+    log("case strided, NaN query")
+    g = torch.Generator().manual_seed(25)
+    Hq, Hkv, D, rows = 4, 2, 64, 37
+    lens = [150]
+    codes, scales, table = _cache(g, lens, Hkv, D)
+    buf = torch.randn(rows, 3 * Hq, D, generator=g).to(torch.bfloat16)
+    buf[5, Hq + 1, 3] = float("nan")
+    q = buf[:, Hq:2 * Hq]
+    starts = _starts([rows])
+    want, bound = ref.cache_attention(torch.nan_to_num(q), starts, lens, table, codes, scales,
+                                      0.1, True)
+    out = torch.full((rows, Hq + 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(16, rudder.attention_workspace_bytes(1, rows, rows, 150, Hq, Hkv, D)),
+                     dtype=torch.uint8, device="cuda")
+    rudder.rudder_cache_attention(
+        buf.cuda()[:, Hq:2 * Hq], starts.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+        table.cuda(), codes.cuda(), scales.cuda(), 1, rows, rows, 150, table.shape[1], len(codes),
+        Hq, Hkv, D, 0.1, True, ws, out[:, 1:1 + Hq])
+    out = out.cpu()
+    assert (out[:, 0] == 7.0).all() and (out[:, -1] == 7.0).all()
+    got = out[:, 1:1 + Hq].clone()
+    assert torch.isnan(got[5, 1]).all()
+    got[5, 1] = 0.0
+    want[5, 1], bound[5, 1] = 0.0, 0.0
+    ref.assert_within("O", got, want, bound)
+
+
+CROSS_CASES = [
+    # counts, lens, Hq, Hkv, D
+    ([1], [1], 1, 1, 64),
+    ([1, 1, 1], [77, 0, 300], 4, 4, 128),
+    ([5, 40], [64, 65], 6, 2, 64),
+    ([200, 1], [512, 3], 2, 2, 128),
+    ([96], [77], 4, 1, 128),
+    ([3], [2000], 2, 2, 64),
+    ([129, 130], [1, 63], 1, 1, 128),
+]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("counts,lens,Hq,Hkv,D", CROSS_CASES)
+def test_cross_attention(rudder, counts, lens, Hq, Hkv, D, packed):
+    """Padded and packed states; what lies in the padding (NaN, infinities) does not matter."""
+    log(f"case cross {counts} {lens} Hq={Hq} Hkv={Hkv} D={D} packed={packed}")
+    g = torch.Generator().manual_seed(26)
+    starts = _starts(counts)
+    T, B, L = int(starts[-1]), len(lens), max(lens) + 3
+    q = (torch.randn(T, Hq, D, generator=g) * 2).to(torch.bfloat16)
+    if packed:
+        kv_start = _starts(lens)[:-1]
+        rows = max(sum(lens), 1)
+    else:
+        kv_start = (torch.arange(B) * L).to(torch.int32)
+        rows = B * L
+    kv = torch.full((rows, 2 * Hkv, D), float("nan"), dtype=torch.bfloat16)
+    kv[::2] = float("inf")
+    for b, n in enumerate(lens):
+        at = int(kv_start[b])
+        kv[at:at + n] = torch.randn(n, 2 * Hkv, D, generator=g).to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    want, bound = ref.cross_attention(q, kv[:, :Hkv], kv[:, Hkv:], starts, kv_start, lens, sm)
+    dev = kv.cuda()
+    got = rudder.cross_attention(q.cuda(), dev[:, :Hkv], dev[:, Hkv:], starts.cuda(),
+                                 kv_start.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                 max(counts), max(lens), sm)
+    ref.assert_within("O", got, want, bound)
+
+
+def test_cross_bounds(rudder):
+    """Key rows that the arrays place outside the buffer do not exist."""
+    log("case cross bounds")
+    g = torch.Generator().manual_seed(27)
+    D, H, Tkv = 64, 2, 100
+    q = torch.randn(4, H, D, generator=g).to(torch.bfloat16)
+    kv = torch.randn(Tkv, 2 * H, D, generator=g).to(torch.bfloat16)
+    starts = _starts([2, 2])
+    dev = kv.cuda()
+    got = rudder.cross_attention(q.cuda(), dev[:, :H], dev[:, H:], starts.cuda(),
+                                 torch.tensor([90, 2 ** 31 - 1], dtype=torch.int32).cuda(),
+                                 torch.tensor([50, 50], dtype=torch.int32).cuda(), 2, 50, 0.1)
+    want, bound = ref.cross_attention(q, kv[:, :H], kv[:, H:], starts, torch.tensor([90, 0]),
+                                      [10, 0], 0.1)
+    ref.assert_within("O", got, want, bound)

@@ -298,6 +298,249 @@ rudder_status_t rudder_stream_sq_error(const uint16_t* Y, const float* Yref,
                     f);
 }
 
+// ---------------------------------------------------------------------------
+// Few-row products with group-scaled 4-bit weights.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxGroupedN = 1 << 24;
+
+rudder_status_t check_grouped(const char* f, int K, int N, int group) {
+    if (K <= 0 || N <= 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: K=%d and N=%d must be positive", f, K, N);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: group=%d must be 32, 64 or 128", f, group);
+    if (K % group)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: K=%d must be a multiple of group=%d", f, K,
+                    group);
+    if (K > RUDDER_MAX_K)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: K=%d exceeds %d", f, K, RUDDER_MAX_K);
+    if (N > kMaxGroupedN)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: N=%d exceeds %d", f, N, kMaxGroupedN);
+    return RUDDER_OK;
+}
+
+}  // namespace
+
+size_t rudder_grouped_weight_bytes(int K, int N) {
+    if (K <= 0 || N <= 0 || K > RUDDER_MAX_K || N > kMaxGroupedN) return 0;
+    return ((size_t)K + 127) / 128 * 128 * (((size_t)N + 15) / 16 * 16) / 2;
+}
+
+size_t rudder_grouped_scale_count(int K, int N, int group) {
+    if (K <= 0 || N <= 0 || K > RUDDER_MAX_K || N > kMaxGroupedN ||
+        (group != 32 && group != 64 && group != 128) || K % group)
+        return 0;
+    return (size_t)(K / group) * (((size_t)N + 15) / 16 * 16);
+}
+
+rudder_status_t rudder_quantize_weights_grouped(const uint16_t* W, int K, int N, int group,
+                                                uint8_t* Wq, uint16_t* g_scale, void* stream) {
+    const char* f = "rudder_quantize_weights_grouped";
+    if (!W || !Wq || !g_scale) return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    const rudder_status_t st = check_grouped(f, K, N, group);
+    if (st != RUDDER_OK) return st;
+    if (misaligned(Wq) || misaligned(g_scale))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Wq and g_scale must be 16-byte aligned", f);
+    return from_hip(rudder::launch_quantize_weights_grouped(W, K, N, group, Wq, g_scale,
+                                                            static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_matvec_w4(const uint16_t* X, const uint8_t* stream_id, const uint8_t* Wq,
+                                 const uint16_t* g_scale, const float* comp_a,
+                                 const float* comp_b, int M, int N, int K, int group, int S,
+                                 uint16_t* Y, void* stream) {
+    const char* f = "rudder_matvec_w4";
+    if (!X || !Wq || !g_scale || !Y)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if ((comp_a == nullptr) != (comp_b == nullptr) || (comp_a && !stream_id))
+        return fail(RUDDER_ERR_INVALID_ARG,
+                    "%s: compensation takes comp_a, comp_b and stream_id together", f);
+    if (M < 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: M=%d must be >= 0", f, M);
+    const rudder_status_t st = check_grouped(f, K, N, group);
+    if (st != RUDDER_OK) return st;
+    if (comp_a && (S < 1 || S > RUDDER_MAX_STREAMS))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: S=%d must be in 1..%d", f, S, RUDDER_MAX_STREAMS);
+    if (misaligned(X) || misaligned(Wq) || misaligned(g_scale))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: X, Wq and g_scale must be 16-byte aligned", f);
+    if (M > (1 << 19)) return fail(RUDDER_ERR_UNSUPPORTED, "%s: M=%d exceeds %d", f, M, 1 << 19);
+    if (M == 0) return ok();
+    return from_hip(rudder::launch_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K,
+                                             group, Y, static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+// ---------------------------------------------------------------------------
+// Cache and attention (include/rudder_attention.h).
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxSequences = 65535;
+constexpr int kMaxCacheHeads = 4096;
+
+rudder_status_t check_heads(const char* f, int Hkv, int D) {
+    if (Hkv <= 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Hkv=%d must be positive", f, Hkv);
+    if (D != 64 && D != 128)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: D=%d is neither 64 nor 128", f, D);
+    if (Hkv > kMaxCacheHeads)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: Hkv=%d exceeds %d", f, Hkv, kMaxCacheHeads);
+    return RUDDER_OK;
+}
+
+rudder_status_t check_ld(const char* f, const char* name, int ld, int heads, int D) {
+    if (ld % 8 || (int64_t)ld < (int64_t)heads * D)
+        return fail(RUDDER_ERR_INVALID_ARG,
+                    "%s: %s=%d must be a multiple of 8 and at least %d * %d", f, name, ld, heads,
+                    D);
+    return RUDDER_OK;
+}
+
+rudder_status_t check_attention(const char* f, const void* Q, const void* O,
+                                const void* workspace, int B, int T, int max_rows, int max_kv,
+                                int Hq, int Hkv, int D, int ldq, int ldo, float sm) {
+    if (B < 0 || T < 0 || max_rows < 0 || max_kv < 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: B=%d, T=%d, max_rows=%d and max_kv=%d must be "
+                    ">= 0", f, B, T, max_rows, max_kv);
+    rudder_status_t st = check_heads(f, Hkv, D);
+    if (st != RUDDER_OK) return st;
+    if (Hq <= 0 || Hq % Hkv)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Hq=%d must be a positive multiple of Hkv=%d", f,
+                    Hq, Hkv);
+    if ((st = check_ld(f, "ldq", ldq, Hq, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldo", ldo, Hq, D)) != RUDDER_OK) return st;
+    if (!(sm - sm == 0.0f)) return fail(RUDDER_ERR_INVALID_ARG, "%s: sm must be finite", f);
+    if (misaligned(Q) || misaligned(O) || misaligned(workspace))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Q, O and workspace must be 16-byte aligned", f);
+    if (B > kMaxSequences)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d exceeds %d", f, B, kMaxSequences);
+    if ((int64_t)max_rows * Hq > (1 << 26))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d with Hq=%d exceeds 2^26 rows", f,
+                    max_rows, Hq);
+    if (!workspace &&
+        rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D) > 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: these sizes need a workspace of %zu bytes", f,
+                    rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D));
+    return RUDDER_OK;
+}
+
+}  // namespace
+
+size_t rudder_cache_page_bytes(int Hkv, int D) {
+    if (Hkv <= 0 || Hkv > kMaxCacheHeads || (D != 64 && D != 128)) return 0;
+    return (size_t)Hkv * 2 * RUDDER_CACHE_PAGE * (size_t)D;
+}
+
+rudder_status_t rudder_cache_append(const uint16_t* K, const uint16_t* V,
+                                    const int32_t* row_start, const int32_t* pos,
+                                    const int32_t* page_table, int B, int T, int max_rows,
+                                    int max_pages, int num_pages, int Hkv, int D, int ldk,
+                                    int ldv, int8_t* codes, float* scales, void* stream) {
+    const char* f = "rudder_cache_append";
+    if (!K || !V || !row_start || !pos || !page_table || !codes || !scales)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (B < 0 || T < 0 || max_rows < 0 || max_pages <= 0 || num_pages <= 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: B=%d, T=%d, max_rows=%d must be >= 0, "
+                    "max_pages=%d and num_pages=%d > 0", f, B, T, max_rows, max_pages, num_pages);
+    rudder_status_t st = check_heads(f, Hkv, D);
+    if (st != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldv", ldv, Hkv, D)) != RUDDER_OK) return st;
+    if (misaligned(K) || misaligned(V) || misaligned(codes) || misaligned(scales))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: K, V, codes and scales must be 16-byte aligned",
+                    f);
+    if (B > kMaxSequences)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d exceeds %d", f, B, kMaxSequences);
+    if (B == 0 || T == 0 || max_rows == 0) return ok();
+    return from_hip(rudder::launch_cache_append(K, V, row_start, pos, page_table, B, T,
+                                                max_rows < T ? max_rows : T, max_pages, num_pages,
+                                                Hkv, D, ldk, ldv, codes, scales,
+                                                static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_cache_dequant(const int8_t* codes, const float* scales,
+                                     const int32_t* pages, int n, int num_pages, int Hkv, int D,
+                                     float* K_out, float* V_out, void* stream) {
+    const char* f = "rudder_cache_dequant";
+    if (!codes || !scales || !pages || !K_out || !V_out)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (n < 0 || num_pages <= 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: n=%d must be >= 0 and num_pages=%d > 0", f, n,
+                    num_pages);
+    const rudder_status_t st = check_heads(f, Hkv, D);
+    if (st != RUDDER_OK) return st;
+    if (misaligned(codes) || misaligned(K_out) || misaligned(V_out))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: codes, K_out and V_out must be 16-byte aligned",
+                    f);
+    if (n > (1 << 23))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: n=%d exceeds %d", f, n, 1 << 23);
+    if (n == 0) return ok();
+    return from_hip(rudder::launch_cache_dequant(codes, scales, pages, n, num_pages, Hkv, D,
+                                                 K_out, V_out, static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
+                                        int D) {
+    if (B <= 0 || T <= 0 || max_rows <= 0 || max_kv < 0 || Hkv <= 0 || Hkv > kMaxCacheHeads ||
+        Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || B > kMaxSequences ||
+        (int64_t)max_rows * Hq > (1 << 26))
+        return 0;
+    return rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D);
+}
+
+rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_start,
+                                       const int32_t* kv_len, const int32_t* page_table,
+                                       const int8_t* codes, const float* scales, int B, int T,
+                                       int max_rows, int max_kv, int max_pages, int num_pages,
+                                       int Hq, int Hkv, int D, int ldq, int ldo, float sm,
+                                       int causal, void* workspace, uint16_t* O, void* stream) {
+    const char* f = "rudder_cache_attention";
+    if (!Q || !row_start || !kv_len || !page_table || !codes || !scales || !O)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (max_pages <= 0 || num_pages <= 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: max_pages=%d and num_pages=%d must be positive",
+                    f, max_pages, num_pages);
+    const rudder_status_t st = check_attention(f, Q, O, workspace, B, T, max_rows, max_kv, Hq,
+                                               Hkv, D, ldq, ldo, sm);
+    if (st != RUDDER_OK) return st;
+    if (misaligned(codes))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned", f);
+    if (B == 0 || T == 0 || max_rows == 0) return ok();
+    return from_hip(rudder::launch_cache_attention(Q, row_start, kv_len, page_table, codes,
+                                                   scales, B, T, max_rows, max_kv, max_pages,
+                                                   num_pages, Hq, Hkv, D, ldq, ldo, sm, causal,
+                                                   workspace, O,
+                                                   static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, const uint16_t* V,
+                                       const int32_t* row_start, const int32_t* kv_start,
+                                       const int32_t* kv_len, int B, int T, int Tkv, int max_rows,
+                                       int max_kv, int Hq, int Hkv, int D, int ldq, int ldk,
+                                       int ldv, int ldo, float sm, void* workspace, uint16_t* O,
+                                       void* stream) {
+    const char* f = "rudder_cross_attention";
+    if (!Q || !K || !V || !row_start || !kv_start || !kv_len || !O)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (Tkv < 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Tkv=%d must be >= 0", f, Tkv);
+    rudder_status_t st = check_attention(f, Q, O, workspace, B, T, max_rows, max_kv, Hq, Hkv, D,
+                                         ldq, ldo, sm);
+    if (st != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldv", ldv, Hkv, D)) != RUDDER_OK) return st;
+    if (misaligned(K) || misaligned(V))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", f);
+    if (B == 0 || T == 0 || max_rows == 0) return ok();
+    return from_hip(rudder::launch_cross_attention(Q, K, V, row_start, kv_start, kv_len, B, T,
+                                                   Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk,
+                                                   ldv, ldo, sm, workspace, O,
+                                                   static_cast<hipStream_t>(stream)),
+                    f);
+}
+
 size_t rudder_mfma_ceiling_sink_bytes(void) { return rudder::mfma_ceiling_sink_bytes(); }
 
 double rudder_mfma_ceiling_ops(int iters, int codes) {

@@ -1,7 +1,7 @@
 """Python binding of librudder (ctypes).
 
 Argument marshalling only: every step of the layer runs in the HIP kernels
-behind the C ABI declared in include/rudder.h.  torch supplies device memory
+behind the C ABI declared in include/.  torch supplies device memory
 and the current HIP stream.  If the library is missing this module raises;
 there is no CPU fallback.
 
@@ -12,6 +12,12 @@ The calls keep their C names and meanings:
   rudder_linear_gelu_quant -- MLP up-projection with GELU (kept in BF16, App. D)
                               and the down layer's quantizer in its epilogue
   rudder_gelu_bf16         -- that GELU alone, elementwise
+  rudder_quantize_weights_grouped, rudder_matvec_w4
+                           -- few-row products with group-scaled 4-bit weights
+  rudder_cache_append, rudder_cache_dequant
+                           -- the paged 8-bit cache of keys and values
+  rudder_cache_attention, rudder_cross_attention
+                           -- attention over that cache, and to bf16 states
 (SteerQuant = "SteerQuant: Steering Quantization Error with Action-Guided
 Scaling in World-Action Models", paperlayer.ai digest.)
 """
@@ -32,6 +38,7 @@ RUDDER_ERR_INVALID_ARG = 1
 RUDDER_ERR_UNSUPPORTED = 2
 RUDDER_ERR_HIP = 3
 MAX_STREAMS = 8
+CACHE_PAGE = 64     # tokens of a cache page
 
 EXPORTED = (
     "rudder_packed_weight_bytes", "rudder_packed_act_bytes", "rudder_quant_act_workspace_bytes",
@@ -41,6 +48,10 @@ EXPORTED = (
     "rudder_status_string", "rudder_last_error",
     "rudder_mfma_ceiling_sink_bytes", "rudder_mfma_ceiling_ops", "rudder_mfma_ceiling",
     "rudder_mfma_ceiling_shape",
+    "rudder_grouped_weight_bytes", "rudder_grouped_scale_count",
+    "rudder_quantize_weights_grouped", "rudder_matvec_w4",
+    "rudder_cache_page_bytes", "rudder_cache_append", "rudder_cache_dequant",
+    "rudder_attention_workspace_bytes", "rudder_cache_attention", "rudder_cross_attention",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -96,6 +107,27 @@ def load_library() -> ctypes.CDLL:
     lib.rudder_mfma_ceiling.restype = i
     lib.rudder_mfma_ceiling_shape.argtypes = [vp, vp, i, i, i, i, i, i, i, vp, vp]
     lib.rudder_mfma_ceiling_shape.restype = i
+    f = ctypes.c_float
+    lib.rudder_grouped_weight_bytes.argtypes = [i, i]
+    lib.rudder_grouped_weight_bytes.restype = sz
+    lib.rudder_grouped_scale_count.argtypes = [i, i, i]
+    lib.rudder_grouped_scale_count.restype = sz
+    lib.rudder_quantize_weights_grouped.argtypes = [vp, i, i, i, vp, vp, vp]
+    lib.rudder_quantize_weights_grouped.restype = i
+    lib.rudder_matvec_w4.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
+    lib.rudder_matvec_w4.restype = i
+    lib.rudder_cache_page_bytes.argtypes = [i, i]
+    lib.rudder_cache_page_bytes.restype = sz
+    lib.rudder_cache_append.argtypes = [vp, vp, vp, vp, vp] + [i] * 9 + [vp, vp, vp]
+    lib.rudder_cache_append.restype = i
+    lib.rudder_cache_dequant.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp]
+    lib.rudder_cache_dequant.restype = i
+    lib.rudder_attention_workspace_bytes.argtypes = [i] * 7
+    lib.rudder_attention_workspace_bytes.restype = sz
+    lib.rudder_cache_attention.argtypes = [vp] * 6 + [i] * 11 + [f, i, vp, vp, vp]
+    lib.rudder_cache_attention.restype = i
+    lib.rudder_cross_attention.argtypes = [vp] * 6 + [i] * 12 + [f, vp, vp, vp]
+    lib.rudder_cross_attention.restype = i
     lib.rudder_status_string.argtypes = [i]
     lib.rudder_status_string.restype = ctypes.c_char_p
     lib.rudder_last_error.argtypes = []
@@ -213,6 +245,151 @@ def rudder_stream_sq_error(Y, Yref, stream_id, M: int, N: int, S: int, workspace
 
 
 # ---------------------------------------------------------------------------
+# Few-row products, cache and attention (include/rudder_attention.h).  Tensors
+# are checked for their type and size against the sizes passed; device
+# addresses (ints) pass through unchecked.
+# ---------------------------------------------------------------------------
+
+def _arr(name, t, dtypes, least: int) -> Optional[int]:
+    """Device address of a contiguous tensor of one of the named types with at
+    least that many elements (None -> NULL)."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.numel() < least:
+        raise ValueError(f"{name}: {t.numel()} elements, expected at least {least}")
+    return t.data_ptr()
+
+
+_BF16 = ("torch.bfloat16", "torch.int16", "torch.uint16")
+_F32 = ("torch.float32",)
+_I32 = ("torch.int32",)
+_I8 = ("torch.int8",)
+_U8 = ("torch.uint8",)
+
+
+def _rows(name, t, T: int, H: int, D: int, ld: Optional[int]):
+    """(address, row distance) of T rows of H heads of D values: [T, H, D] or
+    [T, H * D], a row's values packed, rows any distance apart."""
+    if t is None or isinstance(t, int):
+        return t, H * D if ld is None else ld
+    if str(t.dtype) not in _BF16:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(_BF16)}")
+    shape, st = tuple(t.shape), t.stride()
+    if len(shape) == 3 and shape[1:] == (H, D):
+        packed = (D == 1 or st[2] == 1) and (H == 1 or st[1] == D)
+    else:
+        packed = len(shape) == 2 and shape[1] == H * D and st[1] == 1
+    if not packed or shape[0] < T:
+        raise ValueError(f"{name}: shape {shape} with strides {st}, expected at least {T} rows "
+                         f"of {H} x {D} packed values")
+    if ld is not None and ld != st[0]:
+        raise ValueError(f"{name}: row distance {ld}, but the tensor's is {st[0]}")
+    return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], H * D)
+
+
+def grouped_weight_bytes(K: int, N: int) -> int:
+    return int(load_library().rudder_grouped_weight_bytes(K, N))
+
+
+def grouped_scale_count(K: int, N: int, group: int) -> int:
+    return int(load_library().rudder_grouped_scale_count(K, N, group))
+
+
+def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
+                                    stream=None) -> None:
+    _check(load_library().rudder_quantize_weights_grouped(
+        _arr("W", W, _BF16, K * N), K, N, group,
+        _arr("Wq", Wq, _U8, grouped_weight_bytes(K, N)),
+        _arr("g_scale", g_scale, _BF16, grouped_scale_count(K, N, group)), _stream(stream)))
+
+
+def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, K: int,
+                     group: int, S: int, Y, stream=None) -> None:
+    _check(load_library().rudder_matvec_w4(
+        _arr("X", X, _BF16, M * K), _arr("stream_id", stream_id, _U8, M),
+        _arr("Wq", Wq, _U8, K * N // 2), _arr("g_scale", g_scale, _BF16, K * N // max(group, 1)),
+        _arr("comp_a", comp_a, _F32, S * N), _arr("comp_b", comp_b, _F32, S * N), M, N, K, group,
+        S, _arr("Y", Y, _BF16, M * N), _stream(stream)))
+
+
+def cache_page_bytes(Hkv: int, D: int) -> int:
+    return int(load_library().rudder_cache_page_bytes(Hkv, D))
+
+
+def _cache(codes, scales, num_pages: int, Hkv: int, D: int):
+    blocks = num_pages * Hkv * 2
+    return (_arr("codes", codes, _I8, blocks * CACHE_PAGE * D),
+            _arr("scales", scales, _F32, blocks))
+
+
+def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_rows: int,
+                        max_pages: int, num_pages: int, Hkv: int, D: int, codes, scales,
+                        stream=None, ldk=None, ldv=None) -> None:
+    k, ldk = _rows("K", K, T, Hkv, D, ldk)
+    v, ldv = _rows("V", V, T, Hkv, D, ldv)
+    c, s = _cache(codes, scales, num_pages, Hkv, D)
+    _check(load_library().rudder_cache_append(
+        k, v, _arr("row_start", row_start, _I32, B + 1), _arr("pos", pos, _I32, B),
+        _arr("page_table", page_table, _I32, B * max_pages), B, T, max_rows, max_pages, num_pages,
+        Hkv, D, ldk, ldv, c, s, _stream(stream)))
+
+
+def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int, D: int, K_out,
+                         V_out, stream=None) -> None:
+    c, s = _cache(codes, scales, num_pages, Hkv, D)
+    size = n * Hkv * CACHE_PAGE * D
+    _check(load_library().rudder_cache_dequant(
+        c, s, _arr("pages", pages, _I32, n), n, num_pages, Hkv, D,
+        _arr("K_out", K_out, _F32, size), _arr("V_out", V_out, _F32, size), _stream(stream)))
+
+
+def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
+                              D: int) -> int:
+    return int(load_library().rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv,
+                                                               D))
+
+
+def _workspace(t, B, T, max_rows, max_kv, Hq, Hkv, D) -> Optional[int]:
+    if t is None or isinstance(t, int):
+        return t
+    return _arr("workspace", t, _U8,
+                load_library().rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv,
+                                                                D))
+
+
+def rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B: int, T: int,
+                           max_rows: int, max_kv: int, max_pages: int, num_pages: int, Hq: int,
+                           Hkv: int, D: int, sm: float, causal: bool, workspace, O, stream=None,
+                           ldq=None, ldo=None) -> None:
+    q, ldq = _rows("Q", Q, T, Hq, D, ldq)
+    o, ldo = _rows("O", O, T, Hq, D, ldo)
+    c, s = _cache(codes, scales, num_pages, Hkv, D)
+    _check(load_library().rudder_cache_attention(
+        q, _arr("row_start", row_start, _I32, B + 1), _arr("kv_len", kv_len, _I32, B),
+        _arr("page_table", page_table, _I32, B * max_pages), c, s, B, T, max_rows, max_kv,
+        max_pages, num_pages, Hq, Hkv, D, ldq, ldo, sm, int(causal),
+        _workspace(workspace, B, T, max_rows, max_kv, Hq, Hkv, D), o, _stream(stream)))
+
+
+def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int, Tkv: int,
+                           max_rows: int, max_kv: int, Hq: int, Hkv: int, D: int, sm: float,
+                           workspace, O, stream=None, ldq=None, ldk=None, ldv=None,
+                           ldo=None) -> None:
+    q, ldq = _rows("Q", Q, T, Hq, D, ldq)
+    k, ldk = _rows("K", K, Tkv, Hkv, D, ldk)
+    v, ldv = _rows("V", V, Tkv, Hkv, D, ldv)
+    o, ldo = _rows("O", O, T, Hq, D, ldo)
+    _check(load_library().rudder_cross_attention(
+        q, k, v, _arr("row_start", row_start, _I32, B + 1), _arr("kv_start", kv_start, _I32, B),
+        _arr("kv_len", kv_len, _I32, B), B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk, ldv,
+        ldo, sm, _workspace(workspace, B, T, max_rows, max_kv, Hq, Hkv, D), o, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
 # Allocating conveniences (torch allocates; the library computes)
 # ---------------------------------------------------------------------------
 
@@ -281,6 +458,117 @@ def gelu_bf16(x, stream=None):
     out = torch.empty_like(x)
     rudder_gelu_bf16(x, out, x.numel(), stream)
     return out
+
+
+def _on(stream, device):
+    """Context in which `stream` (None: the current one) and its device are
+    current, so that what is allocated and cleared inside belongs to it."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def quantize_weights_grouped(W, group: int, stream=None):
+    """W: bf16 [K, N] device tensor.  Returns (Wq uint8, g_scale bf16) for matvec_w4."""
+    import torch
+    K, N = W.shape
+    with _on(stream, W.device):
+        Wq = torch.empty(grouped_weight_bytes(K, N), dtype=torch.uint8, device=W.device)
+        g_scale = torch.empty(grouped_scale_count(K, N, group), dtype=torch.bfloat16,
+                              device=W.device)
+        rudder_quantize_weights_grouped(W, K, N, group, Wq, g_scale)
+    return Wq, g_scale
+
+
+def matvec_w4(X, Wq, g_scale, N: int, group: int, stream_id=None, comp_a=None, comp_b=None,
+              stream=None):
+    """X: bf16 [M, K], weights from quantize_weights_grouped, optionally the
+    per-stream compensation (stream_id uint8 [M], comp_a and comp_b fp32
+    [S, N]).  Returns Y bf16 [M, N]."""
+    import torch
+    M, K = X.shape
+    S = 1 if comp_a is None else comp_a.shape[0]
+    with _on(stream, X.device):
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        if M:
+            rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y)
+    return Y
+
+
+def new_cache(num_pages: int, Hkv: int, D: int, device="cuda"):
+    """An empty cache: (codes int8 [num_pages, Hkv, 2, 64 * D], scales fp32
+    [num_pages, Hkv, 2])."""
+    import torch
+    return (torch.zeros(num_pages, Hkv, 2, CACHE_PAGE * D, dtype=torch.int8, device=device),
+            torch.zeros(num_pages, Hkv, 2, dtype=torch.float32, device=device))
+
+
+def cache_append(K, V, row_start, pos, page_table, max_rows: int, codes, scales,
+                 stream=None) -> None:
+    """Quantizes K, V [T, Hkv, D] into the cache at pos [B] (see
+    include/rudder_attention.h)."""
+    B, max_pages = page_table.shape
+    T, Hkv, D = K.shape
+    if T == 0 or B == 0:
+        return
+    with _on(stream, codes.device):
+        rudder_cache_append(K, V, row_start, pos, page_table, B, T, max_rows, max_pages,
+                            codes.shape[0], Hkv, D, codes, scales)
+
+
+def cache_dequant(codes, scales, pages, stream=None):
+    """The values of whole pages (int32 [n]): K and V, fp32 [n, Hkv, 64, D]."""
+    import torch
+    num_pages, Hkv = codes.shape[:2]
+    n, D = pages.numel(), codes.shape[3] // CACHE_PAGE
+    with _on(stream, codes.device):
+        K_out = torch.empty(n, Hkv, CACHE_PAGE, D, dtype=torch.float32, device=codes.device)
+        V_out = torch.empty_like(K_out)
+        if n:
+            rudder_cache_dequant(codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out)
+    return K_out, V_out
+
+
+def _attention_buffers(Q, B, max_rows, max_kv, Hkv):
+    import torch
+    T, Hq, D = Q.shape
+    n = attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=Q.device) if n else None
+    return ws, torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=Q.device)
+
+
+def cache_attention(Q, row_start, kv_len, page_table, codes, scales, max_rows: int, max_kv: int,
+                    sm: float, causal: bool = True, stream=None):
+    """Attention of Q bf16 [T, Hq, D] to the cache.  Returns O bf16 [T, Hq, D]
+    (zeros in rows of no sequence)."""
+    B, max_pages = page_table.shape
+    T, Hq, D = Q.shape
+    num_pages, Hkv = codes.shape[:2]
+    with _on(stream, Q.device):
+        ws, O = _attention_buffers(Q, B, max_rows, max_kv, Hkv)
+        if T and B:
+            rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B, T,
+                                   max_rows, max_kv, max_pages, num_pages, Hq, Hkv, D, sm,
+                                   causal, ws, O)
+    return O
+
+
+def cross_attention(Q, K, V, row_start, kv_start, kv_len, max_rows: int, max_kv: int, sm: float,
+                    stream=None):
+    """Cross attention of Q bf16 [T, Hq, D] to K, V bf16 [Tkv, Hkv, D].
+    Returns O bf16 [T, Hq, D] (zeros in rows of no sequence)."""
+    B = kv_len.numel()
+    T, Hq, D = Q.shape
+    Tkv, Hkv = K.shape[:2]
+    with _on(stream, Q.device):
+        ws, O = _attention_buffers(Q, B, max_rows, max_kv, Hkv)
+        if T and B and Tkv:
+            rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows,
+                                   max_kv, Hq, Hkv, D, sm, ws, O)
+    return O
 
 
 # ---------------------------------------------------------------------------
