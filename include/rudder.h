@@ -278,7 +278,9 @@ rudder_status_t rudder_linear(const void* Xq, const float* row_scale, const uint
  *            lane l = n % 16 + 16 * ((k % 32) / 8) has 16 bytes at 16 * l, whose
  *            little-endian word (k % 128) / 32 holds code k as the nibble q + 8
  *            at nibble (k % 8) / 2 + 4 * (k % 2)
- *   g_scale  out: bf16 bits [K / group][ceil(N / 16) * 16], padding 0
+ *   g_scale  out: rudder_grouped_scale_count(K, N, group) bf16 bits, for each
+ *            such tile 16 * (128 / group) of them as
+ *            [(n % 16) / 4][group of the tile][n % 4], padding 0
  * Errors: INVALID_ARG for a null pointer, K or N <= 0, a group other than 32,
  * 64 or 128, K % group != 0, Wq or g_scale not 16-byte aligned; UNSUPPORTED for
  * K > RUDDER_MAX_K or N > 2^24.

@@ -108,7 +108,8 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)
  *   sm       the softmax scale, e.g. 1 / sqrt(D)
- *   workspace  rudder_attention_workspace_bytes(...) bytes (NULL if 0)
+ *   workspace, workspace_bytes  at least rudder_attention_workspace_bytes(...)
+ *            bytes (NULL if 0)
  *   B, T, max_rows, max_kv >= 0 (B, T or max_rows 0 is a no-op), Hq a multiple
  *   of Hkv, D 64 or 128
  * At most two launches: where the rows give too few workgroups, the tokens
@@ -116,7 +117,8 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * anything but the arguments.
  * Errors: INVALID_ARG for a null required pointer, negative sizes, Hq or Hkv
  * <= 0, Hq % Hkv != 0, max_pages or num_pages <= 0, ldq or ldo below Hq * D or
- * not a multiple of 8, sm not finite, Q, codes, O or workspace not 16-byte aligned;
+ * not a multiple of 8, sm not finite, a workspace that is too small, Q, codes, O
+ * or workspace not 16-byte aligned;
  * UNSUPPORTED for D other than 64 or 128, B > 65535, Hkv > 4096, or more than
  * 2^26 (row, head) pairs in max_rows * Hq.
  */
@@ -125,7 +127,8 @@ rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_sta
                                        const int8_t* codes, const float* scales, int B, int T,
                                        int max_rows, int max_kv, int max_pages, int num_pages,
                                        int Hq, int Hkv, int D, int ldq, int ldo, float sm,
-                                       int causal, void* workspace, uint16_t* O, void* stream);
+                                       int causal, void* workspace, size_t workspace_bytes,
+                                       uint16_t* O, void* stream);
 
 /*
  * Cross attention to states of another length: as above without a cache, all
@@ -142,8 +145,8 @@ rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, con
                                        const int32_t* row_start, const int32_t* kv_start,
                                        const int32_t* kv_len, int B, int T, int Tkv, int max_rows,
                                        int max_kv, int Hq, int Hkv, int D, int ldq, int ldk,
-                                       int ldv, int ldo, float sm, void* workspace, uint16_t* O,
-                                       void* stream);
+                                       int ldv, int ldo, float sm, void* workspace,
+                                       size_t workspace_bytes, uint16_t* O, void* stream);
 
 #ifdef __cplusplus
 }

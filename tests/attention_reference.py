@@ -31,7 +31,7 @@ def group_codes(W, group):
 
 
 def pack_grouped(q, s):
-    """Codes and scales in the library's layout (uint8 tensor, bf16 [K / group, Npad])."""
+    """Codes and scales in the library's layout (uint8 tensor, bf16 in tile order)."""
     K, N = q.shape
     Kp, Np = (K + 127) // 128 * 128, (N + 15) // 16 * 16
     full = torch.zeros(Kp, Np, dtype=torch.int64)
@@ -46,9 +46,12 @@ def pack_grouped(q, s):
             lane = n % 16 + 16 * ((k % 32) // 8)
             at = tile * 1024 + 16 * lane + 4 * word + shift // 2
             out[at] |= int(nib[k, n]) << (4 * (shift % 2))
-    sp = torch.zeros(s.shape[0], Np, dtype=torch.bfloat16)
-    sp[:, :N] = s
-    return torch.from_numpy(out), sp
+    group = K // s.shape[0]
+    sp = torch.zeros(Kp // group, Np, dtype=torch.bfloat16)
+    sp[:s.shape[0], :N] = s
+    # [k tile, group of the tile, n tile, n / 4, n % 4] -> [n tile, k tile, n / 4, group, n % 4]
+    sp = sp.view(Kp // 128, 128 // group, Np // 16, 4, 4).permute(2, 0, 3, 1, 4)
+    return torch.from_numpy(out), sp.reshape(-1)
 
 
 def matvec(x, q, s, group, sid=None, a=None, b=None):

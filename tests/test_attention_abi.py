@@ -50,7 +50,7 @@ def test_sizes(r):
     assert r.grouped_weight_bytes(256, 48) == 256 * 48 // 2
     assert r.grouped_weight_bytes(96, 17) == 128 * 32 // 2        # padded to 128 and 16
     assert r.grouped_weight_bytes(0, 17) == 0
-    assert r.grouped_scale_count(96, 17, 32) == 3 * 32
+    assert r.grouped_scale_count(96, 17, 32) == 4 * 32            # padded likewise
     assert r.grouped_scale_count(96, 17, 64) == 0
     assert r.cache_page_bytes(8, 128) == 8 * 2 * 64 * 128
     assert r.cache_page_bytes(8, 96) == 0 and r.cache_page_bytes(0, 64) == 0
@@ -93,9 +93,10 @@ def test_dequant_refusals(r, kw, status):
 
 CACHE = dict(Q=P, row_start=P, kv_len=P, table=P, codes=P, scales=P, B=2, T=4, max_rows=2,
              max_kv=100, max_pages=3, num_pages=9, Hq=4, Hkv=2, D=64, ldq=256, ldo=256, sm=0.1,
-             causal=1, ws=P, O=P)
+             causal=1, ws=P, wbytes=1 << 40, O=P)
 CROSS = dict(Q=P, K=P, V=P, row_start=P, kv_start=P, kv_len=P, B=2, T=4, Tkv=100, max_rows=2,
-             max_kv=50, Hq=4, Hkv=2, D=64, ldq=256, ldk=128, ldv=128, ldo=256, sm=0.1, ws=P, O=P)
+             max_kv=50, Hq=4, Hkv=2, D=64, ldq=256, ldk=128, ldv=128, ldo=256, sm=0.1, ws=P,
+             wbytes=1 << 40, O=P)
 BOTH = [
     (dict(Q=None), 1), (dict(row_start=None), 1), (dict(kv_len=None), 1), (dict(O=None), 1),
     (dict(B=-1), 1), (dict(T=-2), 1), (dict(max_rows=-1), 1), (dict(max_kv=-1), 1),
@@ -104,7 +105,7 @@ BOTH = [
     (dict(Q=P + 8), 1), (dict(O=P + 2), 1), (dict(ws=P + 4), 1), (dict(D=80), 2),
     (dict(B=70000), 2), (dict(max_rows=1 << 25), 2),
     (dict(B=0), 0), (dict(T=0), 0), (dict(max_rows=0), 0),
-    (dict(max_kv=1 << 20, ws=None), 1),               # these need a workspace
+    (dict(max_kv=1 << 20, ws=None), 1), (dict(max_kv=1 << 20, wbytes=1000), 1),   # a workspace
 ]
 
 

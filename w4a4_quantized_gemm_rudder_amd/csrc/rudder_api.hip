@@ -331,7 +331,7 @@ size_t rudder_grouped_scale_count(int K, int N, int group) {
     if (K <= 0 || N <= 0 || K > RUDDER_MAX_K || N > kMaxGroupedN ||
         (group != 32 && group != 64 && group != 128) || K % group)
         return 0;
-    return (size_t)(K / group) * (((size_t)N + 15) / 16 * 16);
+    return ((size_t)K + 127) / 128 * (size_t)(128 / group) * (((size_t)N + 15) / 16 * 16);
 }
 
 rudder_status_t rudder_quantize_weights_grouped(const uint16_t* W, int K, int N, int group,
@@ -397,8 +397,9 @@ rudder_status_t check_ld(const char* f, const char* name, int ld, int heads, int
 }
 
 rudder_status_t check_attention(const char* f, const void* Q, const void* O,
-                                const void* workspace, int B, int T, int max_rows, int max_kv,
-                                int Hq, int Hkv, int D, int ldq, int ldo, float sm) {
+                                const void* workspace, size_t workspace_bytes, int B, int T,
+                                int max_rows, int max_kv, int Hq, int Hkv, int D, int ldq,
+                                int ldo, float sm) {
     if (B < 0 || T < 0 || max_rows < 0 || max_kv < 0)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: B=%d, T=%d, max_rows=%d and max_kv=%d must be "
                     ">= 0", f, B, T, max_rows, max_kv);
@@ -417,10 +418,10 @@ rudder_status_t check_attention(const char* f, const void* Q, const void* O,
     if ((int64_t)max_rows * Hq > (1 << 26))
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d with Hq=%d exceeds 2^26 rows", f,
                     max_rows, Hq);
-    if (!workspace &&
-        rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D) > 0)
-        return fail(RUDDER_ERR_INVALID_ARG, "%s: these sizes need a workspace of %zu bytes", f,
-                    rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D));
+    const size_t need = rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: these sizes need a workspace of %zu bytes, not "
+                    "%zu", f, need, workspace ? workspace_bytes : (size_t)0);
     return RUDDER_OK;
 }
 
@@ -495,15 +496,16 @@ rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_sta
                                        const int8_t* codes, const float* scales, int B, int T,
                                        int max_rows, int max_kv, int max_pages, int num_pages,
                                        int Hq, int Hkv, int D, int ldq, int ldo, float sm,
-                                       int causal, void* workspace, uint16_t* O, void* stream) {
+                                       int causal, void* workspace, size_t workspace_bytes,
+                                       uint16_t* O, void* stream) {
     const char* f = "rudder_cache_attention";
     if (!Q || !row_start || !kv_len || !page_table || !codes || !scales || !O)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
     if (max_pages <= 0 || num_pages <= 0)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: max_pages=%d and num_pages=%d must be positive",
                     f, max_pages, num_pages);
-    const rudder_status_t st = check_attention(f, Q, O, workspace, B, T, max_rows, max_kv, Hq,
-                                               Hkv, D, ldq, ldo, sm);
+    const rudder_status_t st = check_attention(f, Q, O, workspace, workspace_bytes, B, T,
+                                               max_rows, max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if (misaligned(codes))
         return fail(RUDDER_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned", f);
@@ -520,14 +522,14 @@ rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, con
                                        const int32_t* row_start, const int32_t* kv_start,
                                        const int32_t* kv_len, int B, int T, int Tkv, int max_rows,
                                        int max_kv, int Hq, int Hkv, int D, int ldq, int ldk,
-                                       int ldv, int ldo, float sm, void* workspace, uint16_t* O,
-                                       void* stream) {
+                                       int ldv, int ldo, float sm, void* workspace,
+                                       size_t workspace_bytes, uint16_t* O, void* stream) {
     const char* f = "rudder_cross_attention";
     if (!Q || !K || !V || !row_start || !kv_start || !kv_len || !O)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
     if (Tkv < 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Tkv=%d must be >= 0", f, Tkv);
-    rudder_status_t st = check_attention(f, Q, O, workspace, B, T, max_rows, max_kv, Hq, Hkv, D,
-                                         ldq, ldo, sm);
+    rudder_status_t st = check_attention(f, Q, O, workspace, workspace_bytes, B, T, max_rows,
+                                         max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
     if ((st = check_ld(f, "ldv", ldv, Hkv, D)) != RUDDER_OK) return st;

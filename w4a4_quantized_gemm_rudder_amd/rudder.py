@@ -68,6 +68,11 @@ def load_library() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
+    import torch
+    for types, names in ((_BF16, (torch.bfloat16, torch.int16, torch.uint16)),
+                         (_F32, (torch.float32,)), (_I32, (torch.int32,)), (_I8, (torch.int8,)),
+                         (_U8, (torch.uint8,))):
+        types[:] = names
     if not os.path.exists(LIB_PATH):
         raise RudderError(RUDDER_ERR_HIP,
                           f"{LIB_PATH} not found: build it with __graft_entry__.build() "
@@ -124,9 +129,9 @@ def load_library() -> ctypes.CDLL:
     lib.rudder_cache_dequant.restype = i
     lib.rudder_attention_workspace_bytes.argtypes = [i] * 7
     lib.rudder_attention_workspace_bytes.restype = sz
-    lib.rudder_cache_attention.argtypes = [vp] * 6 + [i] * 11 + [f, i, vp, vp, vp]
+    lib.rudder_cache_attention.argtypes = [vp] * 6 + [i] * 11 + [f, i, vp, sz, vp, vp]
     lib.rudder_cache_attention.restype = i
-    lib.rudder_cross_attention.argtypes = [vp] * 6 + [i] * 12 + [f, vp, vp, vp]
+    lib.rudder_cross_attention.argtypes = [vp] * 6 + [i] * 12 + [f, vp, sz, vp, vp]
     lib.rudder_cross_attention.restype = i
     lib.rudder_status_string.argtypes = [i]
     lib.rudder_status_string.restype = ctypes.c_char_p
@@ -137,7 +142,7 @@ def load_library() -> ctypes.CDLL:
 
 
 def _check(status: int) -> None:
-    if status != RUDDER_OK:
+    if status:
         lib = load_library()
         name = lib.rudder_status_string(status).decode()
         raise RudderError(status, f"{name}: {lib.rudder_last_error().decode()}")
@@ -154,10 +159,24 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # the raw handle without a Stream object: a third of the time of current_stream()
+        _raw_stream = ((lambda: get(torch.cuda.current_device())) if get else
+                       (lambda: torch.cuda.current_stream().cuda_stream))
+    return _raw_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -250,44 +269,37 @@ def rudder_stream_sq_error(Y, Yref, stream_id, M: int, N: int, S: int, workspace
 # addresses (ints) pass through unchecked.
 # ---------------------------------------------------------------------------
 
-def _arr(name, t, dtypes, least: int) -> Optional[int]:
+# torch types an argument may have; filled when the library is loaded (importing
+# this module does not import torch)
+_BF16, _F32, _I32, _I8, _U8 = [], [], [], [], []
+
+
+def _arr(name, t, types: list, least: int) -> Optional[int]:
     """Device address of a contiguous tensor of one of the named types with at
     least that many elements (None -> NULL)."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    if str(t.dtype) not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.numel() < least:
-        raise ValueError(f"{name}: {t.numel()} elements, expected at least {least}")
-    return t.data_ptr()
-
-
-_BF16 = ("torch.bfloat16", "torch.int16", "torch.uint16")
-_F32 = ("torch.float32",)
-_I32 = ("torch.int32",)
-_I8 = ("torch.int8",)
-_U8 = ("torch.uint8",)
+    if t.dtype in types and t.numel() >= least and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: {t.dtype}, {t.numel()} elements, strides {t.stride()}: expected "
+                     f"at least {least} contiguous elements of "
+                     f"{' or '.join(str(d) for d in types)}")
 
 
 def _rows(name, t, T: int, H: int, D: int, ld: Optional[int]):
     """(address, row distance) of T rows of H heads of D values: [T, H, D] or
     [T, H * D], a row's values packed, rows any distance apart."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t, H * D if ld is None else ld
-    if str(t.dtype) not in _BF16:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(_BF16)}")
-    shape, st = tuple(t.shape), t.stride()
-    if len(shape) == 3 and shape[1:] == (H, D):
-        packed = (D == 1 or st[2] == 1) and (H == 1 or st[1] == D)
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        packed = shape[1] == H and shape[2] == D and st[2] == 1 and (st[1] == D or H == 1)
     else:
         packed = len(shape) == 2 and shape[1] == H * D and st[1] == 1
-    if not packed or shape[0] < T:
-        raise ValueError(f"{name}: shape {shape} with strides {st}, expected at least {T} rows "
-                         f"of {H} x {D} packed values")
-    if ld is not None and ld != st[0]:
-        raise ValueError(f"{name}: row distance {ld}, but the tensor's is {st[0]}")
+    if not packed or shape[0] < T or t.dtype not in _BF16 or (ld is not None and ld != st[0]):
+        raise ValueError(f"{name}: {t.dtype}, shape {tuple(shape)}, strides {st}: expected at "
+                         f"least {T} rows of {H} x {D} packed bf16 values"
+                         + ("" if ld is None else f", {ld} apart"))
     return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], H * D)
 
 
@@ -301,7 +313,8 @@ def grouped_scale_count(K: int, N: int, group: int) -> int:
 
 def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
                                     stream=None) -> None:
-    _check(load_library().rudder_quantize_weights_grouped(
+    lib = _lib or load_library()
+    _check(lib.rudder_quantize_weights_grouped(
         _arr("W", W, _BF16, K * N), K, N, group,
         _arr("Wq", Wq, _U8, grouped_weight_bytes(K, N)),
         _arr("g_scale", g_scale, _BF16, grouped_scale_count(K, N, group)), _stream(stream)))
@@ -309,9 +322,12 @@ def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
 
 def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, K: int,
                      group: int, S: int, Y, stream=None) -> None:
-    _check(load_library().rudder_matvec_w4(
+    lib = _lib or load_library()
+    n_pad, k_tiles = (N + 15) // 16 * 16, (K + 127) // 128
+    _check(lib.rudder_matvec_w4(
         _arr("X", X, _BF16, M * K), _arr("stream_id", stream_id, _U8, M),
-        _arr("Wq", Wq, _U8, K * N // 2), _arr("g_scale", g_scale, _BF16, K * N // max(group, 1)),
+        _arr("Wq", Wq, _U8, k_tiles * 64 * n_pad),
+        _arr("g_scale", g_scale, _BF16, k_tiles * (128 // max(group, 1)) * n_pad),
         _arr("comp_a", comp_a, _F32, S * N), _arr("comp_b", comp_b, _F32, S * N), M, N, K, group,
         S, _arr("Y", Y, _BF16, M * N), _stream(stream)))
 
@@ -329,10 +345,11 @@ def _cache(codes, scales, num_pages: int, Hkv: int, D: int):
 def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_rows: int,
                         max_pages: int, num_pages: int, Hkv: int, D: int, codes, scales,
                         stream=None, ldk=None, ldv=None) -> None:
+    lib = _lib or load_library()
     k, ldk = _rows("K", K, T, Hkv, D, ldk)
     v, ldv = _rows("V", V, T, Hkv, D, ldv)
     c, s = _cache(codes, scales, num_pages, Hkv, D)
-    _check(load_library().rudder_cache_append(
+    _check(lib.rudder_cache_append(
         k, v, _arr("row_start", row_start, _I32, B + 1), _arr("pos", pos, _I32, B),
         _arr("page_table", page_table, _I32, B * max_pages), B, T, max_rows, max_pages, num_pages,
         Hkv, D, ldk, ldv, c, s, _stream(stream)))
@@ -340,9 +357,10 @@ def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_ro
 
 def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int, D: int, K_out,
                          V_out, stream=None) -> None:
+    lib = _lib or load_library()
     c, s = _cache(codes, scales, num_pages, Hkv, D)
     size = n * Hkv * CACHE_PAGE * D
-    _check(load_library().rudder_cache_dequant(
+    _check(lib.rudder_cache_dequant(
         c, s, _arr("pages", pages, _I32, n), n, num_pages, Hkv, D,
         _arr("K_out", K_out, _F32, size), _arr("V_out", V_out, _F32, size), _stream(stream)))
 
@@ -353,40 +371,43 @@ def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: in
                                                                D))
 
 
-def _workspace(t, B, T, max_rows, max_kv, Hq, Hkv, D) -> Optional[int]:
-    if t is None or isinstance(t, int):
-        return t
-    return _arr("workspace", t, _U8,
-                load_library().rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv,
-                                                                D))
+def _workspace(t):
+    """(address, bytes) of a workspace tensor."""
+    if t is None or t.__class__ is int:
+        return t, 0 if t is None else (1 << 63) - 1
+    return _arr("workspace", t, _U8, 0), t.numel()
 
 
 def rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B: int, T: int,
                            max_rows: int, max_kv: int, max_pages: int, num_pages: int, Hq: int,
                            Hkv: int, D: int, sm: float, causal: bool, workspace, O, stream=None,
                            ldq=None, ldo=None) -> None:
+    lib = _lib or load_library()
     q, ldq = _rows("Q", Q, T, Hq, D, ldq)
     o, ldo = _rows("O", O, T, Hq, D, ldo)
     c, s = _cache(codes, scales, num_pages, Hkv, D)
-    _check(load_library().rudder_cache_attention(
+    w, wbytes = _workspace(workspace)
+    _check(lib.rudder_cache_attention(
         q, _arr("row_start", row_start, _I32, B + 1), _arr("kv_len", kv_len, _I32, B),
         _arr("page_table", page_table, _I32, B * max_pages), c, s, B, T, max_rows, max_kv,
-        max_pages, num_pages, Hq, Hkv, D, ldq, ldo, sm, int(causal),
-        _workspace(workspace, B, T, max_rows, max_kv, Hq, Hkv, D), o, _stream(stream)))
+        max_pages, num_pages, Hq, Hkv, D, ldq, ldo, sm, int(causal), w, wbytes, o,
+        _stream(stream)))
 
 
 def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int, Tkv: int,
                            max_rows: int, max_kv: int, Hq: int, Hkv: int, D: int, sm: float,
                            workspace, O, stream=None, ldq=None, ldk=None, ldv=None,
                            ldo=None) -> None:
+    lib = _lib or load_library()
     q, ldq = _rows("Q", Q, T, Hq, D, ldq)
     k, ldk = _rows("K", K, Tkv, Hkv, D, ldk)
     v, ldv = _rows("V", V, Tkv, Hkv, D, ldv)
     o, ldo = _rows("O", O, T, Hq, D, ldo)
-    _check(load_library().rudder_cross_attention(
+    w, wbytes = _workspace(workspace)
+    _check(lib.rudder_cross_attention(
         q, k, v, _arr("row_start", row_start, _I32, B + 1), _arr("kv_start", kv_start, _I32, B),
         _arr("kv_len", kv_len, _I32, B), B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk, ldv,
-        ldo, sm, _workspace(workspace, B, T, max_rows, max_kv, Hq, Hkv, D), o, _stream(stream)))
+        ldo, sm, w, wbytes, o, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
