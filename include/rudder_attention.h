@@ -100,10 +100,12 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * head h of Hq and its cached head h / (Hq / Hkv):
  *   o = sum_j softmax_j(sm * q . k_j) v_j,  j < kv, and where causal is
  *       not 0 also j <= kv - n + i
- * A row with no visible token gives zeros.  Products in fp16 with fp32 sums
- * (the codes are exact; q is exact relative to its row's largest element to
- * 2^-25; the softmax weights are rounded to fp16), the softmax in fp32, one
- * rounding to bf16.  V scales below 2^-80 count as 2^-80.
+ * A row with no visible token gives zeros, a query row that is not finite NaN.
+ * q . k is formed in integers, q rounded to units of 2^-14 of its row's
+ * largest power of two (elements within 2^-7 of the largest are exact); the
+ * softmax is in fp32, its weights rounded to fp16 for the product with the
+ * codes of V, fp32 sums, one rounding to bf16.  V scales below 2^-80 count as
+ * 2^-80.
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)

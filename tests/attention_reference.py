@@ -117,14 +117,15 @@ def values(codes, scales, pages):
 
 # --- attention -------------------------------------------------------------
 
-def rows_attention(q, k, v, visible, sm, p_half_step):
+def rows_attention(q, k, v, visible, sm, p_half_step, q_step):
     """q [n, D], k, v [kv, D] in 64 bits, visible [n, kv]: (o, bound).
 
     With A = sum p |v|: the weights' rounding (p_half_step), the two rounded sums over the keys
     ((kv + 70) additions or rescalings of 32 bits each) and the weights' relative error from an
     error dz of the exponent, in numerator and denominator: 2 ln 2 dz.  dz: the fp32 product
-    of D terms and its scaling, (D + 8) half steps of c sum |q k|; the small elements of q
-    (2^-25 of the row's largest each); three roundings at the exponent's own magnitude and that of
+    of D terms and its scaling, (D + 8) half steps of c sum |q k|; q's own rounding (q_step of the
+    row's largest element, for the cache half a unit 2^-14 of the largest power of
+    two in the row, or one unit for the largest itself: 2^-15); three roundings at the exponent's own magnitude and that of
     log2 of a scale (80 at most).  Then the absolute floor of weights held in fp16 (2^-33 of the
     largest a key), and the rounding to bf16."""
     if not len(k):
@@ -141,7 +142,7 @@ def rows_attention(q, k, v, visible, sm, p_half_step):
     kv, D = k.shape
     ak = k.abs().amax(0).sum()                           # at least sum |k| of any one key
     zmax = (q.abs() @ k.abs().t()).amax(1, keepdim=True) * abs(c)
-    dz = zmax * (D + 8) * FP32 + abs(c) * q.abs().amax(1, keepdim=True) * ak * 2.0 ** -25
+    dz = zmax * (D + 8) * FP32 + abs(c) * q.abs().amax(1, keepdim=True) * ak * q_step
     dz = dz + 3 * FP32 * (2 * zmax + 80) + 4 * FP32
     A = p @ v.abs()
     e = A * (p_half_step + 2 * math.log(2) * dz + 2 * (kv + 70) * FP32)
@@ -174,7 +175,8 @@ def cache_attention(q, row_start, kv_len, table, codes, scales, sm, causal):
             g = h // (Hq // H)
             kk = torch.where(there[:, None], k[:, g].reshape(-1, D)[:kv], 0.0)
             vv = torch.where(there[:, None], v[:, g].reshape(-1, D)[:kv], 0.0)
-            o[r0:r1, h], e[r0:r1, h] = rows_attention(q[r0:r1, h].double(), kk, vv, vis, sm, FP16)
+            o[r0:r1, h], e[r0:r1, h] = rows_attention(q[r0:r1, h].double(), kk, vv, vis, sm, FP16,
+                                                          2.0 ** -15)
     return o, e
 
 
@@ -191,7 +193,7 @@ def cross_attention(q, k, v, row_start, kv_start, kv_len, sm):
             g = h // (Hq // H)
             o[r0:r1, h], e[r0:r1, h] = rows_attention(
                 q[r0:r1, h].double(), k[k0:k0 + n, g].double(), v[k0:k0 + n, g].double(), vis, sm,
-                BF16)
+                BF16, 0.0)
     return o, e
 
 
