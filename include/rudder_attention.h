@@ -121,8 +121,9 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * <= 0, Hq % Hkv != 0, max_pages or num_pages <= 0, ldq or ldo below Hq * D or
  * not a multiple of 8, sm not finite, a workspace that is too small, Q, codes, O
  * or workspace not 16-byte aligned;
- * UNSUPPORTED for D other than 64 or 128, B > 65535, Hkv > 4096, or more than
- * 2^26 (row, head) pairs in max_rows * Hq.
+ * UNSUPPORTED for D other than 64 or 128, Hkv > 4096, B * Hkv > 65535,
+ * max_rows * Hq > 2^26, or B * Hkv * ceil(max_rows * Hq / Hkv / 128) > 2^21
+ * (give max_rows as it is, not a far larger bound).
  */
 rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_start,
                                        const int32_t* kv_len, const int32_t* page_table,

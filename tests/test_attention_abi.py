@@ -54,11 +54,12 @@ def test_sizes(r):
     assert r.grouped_scale_count(96, 17, 64) == 0
     assert r.cache_page_bytes(8, 128) == 8 * 2 * 64 * 128
     assert r.cache_page_bytes(8, 96) == 0 and r.cache_page_bytes(0, 64) == 0
-    # many rows need no pieces; one row of a long cache does, and its workspace grows with T
-    assert r.attention_workspace_bytes(2, 8384, 4192, 4192, 16, 16, 128) == 0
+    # whole rounds of row tiles need no pieces; one row of a long cache does
+    assert r.attention_workspace_bytes(2, 8192, 4096, 4192, 16, 16, 128) == 0
     one = r.attention_workspace_bytes(1, 1, 1, 40000, 16, 16, 128)
     assert one > 0 and one % (16 * 130 * 4) == 0
-    assert r.attention_workspace_bytes(1, 3, 1, 40000, 16, 16, 128) == 3 * one
+    # bounded by T, not by a loose max_rows
+    assert r.attention_workspace_bytes(1, 1, 1000, 40000, 16, 16, 128) == one
     for bad in ((1, 1, 1, 100, 15, 2, 64), (1, 1, 1, 100, 4, 2, 96), (-1, 1, 1, 100, 4, 2, 64),
                 (1, 1, 1, -1, 4, 2, 64)):
         assert r.attention_workspace_bytes(*bad) == 0
@@ -103,7 +104,8 @@ BOTH = [
     (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(ldq=255), 1), (dict(ldq=248), 1),
     (dict(ldo=260), 1), (dict(sm=float("nan")), 1), (dict(sm=float("inf")), 1),
     (dict(Q=P + 8), 1), (dict(O=P + 2), 1), (dict(ws=P + 4), 1), (dict(D=80), 2),
-    (dict(B=70000), 2), (dict(max_rows=1 << 25), 2),
+    (dict(B=70000), 2), (dict(B=40000), 2), (dict(max_rows=1 << 25), 2),
+    (dict(B=3000, T=1 << 20, max_rows=1 << 20), 2),
     (dict(B=0), 0), (dict(T=0), 0), (dict(max_rows=0), 0),
     (dict(max_kv=1 << 20, ws=None), 1), (dict(max_kv=1 << 20, wbytes=1000), 1),   # a workspace
 ]

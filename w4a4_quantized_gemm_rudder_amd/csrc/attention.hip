@@ -26,6 +26,7 @@
 // maximum of t, P_j = exp2(t_j - m) multiplies plain codes, and
 // l = sum P_j / sv.  P is rounded to fp16 (2^-11 relative, absolute 2^-33 below
 // 2^-22); the sum l is formed from the unrounded values.
+#include <stdlib.h>
 #include <cmath>
 
 #include "rudder_internal.h"
@@ -39,9 +40,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_acc __attribute__((ext_vector_type(16)));
 
 constexpr int kPage = RUDDER_CACHE_PAGE;           // keys a tile
-constexpr int kThreads = 256;
-constexpr int kWaveRows = 32;
-constexpr int kRows = 4 * kWaveRows;               // query rows a workgroup
+constexpr int kWaveRows = 32;                      // query rows a wave of the tile kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 8.0f;                    // cache: P and its sums are held times 2^8
 // Smallest V scale the exponent takes: smaller ones (an all-zero block's 0) are read as this.
@@ -63,15 +62,39 @@ struct Problem {
     int Tkv;
     size_t ldk, ldv;
     // both
-    int T, max_rows, max_kv, Hq, Hkv, causal;
+    int B, T, max_rows, max_kv, Hq, Hkv, causal;
     size_t ldq, ldo;
     float sm;
     uint16_t* O;
-    // split of the key axis: `splits` pieces of `split_tiles` tiles; partial results when > 1
-    int splits, split_tiles;
-    float* part_o;      // [splits][T * Hq][D]
-    float2* part_ml;    // [splits][T * Hq]
+    // Work units: `tile_rows` row tiles of each (head, sequence) pair.  The first `whole` of them
+    // take all of their keys; the others are split into `pieces` of `piece_tiles` tiles whose
+    // results are joined.
+    int tile_rows, units, whole, pieces, piece_tiles, most_tiles;
+    int last_first;     // 1: a pair's row tiles in descending order
+    float* part_o;      // [pieces][units - whole][rows of a unit][D]
+    float2* part_ml;    // [pieces][units - whole][rows of a unit]
 };
+
+// Unit number -> row tile of a pair.  Workgroups go round robin to the eight dies: the tiles of a
+// pair, which read the same keys, are kept on one where the pairs divide evenly.  Causal tiles come
+// longest first.
+struct Place {
+    int h, b, tile;
+};
+// a / b of wave-uniform values, back in a scalar register (the division runs on the vector units)
+__device__ __forceinline__ int quotient(int a, int b) {
+    return __builtin_amdgcn_readfirstlane(a / b);
+}
+__device__ __forceinline__ Place place(const Problem& p, int unit) {
+    const int pairs = p.Hkv * p.B, slot = unit / 8;
+    const bool even = pairs % 8 == 0;
+    const int pair = even ? unit % 8 + 8 * quotient(slot, p.tile_rows)
+                          : quotient(unit, p.tile_rows);
+    const int tile = (even ? slot : unit) - quotient(even ? slot : unit, p.tile_rows) * p.tile_rows;
+    const int b = quotient(pair, p.Hkv);
+    // arithmetic in place of a choice by p.causal, which would make two kernels of one
+    return {pair - b * p.Hkv, b, tile + p.last_first * (p.tile_rows - 1 - 2 * tile)};
+}
 
 // Sequence b's query rows and keys, clamped to the buffers whatever the arrays hold.
 struct Sequence {
@@ -126,40 +149,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return r.u;
 }
 
-// Largest magnitude of a lane's share of a query row.
-template <int N>
-__device__ __forceinline__ float abs_max(const uint4 (&q)[N]) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
-                                     fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
-    }
-    return amax;
-}
-
-// A query row of largest magnitude amax = f * 2^e, f in [1, 2), to fp16 times 2^-e; returns 2^e.
-// A row of zeros or infinities keeps e = 0.
-template <int N>
-__device__ __forceinline__ float to_f16(uint4 (&q)[N], float amax) {
-    const int field = (int)(__float_as_uint(amax) >> 23);
-    const int e = (field == 0 || field == 255) ? 0 : min(max(field - 127, -120), 120);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = pack_f16(__uint_as_float(w[j] << 16) * down,
-                            __uint_as_float(w[j] & 0xFFFF0000u) * down);
-        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return __uint_as_float((uint32_t)(127 + e) << 23);
-}
-
 // Largest magnitude bits of a lane's share of a query row (NaN patterns are the largest).
 template <int N>
 __device__ __forceinline__ uint32_t abs_max_bits(const uint4 (&q)[N]) {
@@ -172,6 +161,25 @@ __device__ __forceinline__ uint32_t abs_max_bits(const uint4 (&q)[N]) {
             top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
     }
     return top;
+}
+
+// A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), to fp16 times
+// 2^-e.  Returns 2^e.
+template <int N>
+__device__ __forceinline__ float to_f16(uint4 (&q)[N], uint32_t top) {
+    const int field = (int)(top >> 7);
+    const int e = field == 0 ? 0 : min(max(field - 127, -120), 120);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = pack_f16(__uint_as_float(w[j] << 16) * down,
+                            __uint_as_float(w[j] & 0xFFFF0000u) * down);
+        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), as integers
@@ -237,143 +245,209 @@ __device__ __forceinline__ bool scales_apart(float lsv, float top_lsv) {
     return __builtin_amdgcn_readfirstlane(lsv < top_lsv - 60.0f);
 }
 
-// One tile of 64 keys on its way from HBM to LDS.
-template <int D, bool CACHE>
+// One tile of 64 keys on its way from HBM to LDS, THREADS threads.  LDS holds the operands of the
+// products: K rows at their accumulator rows, V as [channel][key], 16 bytes behind each row so that
+// 16 rows start at 16 places of the 64 banks.
+template <int D, bool CACHE, int THREADS>
 struct Stage {
-    static constexpr int kKStride = D * 2 + 16;    // bytes of a key's row in LDS
-    static constexpr int kVStride = kPage * 2 + 16;    // bytes of a channel's row in LDS
+    static constexpr int kKStride = D * 2 + 16;            // bytes of a key's row
+    static constexpr int kVStride = kPage * 2 + 16;        // bytes of a channel's row
     static constexpr int kKBytes = kPage * kKStride;
-    static constexpr int kVBytes = D * kVStride;
-    static constexpr int kNK = CACHE ? D / 64 : D / 32;    // 16-byte pieces a thread
-    static constexpr int kNV = CACHE ? D / 64 : 4;
-    uint4 k[kNK], v[kNV];                          // states: v[i] is key i of the thread's four
+    static constexpr int kBytes = kKBytes + D * kVStride;
+    static constexpr int kUnits = CACHE ? kPage * D / 16 : kPage * D / 8;  // 16-byte pieces of K
+    static constexpr int kNK = (kUnits + THREADS - 1) / THREADS;
+    // states: a thread takes kKeys keys x eight channels of V
+    static constexpr int kKeys = kPage * D / 8 / THREADS > 2 ? 4 : 2;
+    static constexpr int kVUnits = CACHE ? kUnits : kPage / kKeys * (D / 8);
+    static constexpr int kNV = CACHE ? kNK : kKeys;
+    uint4 k[kNK], v[kNV];
 
-    // page: the tile's page number (cache); key0, kv: first key and the sequence's keys (states)
+    static constexpr int kGroups = kPage / kKeys;          // of keys
+    // a wave takes 64 bytes of 16 or 32 rows: whole sectors, and transposed writes whose lanes
+    // differ in their keys
+    static __device__ __forceinline__ int v_channel(int tid) {
+        return (tid % 4 + tid / (4 * kGroups) * 4) * 8;
+    }
+    static __device__ __forceinline__ int v_key(int tid) { return tid / 4 % kGroups * kKeys; }
+
+    // page: the tile's page number (cache); key0: its first key (states)
     __device__ __forceinline__ void load(const Problem& p, const Sequence& s, int h, int page,
                                          int key0) {
         const int tid = threadIdx.x;
         if constexpr (CACHE) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.codes + ((size_t)page * p.Hkv + h) * (size_t)(2 * kPage * D));
+            const int8_t* src = p.codes + ((size_t)page * p.Hkv + h) * (size_t)(2 * kPage * D);
 #pragma unroll
-            for (int i = 0; i < kNK; ++i) k[i] = src[tid + i * kThreads];
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) v[i] = src[kPage * D / 16 + tid + i * kThreads];
+            for (int i = 0; i < kNK; ++i) {
+                const int u = tid + i * THREADS;
+                if (kUnits % THREADS == 0 || u < kUnits) {
+                    k[i] = *reinterpret_cast<const uint4*>(src + u * 16);
+                    v[i] = *reinterpret_cast<const uint4*>(src + kPage * D + u * 16);
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kNK; ++i) {
-                const int u = tid + i * kThreads, key = key0 + u / (D / 8);
+                const int u = tid + i * THREADS, key = key0 + u / (D / 8);
                 k[i] = make_uint4(0, 0, 0, 0);
                 if (key < s.kv)
                     k[i] = *reinterpret_cast<const uint4*>(
                         p.K + (size_t)(s.kv0 + key) * p.ldk + (size_t)h * D + u % (D / 8) * 8);
             }
-            // V: four keys x eight channels a thread (all threads for D = 128, half for 64)
-            if (tid < 2 * D) {
+            if (kVUnits % THREADS == 0 || tid < kVUnits) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + tid / (D / 8) * 4 + i;
+                for (int i = 0; i < kKeys; ++i) {
+                    const int key = key0 + v_key(tid) + i;
                     v[i] = make_uint4(0, 0, 0, 0);
                     if (key < s.kv)
                         v[i] = *reinterpret_cast<const uint4*>(
-                            p.V + (size_t)(s.kv0 + key) * p.ldv + (size_t)h * D +
-                            tid % (D / 8) * 8);
+                            p.V + (size_t)(s.kv0 + key) * p.ldv + (size_t)h * D + v_channel(tid));
                 }
             }
         }
     }
 
-    __device__ __forceinline__ void store(uint8_t* lk, uint8_t* lv) const {
+    __device__ __forceinline__ void store(uint8_t* lds) const {
         const int tid = threadIdx.x;
+        uint8_t* lv = lds + kKBytes;
         if constexpr (CACHE) {
 #pragma unroll
             for (int i = 0; i < kNK; ++i) {
-                const int u = tid + i * kThreads, row = swap23(u / (D / 16));
-                uint8_t* d = lk + row * kKStride + u % (D / 16) * 32;
-                put(d, k[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) {
-                const int u = tid + i * kThreads;
-                put(lv + u / 4 * kVStride + u % 4 * 32, v[i]);
+                const int u = tid + i * THREADS;
+                if (kUnits % THREADS == 0 || u < kUnits) {
+                    uint8_t* d = lds + swap23(u / (D / 16)) * kKStride + u % (D / 16) * 32;
+                    put(d, d + 16, k[i]);
+                    d = lv + u / 4 * kVStride + u % 4 * 32;
+                    put(d, d + 16, v[i]);
+                }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < kNK; ++i) {
-                const int u = tid + i * kThreads, row = swap23(u / (D / 8));
-                *reinterpret_cast<uint4*>(lk + row * kKStride + u % (D / 8) * 16) = k[i];
+                const int u = tid + i * THREADS;
+                *reinterpret_cast<uint4*>(lds + swap23(u / (D / 8)) * kKStride +
+                                          u % (D / 8) * 16) = k[i];
             }
-            if (tid < 2 * D) {
-                uint8_t* d = lv + tid % (D / 8) * 8 * kVStride + tid / (D / 8) * 8;
-                put4(d, v[0].x, v[1].x, v[2].x, v[3].x);
-                put4(d + 2 * kVStride, v[0].y, v[1].y, v[2].y, v[3].y);
-                put4(d + 4 * kVStride, v[0].z, v[1].z, v[2].z, v[3].z);
-                put4(d + 6 * kVStride, v[0].w, v[1].w, v[2].w, v[3].w);
+            if (kVUnits % THREADS == 0 || tid < kVUnits) {
+                uint8_t* d = lv + v_channel(tid) * kVStride + v_key(tid) * 2;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[kKeys];
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        w[i] = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
+                    put_keys(d + 2 * j * kVStride, w);
+                }
             }
         }
     }
 
-    // Two channels of four keys, transposed.
-    static __device__ __forceinline__ void put4(uint8_t* d, uint32_t a, uint32_t b, uint32_t c,
-                                                uint32_t e) {
-        *reinterpret_cast<uint2*>(d) = make_uint2(__builtin_amdgcn_perm(b, a, 0x05040100u),
-                                                  __builtin_amdgcn_perm(e, c, 0x05040100u));
-        *reinterpret_cast<uint2*>(d + kVStride) =
-            make_uint2(__builtin_amdgcn_perm(b, a, 0x07060302u),
-                       __builtin_amdgcn_perm(e, c, 0x07060302u));
+    // Two channels of kKeys keys, transposed.
+    static __device__ __forceinline__ void put_keys(uint8_t* d, const uint32_t (&w)[kKeys]) {
+        uint32_t lo[kKeys / 2], hi[kKeys / 2];
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; ++i) {
+            lo[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x05040100u);
+            hi[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302u);
+        }
+        if constexpr (kKeys == 4) {
+            *reinterpret_cast<uint2*>(d) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(d + kVStride) = make_uint2(hi[0], hi[1]);
+        } else {
+            *reinterpret_cast<uint32_t*>(d) = lo[0];
+            *reinterpret_cast<uint32_t*>(d + kVStride) = hi[0];
+        }
     }
 
-    static __device__ __forceinline__ void put(uint8_t* d, uint4 c) {
+    static __device__ __forceinline__ void put(uint8_t* d0, uint8_t* d1, uint4 c) {
         const uint2 a = widen4(c.x), b = widen4(c.y), e = widen4(c.z), f = widen4(c.w);
-        *reinterpret_cast<uint4*>(d) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(d + 16) = make_uint4(e.x, e.y, f.x, f.y);
+        *reinterpret_cast<uint4*>(d0) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(d1) = make_uint4(e.x, e.y, f.x, f.y);
     }
 };
 
-template <int D, bool CACHE>
-__global__ void __launch_bounds__(kThreads, 2)
+// Order of a block of N products, their N LDS reads and the vector work beside them: reads four
+// products ahead, four vector instructions a product.
+template <int N>
+__device__ __forceinline__ void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);     // LDS reads
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // a product
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x400, 1, 0); // an exponential
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // vector instructions
+    }
+}
+
+// The running maximum is raised only where a score passes it by more than 2^6 (P has room for it):
+// most tiles then need no exchange between lanes and no rescaling of O.
+constexpr float kLazy = 6.0f;
+
+// ---------------------------------------------------------------------------
+// Many rows: WAVES waves of 32 rows share the tiles through LDS.
+// ---------------------------------------------------------------------------
+template <int D, bool CACHE, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 2)
 attention_tile_kernel(const Problem p) {
-    using St = Stage<D, CACHE>;
+    using St = Stage<D, CACHE, WAVES * 64>;
+    constexpr int kRows = WAVES * kWaveRows;
     constexpr int kKS = D / 16;                    // steps of the first product
     constexpr int kDT = D / 32;                    // channel tiles of the second
-    __shared__ __align__(16) uint8_t lk[St::kKBytes];
-    __shared__ __align__(16) uint8_t lv[St::kVBytes];
+    // with one workgroup a unit three tiles fit beside each other, which saves a barrier a tile
+    constexpr int kBuffers = WAVES == 8 ? 3 : 2;
+    __shared__ __align__(16) uint8_t lds[kBuffers * St::kBytes];
 
-    const int split = blockIdx.x % p.splits, tile_row = blockIdx.x / p.splits;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5;
+    const int rest = p.units - p.whole;            // split units
+    const int split = (int)blockIdx.x < p.whole ? -1 : quotient(blockIdx.x - p.whole, rest);
+    const int unit = split < 0 ? blockIdx.x : blockIdx.x - split * rest;
+    const Place at_unit = place(p, unit);
+    const int h = at_unit.h, b = at_unit.b, tile_row = at_unit.tile;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int tile0 = max(split, 0) * p.piece_tiles;
+    // page numbers of 64 tiles, one a lane
+    const int32_t* table = CACHE ? p.page_table + (size_t)b * p.max_pages : nullptr;
+    auto page_numbers = [&](int i) {
+        const int64_t at = (int64_t)tile0 + i + lane;
+        return CACHE && at < p.max_pages ? table[at] : -1;
+    };
+    int numbers = page_numbers(0);
     const Sequence s = sequence<CACHE>(p, b);
-    const int G = p.Hq / p.Hkv;
+    const int G = quotient(p.Hq, p.Hkv);
     const int rows = min(s.n, p.max_rows) * G;     // (token, head of the group) pairs
     if (tile_row * kRows >= rows) return;
 
-    // this lane's query row
-    const int row = tile_row * kRows + wave * kWaveRows + (lane & 31);
+    // this lane's query row and the keys it sees; the least and most any row of the wave sees
+    const int row0 = tile_row * kRows + wave * kWaveRows, row = row0 + (lane & 31);
     const bool live = row < rows;
-    const bool wave_live = tile_row * kRows + wave * kWaveRows < rows;
     const int t = live ? row / G : 0;
     const int head = h * G + (live ? row % G : 0);
-    // keys visible to it, and the last row of the workgroup that has any
-    const int limit = !live ? 0 : p.causal ? min(max(s.kv - s.n + t + 1, 0), s.kv) : s.kv;
-    const int last_t = (min(rows, (tile_row + 1) * kRows) - 1) / G;
-    const int most = p.causal ? min(max(s.kv - s.n + last_t + 1, 0), s.kv) : s.kv;
-    const int tile0 = split * p.split_tiles;
-    const int tile1 = min((most + kPage - 1) / kPage, tile0 + p.split_tiles);
-    if (p.splits > 1 && tile0 * kPage >= s.kv) return;     // the join does not read this piece
+    auto sees = [&](int tt) { return p.causal ? min(max(s.kv - s.n + tt + 1, 0), s.kv) : s.kv; };
+    const int limit = live ? sees(t) : 0;
+    const int least = sees(quotient(row0, G));
+    const int wave_most = row0 < rows ? sees(quotient(min(rows, row0 + kWaveRows) - 1, G)) : 0;
+    const int most = sees(quotient(min(rows, (tile_row + 1) * kRows) - 1, G));
+    const int tile1 = min((most + kPage - 1) / kPage,
+                          tile0 + (split < 0 ? p.most_tiles : p.piece_tiles));
+    if (split >= 0 && tile0 * kPage >= s.kv) return;       // the join does not read this piece
 
     uint4 q[kKS];
-    float c = p.sm * kLog2e;
+    float l = 0.0f;                                // the lane's share of the sum of weights
+    // the softmax scale's sign goes to the query, so that exponents grow with the products
+    float c = fabsf(p.sm) * kLog2e;
     {
         const uint16_t* src = p.Q + (size_t)(s.r0 + t) * p.ldq + (size_t)head * D + half * 8;
+        const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < kKS; ++i) {
             q[i] = make_uint4(0, 0, 0, 0);
             if (live) q[i] = *reinterpret_cast<const uint4*>(src + i * 16);
+            q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
         }
-        if (CACHE) {
-            const float amax = abs_max<kKS>(q);
-            c *= to_f16<kKS>(q, fmaxf(amax, __shfl_xor(amax, 32)));
-        }
+        uint32_t top = abs_max_bits<kKS>(q);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        if (CACHE) c *= to_f16<kKS>(q, top);
     }
 
     f32x16_acc o[kDT];
@@ -381,107 +455,177 @@ attention_tile_kernel(const Problem p) {
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -INFINITY, l = 0.0f, top_lsv = -INFINITY;
+    float m = -INFINITY, top_lsv = -INFINITY;
 
-    const int32_t* table = CACHE ? p.page_table + (size_t)b * p.max_pages : nullptr;
-    // The next tile at or behind `i` whose page lies in the pool (others hold no keys).
-    auto next = [&](int i, int& page) {
-        page = 0;
-        if (CACHE)
-            for (; i < tile1; ++i) {
-                page = __builtin_amdgcn_readfirstlane(table[i]);
-                if (page >= 0 && page < p.num_pages) break;
-            }
-        return i;
+    int index = -1;
+    // the next tile's page that lies in the pool, -1 behind the last tile
+    auto next = [&]() {
+        for (;;) {
+            if (tile0 + ++index >= tile1) return -1;
+            if (!CACHE) return 0;
+            if (index > 0 && (index & 63) == 0) numbers = page_numbers(index);
+            const int page = __builtin_amdgcn_readlane(numbers, index & 63);
+            if (page >= 0 && page < p.num_pages) return page;
+        }
     };
-
     St stage;
-    int page;
-    int tile = next(tile0, page);
-    if (tile < tile1) stage.load(p, s, h, page, tile * kPage);
-    while (tile < tile1) {
-        const int at = tile * kPage;
-        float cz = c, lsv = 0.0f, sv_inv = 1.0f;
+    int page = -1, next_at = 0;
+    float sk = 1.0f, sv = 1.0f;
+    auto load = [&]() {                            // the next tile, on its way to registers
+        page = next();
+        if (page < 0) return;
+        next_at = (tile0 + index) * kPage;
+        stage.load(p, s, h, page, next_at);
         if (CACHE) {
             const float* sc = p.scales + ((size_t)page * p.Hkv + h) * 2;
-            cz = c * sc[0];
-            const float sv = fmaxf(sc[1], kMinVScale);
-            lsv = __builtin_amdgcn_logf(sv);       // log2
-            sv_inv = 1.0f / sv;
+            sk = sc[0];
+            sv = sc[1];
         }
-        __syncthreads();                           // the last tile has been read
-        stage.store(lk, lv);
-        tile = next(tile + 1, page);
-        if (tile < tile1) stage.load(p, s, h, page, tile * kPage);
-        __syncthreads();
-        if (!wave_live) continue;
+    };
+    // scores of 32 keys: register j holds key 16 (j / 8) + 8 half + j % 8
+    const int k_lane = (lane & 31) * St::kKStride + half * 16;
+    const int v_lane = St::kKBytes + (lane & 31) * St::kVStride + half * 16;
+    auto scores = [&](const uint8_t* tile, int hf) {
+        f32x16_acc z;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKS; ++i)
+            z = mma<CACHE>(*reinterpret_cast<const uint4*>(tile + k_lane + hf * 32 * St::kKStride +
+                                                           i * 32), q[i], z);
+        return z;
+    };
+    uint4 pend0 = make_uint4(0, 0, 0, 0), pend1 = pend0;   // P of the 32 keys before
+    auto weigh = [&](const uint8_t* tile, int hf) {        // O += V P of these
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt) {
+            const uint8_t* v = tile + v_lane + dt * 32 * St::kVStride + hf * 64;
+            o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(v), pend0, o[dt]);
+            o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(v + 32), pend1, o[dt]);
+        }
+    };
 
-        f32x16_acc z[2];
+    // Software pipeline over halves of tiles: while the weights of 32 keys are formed on the vector
+    // units, the matrix cores work on the scores of the next 32 and the values of the last 32.
+    load();
+    if (page >= 0) {
+        uint8_t* cur = lds;                        // holds the tile at hand
+        uint8_t* old = lds;                        // the one before
+        int slot = 0;
+        stage.store(cur);
+        int at = next_at;
+        float cz = 0.0f, lsv = 0.0f, sv_inv = 1.0f;
+        auto scales = [&]() {
+            // c or a K scale of 0 must leave masked scores at -inf
+            cz = fmaxf(CACHE ? c * sk : c, 1e-30f);
+            const float svc = CACHE ? fmaxf(sv, kMinVScale) : 1.0f;
+            lsv = CACHE ? __builtin_amdgcn_logf(svc) : 0.0f;       // log2
+            sv_inv = CACHE ? 1.0f / svc : 1.0f;
+        };
+        scales();
+        load();
+        __syncthreads();
+        f32x16_acc z;
+        if (at < wave_most) z = scores(cur, 0);
+        bool mine = at < wave_most;                // some row of this wave sees the tile at hand
+
+        // z, the scores of half hf, become weights; `ahead` runs the products beside
+        auto step = [&](int hf, auto ahead, const uint8_t* before, int before_hf) {
+            const int key0 = at + 32 * hf;
+            if (key0 + 32 > least) {               // some row does not see all of these keys
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[tt][j] = 0.0f;
-            const uint8_t* kr = lk + (tt * 32 + (lane & 31)) * St::kKStride + half * 16;
-#pragma unroll
-            for (int i = 0; i < kKS; ++i)
-                z[tt] = mma<CACHE>(*reinterpret_cast<const uint4*>(kr + i * 32), q[i], z[tt]);
-        }
-        // t = c * z + log2(sv); key of register j: 32 tt + 16 (j / 8) + 8 half + j % 8
-        float top = -INFINITY;
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int key = at + 32 * tt + 16 * (j >> 3) + 8 * half + (j & 7);
-                const float v = key < limit ? fmaf(cz, z[tt][j], lsv) : -INFINITY;
-                z[tt][j] = v;
-                top = fmaxf(top, v);
+                for (int j = 0; j < 16; ++j)
+                    if (key0 + 16 * (j >> 3) + 8 * half + (j & 7) >= limit) z[j] = -INFINITY;
             }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m, top);
-        const float base = (m_new == -INFINITY ? 0.0f : m_new) - (CACHE ? kPShift : 0.0f);
-        const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
-        float sum = 0.0f, own = 0.0f;
-        top_lsv = fmaxf(top_lsv, lsv);
-        const bool far = CACHE && scales_apart(lsv, top_lsv);
-        if (far)
+            float top = z[0];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, z[j]);
+            top = fmaf(cz, top, lsv);              // -inf: nothing visible
+            if (__any(top > m + kLazy)) {
+                weigh(before, before_hf);          // still under the old maximum
+                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+                const float m_new = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+                m = m_new;
+                l *= alpha;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) own += __builtin_amdgcn_exp2f(z[tt][j] - lsv - base);
-        uint4 pk[4];
+                for (int dt = 0; dt < kDT; ++dt)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t w[4];
+                    for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
+            }
+            // P = exp2(c z + log2(sv) - m), for the cache times 2^8
+            const float shift = lsv - (m == -INFINITY ? 0.0f : m) + (CACHE ? kPShift : 0.0f);
+            bool apart = false;
+            if (CACHE) {
+                top_lsv = fmaxf(top_lsv, lsv);
+                apart = scales_apart(lsv, top_lsv);
+                if (apart)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = (ks & 1) * 8 + 2 * j;
-                const float a = __builtin_amdgcn_exp2f(z[ks >> 1][r] - base);
-                const float e = __builtin_amdgcn_exp2f(z[ks >> 1][r + 1] - base);
+                    for (int j = 0; j < 16; ++j)
+                        l += __builtin_amdgcn_exp2f(fmaf(cz, z[j], shift - lsv));
+            }
+            f32x16_acc zn = ahead();
+            weigh(before, before_hf);
+            float sum = 0.0f;
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float a = __builtin_amdgcn_exp2f(fmaf(cz, z[2 * j], shift));
+                const float e = __builtin_amdgcn_exp2f(fmaf(cz, z[2 * j + 1], shift));
                 sum += a + e;
                 w[j] = CACHE ? pack_f16(a, e) : pack_bf16(a, e);
             }
-            pk[ks] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        l = fmaf(l, alpha, far ? own : sum * sv_inv);
-        m = m_new;
-#pragma unroll
-        for (int dt = 0; dt < kDT; ++dt) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
-            const uint8_t* vr = lv + (dt * 32 + (lane & 31)) * St::kVStride + half * 16;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(vr + ks * 32), pk[ks], o[dt]);
+            interleave<2 * kDT + kKS>();
+            l = fmaf(sum, apart ? 0.0f : sv_inv, l);
+            pend0 = make_uint4(w[0], w[1], w[2], w[3]);
+            pend1 = make_uint4(w[4], w[5], w[6], w[7]);
+            z = zn;
+        };
+        for (;;) {
+            if (mine) step(0, [&]() { return scores(cur, 1); }, old, 1);
+            if (kBuffers == 2) __syncthreads();    // the tile before has been read
+            const bool more = page >= 0;
+            uint8_t* ahead = cur;
+            const int ahead_at = next_at;
+            const float sk1 = sk, sv1 = sv;
+            if (more) {
+                slot = slot + 1 == kBuffers ? 0 : slot + 1;
+                ahead = lds + slot * St::kBytes;
+                stage.store(ahead);
+                load();
+            }
+            __syncthreads();
+            const bool mine_next = more && ahead_at < wave_most;
+            if (mine_next)
+                step(1, [&]() { return scores(ahead, 0); }, cur, 0);
+            else if (mine) {
+                step(1, [&]() { return z; }, cur, 0);
+                weigh(cur, 1);                     // the wave's last keys
+                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+            }
+            if (!more) break;
+            old = cur;
+            cur = ahead;
+            at = ahead_at;
+            mine = mine_next;
+            {
+                const float sk2 = sk, sv2 = sv;
+                sk = sk1;
+                sv = sv1;
+                scales();
+                sk = sk2;
+                sv = sv2;
+            }
         }
     }
     l += __shfl_xor(l, 32);
     if (!live) return;
     const size_t out_row = (size_t)(s.r0 + t);
-    if (p.splits > 1) {
-        const size_t at = (size_t)split * ((size_t)p.T * p.Hq) + out_row * p.Hq + head;
-        if (half == 0) p.part_ml[at] = make_float2(m, l);
-        float* d = p.part_o + at * D;
+    if (split >= 0) {
+        const size_t to = ((size_t)split * rest + (unit - p.whole)) * kRows +
+                          (row - tile_row * kRows);
+        if (half == 0) p.part_ml[to] = make_float2(m, l);
+        float* d = p.part_o + to * D;
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt)
 #pragma unroll
@@ -511,10 +655,6 @@ attention_tile_kernel(const Problem p) {
 // 0..7), the 16 bytes of a V row two steps of 32 tokens (16 g + 8 e + 0..7), and the key at row
 // r of score tile (e, a) is 16 (r / 4) + 8 e + 4 a + r % 4, so that the scores of tiles (e, 0)
 // and (e, 1) are the operand of step e.
-// The running maximum is raised only where a score passes it by more than 2^6 (P has room for
-// it): most pages then need no exchange between lanes and no rescaling.
-constexpr float kLazy = 6.0f;
-
 typedef float f32x4_acc __attribute__((ext_vector_type(4)));
 typedef int i32x4_acc __attribute__((ext_vector_type(4)));
 
@@ -558,6 +698,8 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+constexpr int kFewRows = 16;
+
 template <int D, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2)
 attention_few_kernel(const Problem p) {
@@ -566,10 +708,11 @@ attention_few_kernel(const Problem p) {
     __shared__ float lo[WAVES][16][D + 4];
     __shared__ float lm[WAVES][16], ll[WAVES][16];
 
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int unit = quotient(blockIdx.x, p.pieces), split = blockIdx.x - unit * p.pieces;
+    const int b = quotient(unit, p.Hkv), h = unit - b * p.Hkv;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    const int tile0 = split * p.split_tiles;
+    const int tile0 = split * p.piece_tiles;
     // the wave's tiles are tile0 + wave + i * WAVES; the page numbers of 64 of them, one a lane
     const int32_t* table = p.page_table + (size_t)b * p.max_pages;
     auto page_numbers = [&](int i) {
@@ -578,7 +721,7 @@ attention_few_kernel(const Problem p) {
     };
     int numbers = page_numbers(0);                 // needs no length: on its way beside them
     const Sequence s = sequence<true>(p, b);
-    const int G = p.Hq / p.Hkv;
+    const int G = quotient(p.Hq, p.Hkv);
     const int rows = min(s.n, p.max_rows) * G;     // at most 16
     if (rows <= 0) return;
     const bool live = col < rows;
@@ -588,8 +731,8 @@ attention_few_kernel(const Problem p) {
     const int last_t = (rows - 1) / G;
     const int least = p.causal ? min(max(s.kv - s.n + 1, 0), s.kv) : s.kv;
     const int most = p.causal ? min(max(s.kv - s.n + last_t + 1, 0), s.kv) : s.kv;
-    const int tile1 = min((most + kPage - 1) / kPage, tile0 + p.split_tiles);
-    if (p.splits > 1 && tile0 * kPage >= s.kv) return;     // the join does not read this piece
+    const int tile1 = min((most + kPage - 1) / kPage, tile0 + p.piece_tiles);
+    if (p.pieces > 1 && tile0 * kPage >= s.kv) return;     // the join does not read this piece
 
     const size_t block = (size_t)(2 * kPage * D);
     const uint32_t k_lane = (uint32_t)((col >> 2) * 16 + (col & 3)) * D + g * 16;
@@ -777,8 +920,8 @@ attention_few_kernel(const Problem p) {
         }
         const size_t row = (size_t)(s.r0 + r / G);
         const int hd = h * G + r % G;
-        if (p.splits > 1) {
-            const size_t to = (size_t)split * ((size_t)p.T * p.Hq) + row * p.Hq + hd;
+        if (p.pieces > 1) {
+            const size_t to = ((size_t)split * p.units + unit) * kFewRows + r;
             if (d == 0) p.part_ml[to] = make_float2(best, total);
             *reinterpret_cast<float4*>(p.part_o + to * D + d) = a;
         } else {
@@ -789,18 +932,19 @@ attention_few_kernel(const Problem p) {
     }
 }
 
-// Joins the pieces of the key axis in their order: one wave a (token, head) row.
+// Joins the pieces of the split units in their order: one wave a row.  unit_rows: rows of a unit.
 template <int D, bool CACHE>
-__global__ void __launch_bounds__(256) attention_join_kernel(const Problem p) {
-    const int b = blockIdx.y, lane = threadIdx.x & 63;
-    const Sequence s = sequence<CACHE>(p, b);
-    const int idx = blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int t = idx / p.Hq, head = idx % p.Hq;
-    if (t >= min(s.n, p.max_rows)) return;
-    const size_t stride = (size_t)p.T * p.Hq;
-    const size_t at = (size_t)(s.r0 + t) * p.Hq + head;
-    const int used = min(p.splits, ((s.kv + kPage - 1) / kPage + p.split_tiles - 1) /
-                                       p.split_tiles);
+__global__ void __launch_bounds__(256) attention_join_kernel(const Problem p, int unit_rows) {
+    const int lane = threadIdx.x & 63, rest = p.units - p.whole;
+    const Place u = place(p, p.whole + blockIdx.y);
+    const Sequence s = sequence<CACHE>(p, u.b);
+    const int G = p.Hq / p.Hkv, r = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int row = u.tile * unit_rows + r;
+    if (r >= unit_rows || row >= min(s.n, p.max_rows) * G) return;
+    const int t = row / G, head = u.h * G + row % G;
+    const size_t stride = (size_t)rest * unit_rows, at = (size_t)blockIdx.y * unit_rows + r;
+    const int used = min(p.pieces, ((s.kv + kPage - 1) / kPage + p.piece_tiles - 1) /
+                                       p.piece_tiles);
     // the pieces' maxima and sums, 64 at a time, one a lane
     float m = -INFINITY, l = 0.0f, o[D / 64];
 #pragma unroll
@@ -839,85 +983,107 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const Problem p) {
         *d = (uint16_t)(pack_bf16(o[0] * f, 0.0f) & 0xFFFFu);
 }
 
-// Pieces of the key axis, `tiles` tiles each.
-struct Split {
-    int splits, tiles;
+// How a call's work is laid out (Problem's fields of the same names).
+struct Plan {
+    int waves;          // of a workgroup; 0: the kernel for few rows
+    int unit_rows, tile_rows, units, whole, pieces, piece_tiles;
+    size_t part_rows() const {
+        return pieces > 1 ? (size_t)pieces * (units - whole) * unit_rows : 0;
+    }
 };
-Split pieces(int64_t wanted, int tiles, int least) {
-    const int most = (tiles + least - 1) / least;
-    const int splits = (int)(wanted < most ? wanted : most);
-    if (splits <= 1) return {1, tiles > 0 ? tiles : 1};
-    const int each = (tiles + splits - 1) / splits;
-    return {(tiles + each - 1) / each, each};
-}
 
-constexpr int kFewRows = 16;
 constexpr int kFewWaves = 4;
 
-bool few_rows(int max_rows, int Hq, int Hkv) {
-    return (int64_t)max_rows * (Hq / Hkv) <= kFewRows;
+int tile_waves(int64_t rows) { const char* e = getenv("TW"); return e ? atoi(e) : rows > 128 ? 8 : 4; }
+
+// Pieces of at least `least` tiles, `wanted` of them where the tiles suffice.
+void split(Plan& p, int64_t wanted, int tiles, int least) {
+    const int most = (tiles + least - 1) / least;
+    const int n = (int)(wanted < most ? wanted : most);
+    p.piece_tiles = tiles > 0 ? tiles : 1;
+    p.pieces = 1;
+    if (n <= 1) return;
+    p.piece_tiles = (tiles + n - 1) / n;
+    p.pieces = (tiles + p.piece_tiles - 1) / p.piece_tiles;
 }
 
 // Enough workgroups for the 256 compute units where sequences, heads and query rows give fewer.
 // Few rows, measured with 16 heads of 128 channels, one sequence (us, pieces a head in brackets):
-// 512 tokens 8.9 [1]; 777 tokens 12.2 [1], 10.6 [4]; 4096 tokens 17.8 [4], 14.1 [16]; 16384 tokens 23.3
-// [16], 26 [32]; 65536 tokens 56 [32], 65 [64].  A single unit draws about 50 GB/s, so that up to
-// 4096 tiles one workgroup a unit is best and above two; from 256 (sequence, head) pairs on, ragged
-// lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135 [2]).
-Split plan(bool cache, int B, int max_rows, int max_kv, int Hq, int Hkv, int D) {
+// 512 tokens 8.9 [1]; 777 tokens 12.2 [1], 10.6 [4]; 4096 tokens 17.8 [4], 14.1 [16]; 16384 tokens
+// 23.3 [16], 26 [32]; 65536 tokens 56 [32], 65 [64].  A single unit draws about 50 GB/s, so that up
+// to 4096 tiles one workgroup a unit is best and above two; from 256 (sequence, head) pairs on,
+// ragged lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135 [2]).
+// False for more workgroups than a launch takes.
+bool plan(bool cache, int B, int max_rows, int max_kv, int Hq, int Hkv, int D, Plan& p) {
     const int tiles = (int)(((int64_t)max_kv + kPage - 1) / kPage);
-    if (cache && few_rows(max_rows, Hq, Hkv)) {
-        const int64_t groups = (int64_t)B * Hkv;
-        const int64_t total = groups * tiles;
-        if (tiles * D <= 8 * 128) return {1, tiles > 0 ? tiles : 1};
-        const int64_t want = groups >= 256 ? 1024 : total <= 4096 ? 256 : 512;
-        return pieces((want + groups - 1) / groups, tiles, kFewWaves);
+    const int64_t rows = (int64_t)max_rows * (Hq / Hkv), pairs = (int64_t)B * Hkv;
+    p.whole = 0;
+    if (cache && rows <= kFewRows) {
+        p.waves = 0;
+        p.unit_rows = kFewRows;
+        p.tile_rows = 1;
+        p.units = (int)pairs;
+        const int64_t want = pairs >= 256 ? 1024 : pairs * tiles <= 4096 ? 256 : 512;
+        split(p, tiles * D <= 8 * 128 ? 1 : (want + pairs - 1) / pairs, tiles, kFewWaves);
+        return pairs * p.pieces <= (1 << 22);
     }
-    const int64_t groups =
-        ((int64_t)max_rows * (Hq / Hkv) + kRows - 1) / kRows * Hkv * (int64_t)B;
-    if (groups >= 512) return {1, tiles > 0 ? tiles : 1};
-    return pieces((512 + groups - 1) / (groups > 0 ? groups : 1), tiles, 4);
+    p.waves = tile_waves(rows);
+    p.unit_rows = kWaveRows * p.waves;
+    const int64_t tile_rows = (rows + p.unit_rows - 1) / p.unit_rows, units = tile_rows * pairs;
+    if (units > (1 << 21)) return false;
+    p.tile_rows = (int)tile_rows;
+    p.units = (int)units;
+    // a round is what runs at once; what is left over after whole rounds is split into one more
+    const int round = p.waves == 8 ? 256 : 512, rest = p.units % round;
+    const char* ns = getenv("NS"); const int NS = ns ? atoi(ns) : 99;
+    split(p, rest > 0 && rest <= round / 2 ? (round / rest < NS ? round / rest : NS) : 1, tiles, p.units < round ? 4 : 2);
+    p.whole = p.pieces > 1 ? p.units - rest : p.units;
+    return true;
 }
 
 template <int D, bool CACHE>
-hipError_t launch(Problem p, int B, void* workspace, hipStream_t stream) {
-    const Split sp = plan(CACHE, B, p.max_rows, p.max_kv, p.Hq, p.Hkv, D);
-    p.splits = sp.splits;
-    p.split_tiles = sp.tiles;
+hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
+    Plan sp;
+    if (!plan(CACHE, p.B, p.max_rows, p.max_kv, p.Hq, p.Hkv, D, sp)) return hipErrorInvalidValue;
+    p.tile_rows = sp.tile_rows;
+    p.units = sp.units;
+    p.whole = sp.whole;
+    p.pieces = sp.pieces;
+    p.piece_tiles = sp.piece_tiles;
+    p.last_first = p.causal ? 1 : 0;
+    p.most_tiles = (int)(((int64_t)p.max_kv + kPage - 1) / kPage);
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)sp.splits * p.T * p.Hq * D);
-    bool few = false;
-    if constexpr (CACHE) {
-        few = few_rows(p.max_rows, p.Hq, p.Hkv);
-        if (few && sp.splits == 1)
-            attention_few_kernel<D, 8><<<dim3(1, p.Hkv, B), 512, 0, stream>>>(p);
-        else if (few)
-            attention_few_kernel<D, kFewWaves>
-                <<<dim3(sp.splits, p.Hkv, B), kFewWaves * 64, 0, stream>>>(p);
-    }
-    if (!few) {
-        const int64_t tiles = ((int64_t)p.max_rows * (p.Hq / p.Hkv) + kRows - 1) / kRows;
-        attention_tile_kernel<D, CACHE>
-            <<<dim3((unsigned)(tiles * sp.splits), p.Hkv, B), kThreads, 0, stream>>>(p);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + sp.part_rows() * D);
+    const unsigned grid = (unsigned)(p.whole + (p.units - p.whole) * p.pieces);
+    if (sp.waves == 0) {
+        if constexpr (CACHE) {
+            if (p.pieces == 1)
+                attention_few_kernel<D, 8><<<grid, 512, 0, stream>>>(p);
+            else
+                attention_few_kernel<D, kFewWaves><<<grid, kFewWaves * 64, 0, stream>>>(p);
+        }
+    } else if (sp.waves == 8) {
+        attention_tile_kernel<D, CACHE, 8><<<grid, 512, 0, stream>>>(p);
+    } else {
+        attention_tile_kernel<D, CACHE, 4><<<grid, 256, 0, stream>>>(p);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || sp.splits == 1) return e;
+    if (e != hipSuccess || p.pieces == 1) return e;
+    const int64_t rows = (int64_t)p.max_rows * (p.Hq / p.Hkv);
+    const unsigned most = (unsigned)(rows < sp.unit_rows ? rows : sp.unit_rows);
     attention_join_kernel<D, CACHE>
-        <<<dim3((unsigned)(((int64_t)p.max_rows * p.Hq + 3) / 4), B), 256, 0, stream>>>(p);
+        <<<dim3((most + 3) / 4, p.units - p.whole), 256, 0, stream>>>(p, sp.unit_rows);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D) {
-    // one size for both calls
-    int splits = 1;
-    for (const bool cache : {false, true}) {
-        const Split sp = plan(cache, B, max_rows < T ? max_rows : T, max_kv, Hq, Hkv, D);
-        splits = splits > sp.splits ? splits : sp.splits;
-    }
-    if (splits == 1) return 0;
-    return (size_t)splits * (size_t)T * (size_t)Hq * (size_t)(D + 2) * sizeof(float);
+bool attention_workspace(bool cache, int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D,
+                         size_t& bytes) {
+    Plan p;
+    if (!plan(cache, B, max_rows < T ? max_rows : T, max_kv, Hq, Hkv, D, p)) return false;
+    bytes = p.part_rows() * (size_t)(D + 2) * sizeof(float);
+    return true;
 }
 
 hipError_t launch_cache_attention(const uint16_t* Q, const int32_t* row_start,
@@ -936,6 +1102,7 @@ hipError_t launch_cache_attention(const uint16_t* Q, const int32_t* row_start,
     p.scales = scales;
     p.max_pages = max_pages;
     p.num_pages = num_pages;
+    p.B = B;
     p.T = T;
     p.max_rows = max_rows;
     p.max_kv = max_kv;
@@ -946,8 +1113,8 @@ hipError_t launch_cache_attention(const uint16_t* Q, const int32_t* row_start,
     p.ldo = ldo;
     p.sm = sm;
     p.O = O;
-    return D == 64 ? launch<64, true>(p, B, workspace, stream)
-                   : launch<128, true>(p, B, workspace, stream);
+    return D == 64 ? launch<64, true>(p, workspace, stream)
+                   : launch<128, true>(p, workspace, stream);
 }
 
 hipError_t launch_cross_attention(const uint16_t* Q, const uint16_t* K, const uint16_t* V,
@@ -964,6 +1131,7 @@ hipError_t launch_cross_attention(const uint16_t* Q, const uint16_t* K, const ui
     p.row_start = row_start;
     p.kv_start = kv_start;
     p.kv_len = kv_len;
+    p.B = B;
     p.T = T;
     p.Tkv = Tkv;
     p.max_rows = max_rows;
@@ -976,8 +1144,8 @@ hipError_t launch_cross_attention(const uint16_t* Q, const uint16_t* K, const ui
     p.ldo = ldo;
     p.sm = sm;
     p.O = O;
-    return D == 64 ? launch<64, false>(p, B, workspace, stream)
-                   : launch<128, false>(p, B, workspace, stream);
+    return D == 64 ? launch<64, false>(p, workspace, stream)
+                   : launch<128, false>(p, workspace, stream);
 }
 
 }  // namespace rudder

@@ -396,7 +396,7 @@ rudder_status_t check_ld(const char* f, const char* name, int ld, int heads, int
     return RUDDER_OK;
 }
 
-rudder_status_t check_attention(const char* f, const void* Q, const void* O,
+rudder_status_t check_attention(const char* f, bool cache, const void* Q, const void* O,
                                 const void* workspace, size_t workspace_bytes, int B, int T,
                                 int max_rows, int max_kv, int Hq, int Hkv, int D, int ldq,
                                 int ldo, float sm) {
@@ -415,10 +415,17 @@ rudder_status_t check_attention(const char* f, const void* Q, const void* O,
         return fail(RUDDER_ERR_INVALID_ARG, "%s: Q, O and workspace must be 16-byte aligned", f);
     if (B > kMaxSequences)
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d exceeds %d", f, B, kMaxSequences);
+    if ((int64_t)B * Hkv > kMaxSequences)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d with Hkv=%d exceeds %d", f, B, Hkv,
+                    kMaxSequences);
     if ((int64_t)max_rows * Hq > (1 << 26))
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d with Hq=%d exceeds 2^26 rows", f,
                     max_rows, Hq);
-    const size_t need = rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D);
+    if (B == 0 || T == 0 || max_rows == 0) return RUDDER_OK;
+    size_t need = 0;
+    if (!rudder::attention_workspace(cache, B, T, max_rows, max_kv, Hq, Hkv, D, need))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d sequences of max_rows=%d rows exceed a launch",
+                    f, B, max_rows);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(RUDDER_ERR_INVALID_ARG, "%s: these sizes need a workspace of %zu bytes, not "
                     "%zu", f, need, workspace ? workspace_bytes : (size_t)0);
@@ -485,10 +492,15 @@ rudder_status_t rudder_cache_dequant(const int8_t* codes, const float* scales,
 size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
                                         int D) {
     if (B <= 0 || T <= 0 || max_rows <= 0 || max_kv < 0 || Hkv <= 0 || Hkv > kMaxCacheHeads ||
-        Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || B > kMaxSequences ||
+        Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || (int64_t)B * Hkv > kMaxSequences ||
         (int64_t)max_rows * Hq > (1 << 26))
         return 0;
-    return rudder::attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv, D);
+    // one size for both calls
+    size_t bytes = 0, most = 0;
+    for (const bool cache : {false, true})
+        if (rudder::attention_workspace(cache, B, T, max_rows, max_kv, Hq, Hkv, D, bytes))
+            most = most > bytes ? most : bytes;
+    return most;
 }
 
 rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_start,
@@ -504,7 +516,7 @@ rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_sta
     if (max_pages <= 0 || num_pages <= 0)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: max_pages=%d and num_pages=%d must be positive",
                     f, max_pages, num_pages);
-    const rudder_status_t st = check_attention(f, Q, O, workspace, workspace_bytes, B, T,
+    const rudder_status_t st = check_attention(f, true, Q, O, workspace, workspace_bytes, B, T,
                                                max_rows, max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if (misaligned(codes))
@@ -528,7 +540,7 @@ rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, con
     if (!Q || !K || !V || !row_start || !kv_start || !kv_len || !O)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
     if (Tkv < 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Tkv=%d must be >= 0", f, Tkv);
-    rudder_status_t st = check_attention(f, Q, O, workspace, workspace_bytes, B, T, max_rows,
+    rudder_status_t st = check_attention(f, false, Q, O, workspace, workspace_bytes, B, T, max_rows,
                                          max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
