@@ -156,9 +156,9 @@ def visible(n, kv, causal):
     return (j <= kv - n + i) if causal else torch.ones(n, kv, dtype=torch.bool)
 
 
-def cache_attention(q, row_start, kv_len, table, codes, scales, sm, causal):
+def cache_attention(q, row_start, kv_len, table, codes, scales, sm, causal, heads=None):
     """O and bound [T, Hq, D] in 64 bits (zeros in rows of no sequence); pages outside the pool
-    are not visible."""
+    are not visible.  `heads`: those that are computed, all by default."""
     T, Hq, D = q.shape
     P, H = codes.shape[:2]
     o = torch.zeros(T, Hq, D, dtype=torch.float64)
@@ -171,7 +171,7 @@ def cache_attention(q, row_start, kv_len, table, codes, scales, sm, causal):
         k, v = values(codes, scales, torch.where(good, pages, 0))
         there = good.repeat_interleave(PAGE)[:kv]
         vis = visible(r1 - r0, kv, causal) & there[None, :]
-        for h in range(Hq):
+        for h in range(Hq) if heads is None else heads:
             g = h // (Hq // H)
             kk = torch.where(there[:, None], k[:, g].reshape(-1, D)[:kv], 0.0)
             vv = torch.where(there[:, None], v[:, g].reshape(-1, D)[:kv], 0.0)
@@ -180,7 +180,7 @@ def cache_attention(q, row_start, kv_len, table, codes, scales, sm, causal):
     return o, e
 
 
-def cross_attention(q, k, v, row_start, kv_start, kv_len, sm):
+def cross_attention(q, k, v, row_start, kv_start, kv_len, sm, heads=None):
     T, Hq, D = q.shape
     H = k.shape[1]
     o = torch.zeros(T, Hq, D, dtype=torch.float64)
@@ -189,7 +189,7 @@ def cross_attention(q, k, v, row_start, kv_start, kv_len, sm):
         r0, r1 = int(row_start[b]), int(row_start[b + 1])
         k0, n = int(kv_start[b]), int(kv_len[b])
         vis = torch.ones(r1 - r0, n, dtype=torch.bool)
-        for h in range(Hq):
+        for h in range(Hq) if heads is None else heads:
             g = h // (Hq // H)
             o[r0:r1, h], e[r0:r1, h] = rows_attention(
                 q[r0:r1, h].double(), k[k0:k0 + n, g].double(), v[k0:k0 + n, g].double(), vis, sm,

@@ -84,6 +84,93 @@ def test_cache_attention(rudder, counts, lens, Hq, Hkv, D, causal):
     ref.assert_within("O", got, want, bound)
 
 
+# Row tiles left over after whole rounds of workgroups are split over the tokens, rows of 256 go
+# to a workgroup where all see long stretches: every head takes part, a few are compared.
+LARGE_CASES = [
+    # counts, lens, Hq, Hkv, D, causal, heads
+    ([300, 41], [1100, 1030], 4, 2, 128, False, [0, 3]),       # 256 rows a workgroup
+    ([1100, 700], [1025, 1500], 32, 32, 128, False, [0, 17, 31]),
+    ([700], [1400], 96, 96, 64, True, [0, 1, 50, 95]),
+    ([257, 513], [1100, 1600], 96, 48, 128, True, [0, 95]),
+]
+
+
+@pytest.mark.parametrize("counts,lens,Hq,Hkv,D,causal,heads", LARGE_CASES)
+def test_cache_attention_large(rudder, counts, lens, Hq, Hkv, D, causal, heads):
+    log(f"case large {counts} {lens} Hq={Hq} Hkv={Hkv} D={D} causal={causal}")
+    g = torch.Generator().manual_seed(31)
+    codes, scales, table = _cache(g, lens, Hkv, D)
+    starts = _starts(counts)
+    q = (torch.randn(int(starts[-1]), Hq, D, generator=g) * 2).to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, causal, heads)
+    got = _run_cache(rudder, q, starts, lens, table, codes, scales, sm, causal)
+    ref.assert_within("O", got[:, heads], want[:, heads], bound[:, heads])
+
+
+@pytest.mark.parametrize("counts,lens,Hq,Hkv,D,heads", [
+    ([300, 41], [1100, 1030], 4, 2, 128, [0, 3]),
+    ([1100, 700], [1025, 1500], 32, 32, 128, [0, 31]),
+    ([700], [1400], 96, 96, 64, [0, 95]),
+])
+def test_cross_attention_large(rudder, counts, lens, Hq, Hkv, D, heads):
+    log(f"case cross large {counts} {lens} Hq={Hq} Hkv={Hkv} D={D}")
+    g = torch.Generator().manual_seed(32)
+    starts, kv_start = _starts(counts), _starts(lens)[:-1]
+    q = (torch.randn(int(starts[-1]), Hq, D, generator=g) * 2).to(torch.bfloat16)
+    kv = torch.randn(sum(lens), 2 * Hkv, D, generator=g).to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    want, bound = ref.cross_attention(q, kv[:, :Hkv], kv[:, Hkv:], starts, kv_start, lens, sm,
+                                      heads)
+    dev = kv.cuda()
+    got = rudder.cross_attention(q.cuda(), dev[:, :Hkv], dev[:, Hkv:], starts.cuda(),
+                                 kv_start.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                 max(counts), max(lens), sm)
+    ref.assert_within("O", got[:, heads], want[:, heads], bound[:, heads])
+
+
+@pytest.mark.parametrize("rows,ctx", [(3, 90), (3, 3000), (150, 300), (300, 1200)])
+def test_rows_that_are_not_finite(rudder, rows, ctx):
+    """A query row with a NaN, an infinity of either sign or both gives NaN in its row and head
+    and leaves the others, in every kernel; a negative softmax scale."""
+    log(f"case not finite rows={rows} ctx={ctx}")
+    g = torch.Generator().manual_seed(33)
+    Hq, Hkv, D = 2, 1, 128
+    codes, scales, table = _cache(g, [ctx], Hkv, D)
+    q = torch.randn(rows, Hq, D, generator=g).to(torch.bfloat16)
+    clean = q.clone()
+    bad = [(0, 0, float("nan")), (1, 1, float("inf")), (2, 0, -float("inf"))]
+    for r, h, v in bad:
+        q[r, h, 7 * r] = v
+    starts = _starts([rows])
+    for causal in (False, True):
+        want, bound = ref.cache_attention(clean, starts, [ctx], table, codes, scales, -0.1, causal)
+        got = _run_cache(rudder, q, starts, [ctx], table, codes, scales, -0.1, causal).cpu()
+        for r, h, _ in bad:
+            assert torch.isnan(got[r, h]).all(), (r, h)
+            got[r, h], want[r, h], bound[r, h] = 0.0, 0.0, 0.0
+        ref.assert_within("O", got, want, bound)
+
+
+def test_long_tables(rudder):
+    """More than 64 pages a wave and more than 64 pieces' worth of tiles: page numbers are
+    fetched anew."""
+    log("case long tables")
+    g = torch.Generator().manual_seed(34)
+    D, ctx = 64, 64 * 700 + 5
+    codes, scales, table = _cache(g, [ctx], 1, D)
+    table[0, 600] = -1
+    for rows, B in ((1, 1), (1, 300), (20, 1), (140, 60)):
+        # many sequences leave one piece to each, so that a wave walks all of the table
+        q = torch.randn(B * rows, 1, D, generator=g).to(torch.bfloat16)
+        starts = (torch.arange(B + 1) * rows).to(torch.int32)
+        two = starts[:2]
+        want, bound = ref.cache_attention(q[:rows], two, [ctx], table, codes, scales, 0.1, False)
+        got = _run_cache(rudder, q, starts, [ctx] * B, table.expand(B, -1).contiguous(), codes,
+                         scales, 0.1, False)
+        ref.assert_within(f"O rows={rows} B={B}", got[:rows], want, bound)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("counts,lens", [([1, 1], [500, 1000]), ([70], [400])])
 def test_scales_of_all_sizes(rudder, D, counts, lens):

@@ -1,0 +1,216 @@
+"""The operators as a block uses them: QKV linear, append, attention over the
+cache, cross attention and O linear; single tokens through the few-row
+products; the same calls captured in a graph, on two streams and with a
+shared buffer of rows."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+from gpu_harness import log
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module")
+def rudder():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    from w4a4_quantized_gemm_rudder_amd import rudder as r
+    r.load_library()
+    return r
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def _block(rudder, M, H, D, seed):
+    """QKV and O layers (W4A8), their inputs and an empty cache for two sequences."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    K, N = 256, 3 * H * D
+    X = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn(K, N, generator=g, device="cuda") * 0.06).to(torch.bfloat16)
+    Wo = (torch.randn(H * D, K, generator=g, device="cuda") * 0.06).to(torch.bfloat16)
+    one = {n: torch.ones(n, device="cuda") for n in (K, H * D)}
+    qkv = rudder.quantize_weights(W, one[K])
+    out = rudder.quantize_weights(Wo, one[H * D])
+    sid = torch.zeros(M, dtype=torch.uint8, device="cuda")
+    comp = {n: (torch.ones(1, n, device="cuda"), torch.zeros(1, n, device="cuda"))
+            for n in (K, N)}
+    return X, qkv, out, sid, comp, K, N, W, Wo
+
+
+def test_block_step(rudder):
+    """Two sequences of 40 and 1 new rows behind 100 and 63 cached ones: each stage against its
+    64-bit form on the previous stage's GPU output, and O against the bf16 chain."""
+    H, D, counts, before = 2, 64, [40, 1], [100, 63]
+    log("case block step")
+    M, B = sum(counts), 2
+    X, qkv, out, sid, comp, K, N, W, Wo = _block(rudder, M, H, D, 51)
+    g = torch.Generator().manual_seed(52)
+    codes = torch.randint(-127, 128, (8, H, 2, PAGE * D), generator=g).to(torch.int8)
+    scales = torch.rand(8, H, 2, generator=g) * 0.01
+    table = torch.tensor([[5, 2, 7], [1, 0, -1]], dtype=torch.int32)
+    starts, pos = _i32([0, 40, 41]), _i32(before)
+    kv_len = _i32([b + c for b, c in zip(before, counts)])
+    xq, rs = rudder.quant_act(X, sid, qkv[2], None, 1, 8)
+    Y = rudder.linear(xq, rs, sid, qkv[0], qkv[1], *comp[N], M, N, K, 1, 8)
+    rows = Y.view(M, 3 * H, D)
+    dc, ds = codes.cuda(), scales.cuda()
+    rudder.cache_append(rows[:, H:2 * H], rows[:, 2 * H:], starts.cuda(), pos.cuda(),
+                        table.cuda(), max(counts), dc, ds)
+    O = rudder.cache_attention(rows[:, :H], starts.cuda(), kv_len.cuda(), table.cuda(), dc, ds,
+                               max(counts), int(kv_len.max()), 1 / math.sqrt(D), True)
+    oq, ors = rudder.quant_act(O.view(M, H * D), sid, out[2], None, 1, 8)
+    Z = rudder.linear(oq, ors, sid, out[0], out[1], *comp[K], M, K, H * D, 1, 8)
+
+    host = rows.cpu()
+    ref.append(host[:, H:2 * H], host[:, 2 * H:], starts, pos, table, codes, scales)
+    assert torch.equal(dc.cpu(), codes) and torch.equal(ds.cpu(), scales)
+    want, bound = ref.cache_attention(host[:, :H], starts, kv_len, table, codes, scales,
+                                      1 / math.sqrt(D), True)
+    ref.assert_within("O", O, want, bound)
+    # W4A8 against the unquantized product: int4 weights of N(0, s) within half a step of
+    # absmax / 7 (about 4 s / 7 / 2 each, uniform: rms 0.16 s), 8-bit rows within 1 / 254
+    full = O.view(M, -1).double() @ Wo.double()
+    err = (Z.double() - full).norm() / full.norm()
+    assert err < 0.25, float(err)
+
+
+def test_single_token_chain(rudder):
+    """One token through group-scaled QKV, append, attention and group-scaled O, step by step
+    for 70 tokens (over a page's end): the last outputs against the 64-bit chain on the
+    library's own cache."""
+    log("case single token chain")
+    H, D, K, group = 2, 64, 128, 64
+    g = torch.Generator().manual_seed(53)
+    W = (torch.randn(K, 3 * H * D, generator=g) * 0.1).to(torch.bfloat16)
+    Wo = (torch.randn(H * D, K, generator=g) * 0.1).to(torch.bfloat16)
+    wq, wo = (rudder.quantize_weights_grouped(w.cuda(), group) for w in (W, Wo))
+    codes, scales = rudder.new_cache(3, H, D)
+    table = _i32([[2, 0]]).cuda()
+    starts = _i32([0, 1]).cuda()
+    x = torch.randn(70, K, generator=g).to(torch.bfloat16)
+    for t in range(70):
+        xt = x[t:t + 1].cuda()
+        y = rudder.matvec_w4(xt, *wq, 3 * H * D, group).view(1, 3 * H, D)
+        rudder.cache_append(y[:, H:2 * H], y[:, 2 * H:], starts, _i32([t]).cuda(), table, 1,
+                            codes, scales)
+        o = rudder.cache_attention(y[:, :H], starts, _i32([t + 1]).cuda(), table, codes, scales,
+                                   1, 128, 0.125)
+        z = rudder.matvec_w4(o.view(1, H * D), *wo, K, group)
+    q, s = ref.group_codes(W, group)
+    want, bound = ref.matvec(x[69:], q, s, group)
+    ref.assert_within("QKV", y.view(1, -1), want, bound)
+    want, bound = ref.cache_attention(y[:, :H].cpu(), [0, 1], [70], table.cpu(), codes.cpu(),
+                                      scales.cpu(), 0.125, True)
+    ref.assert_within("O", o, want, bound)
+    q, s = ref.group_codes(Wo, group)
+    want, bound = ref.matvec(o.view(1, -1).cpu(), q, s, group)
+    ref.assert_within("Z", z, want, bound)
+
+
+def _graph_case(rudder, rows, ctx, H=2, Hq=4, D=128, B=2):
+    """A decode or chunk step with preallocated buffers: (run, outputs)."""
+    g = torch.Generator(device="cuda").manual_seed(60 + rows)
+    pages = (ctx + rows + PAGE) // PAGE + 1
+    codes, scales = rudder.new_cache(B * pages, H, D)
+    codes.random_(-127, 128, generator=g)
+    scales.uniform_(0.005, 0.01, generator=g)
+    table = torch.randperm(B * pages, generator=g, device="cuda").view(B, pages).to(torch.int32)
+    starts = (torch.arange(B + 1) * rows).to(torch.int32).cuda()
+    pos = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+    kv_len = pos + rows
+    T = B * rows
+    buf = torch.randn(T, Hq + 2 * H, D, generator=g, device="cuda").to(torch.bfloat16)
+    group, K = 64, Hq * D
+    W = (torch.randn(K, 256, generator=g, device="cuda") * 0.05).to(torch.bfloat16)
+    Wq, gs = rudder.quantize_weights_grouped(W, group)
+    n = rudder.attention_workspace_bytes(B, T, rows, ctx + rows, Hq, H, D)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    O = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    C = torch.zeros_like(O)
+    Y = torch.zeros(T, 256, dtype=torch.bfloat16, device="cuda")
+    L = 77
+    enc = torch.randn(B * L, 2 * H, D, generator=g, device="cuda").to(torch.bfloat16)
+    kv_start = (torch.arange(B) * L).to(torch.int32).cuda()
+    enc_len = _i32([L, 30]).cuda()
+    ws2 = torch.empty(max(16, rudder.attention_workspace_bytes(B, T, rows, L, Hq, H, D)),
+                      dtype=torch.uint8, device="cuda")
+
+    def run():
+        rudder.rudder_cache_append(buf[:, Hq:Hq + H], buf[:, Hq + H:], starts, pos, table, B, T,
+                                   rows, pages, B * pages, H, D, codes, scales)
+        rudder.rudder_cache_attention(buf[:, :Hq], starts, kv_len, table, codes, scales, B, T,
+                                      rows, ctx + rows, pages, B * pages, Hq, H, D, 0.09, True,
+                                      ws, O)
+        rudder.rudder_cross_attention(O, enc[:, :H], enc[:, H:], starts, kv_start, enc_len, B, T,
+                                      B * L, rows, L, Hq, H, D, 0.09, ws2, C)
+        rudder.rudder_matvec_w4(C.view(T, -1), None, Wq, gs, None, None, T, 256, K, group, 1, Y)
+
+    return run, [codes, scales, O, C, Y]
+
+
+@pytest.mark.parametrize("rows,ctx", [(1, 500), (1, 5000), (60, 300)])
+def test_graph_replays(rudder, rows, ctx):
+    """The captured step replayed three times, with eager work between, equals the eager run
+    bit for bit (an append again at the same place changes nothing)."""
+    log(f"case graph rows={rows} ctx={ctx}")
+    run, outputs = _graph_case(rudder, rows, ctx)
+    run()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outputs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    scratch = torch.randn(512, 512, device="cuda")
+    for rep in range(3):
+        for o in outputs[2:]:
+            o.fill_(9.0)
+        (scratch @ scratch).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (o, w) in enumerate(zip(outputs, want)):
+            assert torch.equal(o.view(torch.uint8), w.view(torch.uint8)), (rep, i)
+
+
+def test_two_streams(rudder):
+    """Two steps with buffers of their own on two streams at a time equal the same steps alone."""
+    log("case two streams")
+    cases = [_graph_case(rudder, 1, 6000), _graph_case(rudder, 7, 3000)]
+    wants = []
+    for run, outputs in cases:
+        run()
+        torch.cuda.synchronize()
+        wants.append([o.clone() for o in outputs])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (run, _o), st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                run()
+    torch.cuda.synchronize()
+    for (run, outputs), want in zip(cases, wants):
+        for o, w in zip(outputs, want):
+            assert torch.equal(o.view(torch.uint8), w.view(torch.uint8))
+
+
+def test_conveniences_on_a_given_stream(rudder):
+    """The allocating forms on a stream that is not the current one."""
+    log("case given stream")
+    g = torch.Generator(device="cuda").manual_seed(70)
+    H, D, ctx = 2, 64, 4000
+    codes, scales = rudder.new_cache(ctx // PAGE + 1, H, D)
+    codes.random_(-127, 128, generator=g)
+    scales.fill_(0.01)
+    table = torch.arange(ctx // PAGE + 1, dtype=torch.int32, device="cuda").view(1, -1)
+    q = torch.randn(1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    args = (q, _i32([0, 1]).cuda(), _i32([ctx]).cuda(), table, codes, scales, 1, ctx, 0.1)
+    want = rudder.cache_attention(*args)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for stream in (st, st.cuda_stream):
+        got = rudder.cache_attention(*args, stream=stream)
+        st.synchronize()
+        assert torch.equal(got, want)

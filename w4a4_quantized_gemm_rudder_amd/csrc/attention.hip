@@ -26,7 +26,6 @@
 // maximum of t, P_j = exp2(t_j - m) multiplies plain codes, and
 // l = sum P_j / sv.  P is rounded to fp16 (2^-11 relative, absolute 2^-33 below
 // 2^-22); the sum l is formed from the unrounded values.
-#include <stdlib.h>
 #include <cmath>
 
 #include "rudder_internal.h"
@@ -184,7 +183,7 @@ __device__ __forceinline__ float to_f16(uint4 (&q)[N], uint32_t top) {
 
 // A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), as integers
 // q * 2^(14 - e) in [-32639, 32639] and these as two digits, 256 * high + low: N pairs of 16 bytes
-// (16 channels) become one of each.  Returns 2^(e - 14), or NaN for a row that is not finite.
+// (16 channels) become one of each.  Returns 2^(e - 14).
 template <int N>
 __device__ __forceinline__ float to_digits(const uint4 (&q)[2 * N], uint32_t top, uint4 (&high)[N],
                                            uint4 (&low)[N]) {
@@ -213,8 +212,7 @@ __device__ __forceinline__ float to_digits(const uint4 (&q)[2 * N], uint32_t top
         high[i] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         low[i] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
-    return field == 255 ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float((uint32_t)(127 + max(e - 14, -126)) << 23);
+    return __uint_as_float((uint32_t)(127 + max(e - 14, -126)) << 23);
 }
 
 // What turns a row's sum of P * code (or P * v) into its output: 0 where no key is visible.
@@ -383,19 +381,48 @@ __device__ __forceinline__ void interleave() {
 // most tiles then need no exchange between lanes and no rescaling of O.
 constexpr float kLazy = 6.0f;
 
+// A lane's share of its query row: the row's output, or for a piece of the keys its partial result.
+template <int D>
+__device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, int split, int unit,
+                                           int rest, int unit_rows, int unit_row, int t, int head,
+                                           int half, float m, float l,
+                                           const f32x16_acc (&o)[D / 32]) {
+    constexpr int kDT = D / 32;
+    const size_t out_row = (size_t)(s.r0 + t);
+    if (split >= 0) {
+        const size_t to = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
+        if (half == 0) p.part_ml[to] = make_float2(m, l);
+        float* d = p.part_o + to * D;
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<float4*>(d + dt * 32 + g * 8 + half * 4) = make_float4(
+                    o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
+        return;
+    }
+    const float f = row_factor(l);
+    uint16_t* d = p.O + out_row * p.ldo + (size_t)head * D;
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<uint2*>(d + dt * 32 + g * 8 + half * 4) =
+                make_uint2(pack_bf16(o[dt][4 * g] * f, o[dt][4 * g + 1] * f),
+                           pack_bf16(o[dt][4 * g + 2] * f, o[dt][4 * g + 3] * f));
+}
+
 // ---------------------------------------------------------------------------
-// Many rows: WAVES waves of 32 rows share the tiles through LDS.
+// Many rows: 128 of them a workgroup, four waves of 32 that share the tiles through LDS.
 // ---------------------------------------------------------------------------
-template <int D, bool CACHE, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, 2)
+template <int D, bool CACHE>
+__global__ void __launch_bounds__(256, 2)
 attention_tile_kernel(const Problem p) {
-    using St = Stage<D, CACHE, WAVES * 64>;
-    constexpr int kRows = WAVES * kWaveRows;
+    using St = Stage<D, CACHE, 256>;
+    constexpr int kRows = 4 * kWaveRows;
     constexpr int kKS = D / 16;                    // steps of the first product
     constexpr int kDT = D / 32;                    // channel tiles of the second
-    // with one workgroup a unit three tiles fit beside each other, which saves a barrier a tile
-    constexpr int kBuffers = WAVES == 8 ? 3 : 2;
-    __shared__ __align__(16) uint8_t lds[kBuffers * St::kBytes];
+    __shared__ __align__(16) uint8_t lds[2 * St::kBytes];
 
     const int rest = p.units - p.whole;            // split units
     const int split = (int)blockIdx.x < p.whole ? -1 : quotient(blockIdx.x - p.whole, rest);
@@ -583,13 +610,13 @@ attention_tile_kernel(const Problem p) {
         };
         for (;;) {
             if (mine) step(0, [&]() { return scores(cur, 1); }, old, 1);
-            if (kBuffers == 2) __syncthreads();    // the tile before has been read
+            __syncthreads();                       // the tile before has been read
             const bool more = page >= 0;
             uint8_t* ahead = cur;
             const int ahead_at = next_at;
             const float sk1 = sk, sv1 = sv;
             if (more) {
-                slot = slot + 1 == kBuffers ? 0 : slot + 1;
+                slot ^= 1;
                 ahead = lds + slot * St::kBytes;
                 stage.store(ahead);
                 load();
@@ -620,29 +647,236 @@ attention_tile_kernel(const Problem p) {
     }
     l += __shfl_xor(l, 32);
     if (!live) return;
-    const size_t out_row = (size_t)(s.r0 + t);
-    if (split >= 0) {
-        const size_t to = ((size_t)split * rest + (unit - p.whole)) * kRows +
-                          (row - tile_row * kRows);
-        if (half == 0) p.part_ml[to] = make_float2(m, l);
-        float* d = p.part_o + to * D;
+    write_rows<D>(p, s, split, unit, rest, kRows, row - tile_row * kRows, t, head, half, m, l, o);
+}
+
+// ---------------------------------------------------------------------------
+// Very many rows: 256 of them a workgroup, two groups of four waves in opposite phases.
+// ---------------------------------------------------------------------------
+// A wave alternates between a phase of products (scores of the next tile, values of this one) and a
+// phase of vector work (weights of the next tile, staging of a later one).  Waves w and w + 4 share
+// a vector unit and a matrix core and are one phase apart, kept so by a barrier a phase: one has
+// the matrix core while the other has the vector unit.  Tile i lives in slot i % 4 of LDS: group A's
+// phases of tile i are 2 i (products: K of i + 1, V of i) and 2 i + 1 (stores i + 3), B's one later,
+// so that slot (i + 3) % 4 = (i - 1) % 4 was last read in phase 2 i - 1 and is first read in
+// 2 i + 4.
+template <int D, bool CACHE>
+__global__ void __launch_bounds__(512, 2)
+attention_wide_kernel(const Problem p) {
+    using St = Stage<D, CACHE, 512>;
+    constexpr int kRows = 8 * kWaveRows;
+    constexpr int kKS = D / 16, kDT = D / 32;
+    __shared__ __align__(16) uint8_t lds[4 * St::kBytes];
+    __shared__ float2 lds_scale[4];
+    __shared__ int lds_at[4];
+
+    const int rest = p.units - p.whole;            // split units
+    const int split = (int)blockIdx.x < p.whole ? -1 : quotient(blockIdx.x - p.whole, rest);
+    const int unit = split < 0 ? blockIdx.x : blockIdx.x - split * rest;
+    const Place at_unit = place(p, unit);
+    const int h = at_unit.h, b = at_unit.b, tile_row = at_unit.tile;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int tile0 = max(split, 0) * p.piece_tiles;
+    // page numbers of 64 tiles, one a lane
+    const int32_t* table = CACHE ? p.page_table + (size_t)b * p.max_pages : nullptr;
+    auto page_numbers = [&](int i) {
+        const int64_t at = (int64_t)tile0 + i + lane;
+        return CACHE && at < p.max_pages ? table[at] : -1;
+    };
+    int numbers = page_numbers(0);
+    const Sequence s = sequence<CACHE>(p, b);
+    const int G = quotient(p.Hq, p.Hkv);
+    const int rows = min(s.n, p.max_rows) * G;     // (token, head of the group) pairs
+    if (tile_row * kRows >= rows) return;
+
+    // this lane's query row and the keys it sees; the least and most any row of the wave sees
+    const int row0 = tile_row * kRows + wave * kWaveRows, row = row0 + (lane & 31);
+    const bool live = row < rows;
+    const int t = live ? row / G : 0;
+    const int head = h * G + (live ? row % G : 0);
+    auto sees = [&](int tt) { return p.causal ? min(max(s.kv - s.n + tt + 1, 0), s.kv) : s.kv; };
+    const int limit = live ? sees(t) : 0;
+    const int least = sees(quotient(row0, G));
+    const int wave_most = row0 < rows ? sees(quotient(min(rows, row0 + kWaveRows) - 1, G)) : 0;
+    const int most = sees(quotient(min(rows, (tile_row + 1) * kRows) - 1, G));
+    const int tile1 = min((most + kPage - 1) / kPage,
+                          tile0 + (split < 0 ? p.most_tiles : p.piece_tiles));
+    if (split >= 0 && tile0 * kPage >= s.kv) return;       // the join does not read this piece
+
+    int index = -1;
+    // the next tile's page that lies in the pool, -1 behind the last tile
+    auto next = [&]() {
+        for (;;) {
+            if (tile0 + ++index >= tile1) return -1;
+            if (!CACHE) return 0;
+            if (index > 0 && (index & 63) == 0) numbers = page_numbers(index);
+            const int page = __builtin_amdgcn_readlane(numbers, index & 63);
+            if (page >= 0 && page < p.num_pages) return page;
+        }
+    };
+    St stage;
+    int page = 0, stage_at = 0, stored = 0;        // page < 0: no tile is on its way
+    float sk = 1.0f, sv = 1.0f;
+    auto load = [&]() {                            // the next tile, on its way to registers
+        page = page < 0 ? -1 : next();
+        if (page < 0) return;
+        stage_at = (tile0 + index) * kPage;
+        stage.load(p, s, h, page, stage_at);
+        if (CACHE) {
+            const float* sc = p.scales + ((size_t)page * p.Hkv + h) * 2;
+            sk = sc[0];
+            sv = sc[1];
+        }
+    };
+    auto store = [&]() {                           // the tile in registers, to its slot
+        if (page < 0) return;
+        const int slot = stored & 3;
+        stage.store(lds + slot * St::kBytes);
+        if (threadIdx.x == 0) {
+            lds_scale[slot] = make_float2(sk, sv);
+            lds_at[slot] = stage_at;
+        }
+        ++stored;
+    };
+    load();
+
+    uint4 q[kKS];
+    float l = 0.0f;                                // the lane's share of the sum of weights
+    // the softmax scale's sign goes to the query, so that exponents grow with the products
+    float c = fabsf(p.sm) * kLog2e;
+    {
+        const uint16_t* src = p.Q + (size_t)(s.r0 + t) * p.ldq + (size_t)head * D + half * 8;
+        const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int dt = 0; dt < kDT; ++dt)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<float4*>(d + dt * 32 + g * 8 + half * 4) = make_float4(
-                    o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
-        return;
+        for (int i = 0; i < kKS; ++i) {
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (live) q[i] = *reinterpret_cast<const uint4*>(src + i * 16);
+            q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
+        }
+        uint32_t top = abs_max_bits<kKS>(q);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        if (CACHE) c *= to_f16<kKS>(q, top);
     }
-    const float f = row_factor(l);
-    uint16_t* d = p.O + out_row * p.ldo + (size_t)head * D;
+
+    f32x16_acc o[kDT], z[2];
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt)
+    for (int i = 0; i < kDT; ++i)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<uint2*>(d + dt * 32 + g * 8 + half * 4) =
-                make_uint2(pack_bf16(o[dt][4 * g] * f, o[dt][4 * g + 1] * f),
-                           pack_bf16(o[dt][4 * g + 2] * f, o[dt][4 * g + 3] * f));
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    uint4 pk[4];
+    float m = -INFINITY, top_lsv = -INFINITY;
+    const int k_lane = (lane & 31) * St::kKStride + half * 16;
+    const int v_lane = St::kKBytes + (lane & 31) * St::kVStride + half * 16;
+
+    store();
+    load();
+    store();
+    load();                                        // two tiles in LDS, the third on its way
+    __syncthreads();
+    if (wave >= 4) __syncthreads();                // group B: one phase behind
+    bool now = false;                              // the wave sees the tile whose V is next
+    for (int i = -1;; ++i) {
+        // Phase of products.  Tile i + 1 is there if it has been stored: `stored` is the same in
+        // both groups where it is compared with i + 1, the tiles up to i + 2 being decided.
+        const bool more = i + 1 < stored;
+        const uint8_t* kt = lds + ((i + 1) & 3) * St::kBytes;
+        const uint8_t* vt = lds + (i & 3) * St::kBytes;
+        const int at = more ? __builtin_amdgcn_readfirstlane(lds_at[(i + 1) & 3]) : 0;
+        const bool ahead = more && at < wave_most;
+        if (ahead) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[tt][j] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kKS; ++k)
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+                    z[tt] = mma<CACHE>(*reinterpret_cast<const uint4*>(
+                                           kt + k_lane + tt * 32 * St::kKStride + k * 32),
+                                       q[k], z[tt]);
+        }
+        if (now)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                for (int dt = 0; dt < kDT; ++dt)
+                    o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(
+                                           vt + v_lane + dt * 32 * St::kVStride + ks * 32),
+                                       pk[ks], o[dt]);
+        __syncthreads();
+        if (!more) break;
+        // Phase of vector work: tile i + 3 to LDS, the one behind on its way, weights of i + 1.
+        store();
+        load();
+        now = ahead;
+        if (ahead) {
+            const float2 sc = lds_scale[(i + 1) & 3];
+            // c or a K scale of 0 must leave masked scores at -inf
+            const float cz = fmaxf(CACHE ? c * sc.x : c, 1e-30f);
+            const float svc = CACHE ? fmaxf(sc.y, kMinVScale) : 1.0f;
+            const float lsv = CACHE ? __builtin_amdgcn_logf(svc) : 0.0f;       // log2
+            if (at + kPage > least)                // some row does not see all of the tile
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (at + 32 * tt + 16 * (j >> 3) + 8 * half + (j & 7) >= limit)
+                            z[tt][j] = -INFINITY;
+            float top = z[0][0];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = fmaxf(top, z[tt][j]);
+            top = fmaf(cz, top, lsv);              // -inf: nothing visible
+            if (__any(top > m + kLazy)) {
+                const float m_new = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+                m = m_new;
+                l *= alpha;
+#pragma unroll
+                for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
+            }
+            // P = exp2(c z + log2(sv) - m), for the cache times 2^8
+            const float shift = lsv - (m == -INFINITY ? 0.0f : m) + (CACHE ? kPShift : 0.0f);
+            bool apart = false;
+            if (CACHE) {
+                top_lsv = fmaxf(top_lsv, lsv);
+                apart = scales_apart(lsv, top_lsv);
+                if (apart)
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            l += __builtin_amdgcn_exp2f(fmaf(cz, z[tt][j], shift - lsv));
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = (ks & 1) * 8 + 2 * j;
+                    const float a = __builtin_amdgcn_exp2f(fmaf(cz, z[ks >> 1][r], shift));
+                    const float e = __builtin_amdgcn_exp2f(fmaf(cz, z[ks >> 1][r + 1], shift));
+                    sum += a + e;
+                    w[j] = CACHE ? pack_f16(a, e) : pack_bf16(a, e);
+                }
+                pk[ks] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            l = fmaf(sum, apart ? 0.0f : 1.0f / svc, l);
+        }
+        __syncthreads();
+    }
+    if (wave < 4) __syncthreads();                 // group B's last phase of products
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+    write_rows<D>(p, s, split, unit, rest, kRows, row - tile_row * kRows, t, head, half, m, l, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -773,6 +1007,7 @@ attention_few_kernel(const Problem p) {
     }
 
     uint4 high[kC], low[kC];
+    float l = 0.0f;                                // the lane's share of the sum of weights
     // the softmax scale's sign goes to the query, so that exponents grow with the products
     float c = fabsf(p.sm) * kLog2e;
     {
@@ -785,17 +1020,20 @@ attention_few_kernel(const Problem p) {
             if (live) q[i] = *reinterpret_cast<const uint4*>(src + (i >> 1) * 64 + (i & 1) * 8);
             q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
         }
-        c *= to_digits<kC>(q, column_max(abs_max_bits<2 * kC>(q)), high, low);
+        const uint32_t top = column_max(abs_max_bits<2 * kC>(q));
+        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        c *= to_digits<kC>(q, top, high, low);
     }
 
     f32x4_acc o[kDT];
 #pragma unroll
     for (int i = 0; i < kDT; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -INFINITY, l = 0.0f, top_lsv = -INFINITY;
+    float m = -INFINITY, top_lsv = -INFINITY;
 
     while (page >= 0) {
         const int at = tile * kPage;
-        const float cz = c * sk, svc = fmaxf(sv, kMinVScale);
+        // c or a K scale of 0 must leave masked scores at -inf
+        const float cz = fmaxf(c * sk, 1e-30f), svc = fmaxf(sv, kMinVScale);
         const float lsv = __builtin_amdgcn_logf(svc), sv_inv = 1.0f / svc;
         // 256 * (high digits . K) + (low digits . K): |sums| < 2^30 for D = 128
         i32x4_acc zi[4];
@@ -823,21 +1061,19 @@ attention_few_kernel(const Problem p) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[i][j] = (float)zi[i][j];
-        const bool edge = at + kPage > least;      // some row does not see all of the page
-        auto hide = [&]() {
+        if (at + kPage > least) {                  // some row does not see all of the page
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (at + 16 * g + 4 * i + j >= limit) z[i][j] = -INFINITY;
-        };
-        if (edge) hide();
+        }
         float top = z[0][0];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = fmaxf(top, z[i][j]);
-        top = top == -INFINITY ? top : fmaf(cz, top, lsv);     // -inf: nothing visible
+        top = fmaf(cz, top, lsv);                  // -inf: nothing visible
         if (__any(top > m + kLazy)) {
             const float m_new = fmaxf(m, column_max(top));
             const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
@@ -850,34 +1086,30 @@ attention_few_kernel(const Problem p) {
         }
         const float base = m == -INFINITY ? 0.0f : m;
         const float shift = lsv - base + kPShift;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[i][j] = fmaf(cz, z[i][j], shift);
-        if (edge) hide();                          // again: cz may be 0 or NaN
-        float sum = 0.0f;
         top_lsv = fmaxf(top_lsv, lsv);
-        if (scales_apart(lsv, top_lsv)) {
+        const bool apart = scales_apart(lsv, top_lsv);
+        if (apart)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) l += __builtin_amdgcn_exp2f(z[i][j] - lsv);
-            sum = -INFINITY;                       // marks l as done
-        }
+                for (int j = 0; j < 4; ++j)
+                    l += __builtin_amdgcn_exp2f(fmaf(cz, z[i][j], shift - lsv));
+        float sum = 0.0f;
         uint4 pk[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float a0 = __builtin_amdgcn_exp2f(z[2 * e + (j >> 1)][2 * (j & 1)]);
-                const float a1 = __builtin_amdgcn_exp2f(z[2 * e + (j >> 1)][2 * (j & 1) + 1]);
+                const f32x4_acc& zt = z[2 * e + (j >> 1)];
+                const float a0 = __builtin_amdgcn_exp2f(fmaf(cz, zt[2 * (j & 1)], shift));
+                const float a1 = __builtin_amdgcn_exp2f(fmaf(cz, zt[2 * (j & 1) + 1], shift));
                 sum += a0 + a1;
                 w[j] = pack_f16(a0, a1);
             }
             pk[e] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (sum != -INFINITY) l = fmaf(sum, sv_inv, l);
+        l = fmaf(sum, apart ? 0.0f : sv_inv, l);
 #pragma unroll
         for (int i = 0; i < kDT; ++i) {
             o[i] = mma16(widen8(v[i].x, v[i].y), pk[0], o[i]);
@@ -911,7 +1143,7 @@ attention_few_kernel(const Problem p) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float wm = lm[w][r];
-            if (wm != -INFINITY) total = fmaf(ll[w][r], __builtin_amdgcn_exp2f(wm - best), total);
+            total = fmaf(ll[w][r], wm == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(wm - best), total);
             const float4 x = *reinterpret_cast<const float4*>(&lo[w][r][d]);
             a.x += x.x;
             a.y += x.y;
@@ -994,8 +1226,6 @@ struct Plan {
 
 constexpr int kFewWaves = 4;
 
-int tile_waves(int64_t rows) { const char* e = getenv("TW"); return e ? atoi(e) : rows > 128 ? 8 : 4; }
-
 // Pieces of at least `least` tiles, `wanted` of them where the tiles suffice.
 void split(Plan& p, int64_t wanted, int tiles, int least) {
     const int most = (tiles + least - 1) / least;
@@ -1014,7 +1244,8 @@ void split(Plan& p, int64_t wanted, int tiles, int least) {
 // to 4096 tiles one workgroup a unit is best and above two; from 256 (sequence, head) pairs on,
 // ragged lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135 [2]).
 // False for more workgroups than a launch takes.
-bool plan(bool cache, int B, int max_rows, int max_kv, int Hq, int Hkv, int D, Plan& p) {
+bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int Hkv, int D,
+          Plan& p) {
     const int tiles = (int)(((int64_t)max_kv + kPage - 1) / kPage);
     const int64_t rows = (int64_t)max_rows * (Hq / Hkv), pairs = (int64_t)B * Hkv;
     p.whole = 0;
@@ -1027,16 +1258,20 @@ bool plan(bool cache, int B, int max_rows, int max_kv, int Hq, int Hkv, int D, P
         split(p, tiles * D <= 8 * 128 ? 1 : (want + pairs - 1) / pairs, tiles, kFewWaves);
         return pairs * p.pieces <= (1 << 22);
     }
-    p.waves = tile_waves(rows);
+    // 256 rows a workgroup where every row sees long stretches of keys (128 channels: 2 x 4096 rows
+    // over 16384 tokens 1149 us, 1311 with 128; 4 x 1000 over 1000 50 against 55; causal 941 against
+    // 918, and with 64 channels 925 against 886)
+    p.waves = D == 128 && !causal && rows > 128 && tiles >= 16 ? 8 : 4;
     p.unit_rows = kWaveRows * p.waves;
     const int64_t tile_rows = (rows + p.unit_rows - 1) / p.unit_rows, units = tile_rows * pairs;
     if (units > (1 << 21)) return false;
     p.tile_rows = (int)tile_rows;
     p.units = (int)units;
     // a round is what runs at once; what is left over after whole rounds is split into one more
+    // (2 x 4192 rows over 12576 tokens, 544 units: 1188 us whole, 976 split)
     const int round = p.waves == 8 ? 256 : 512, rest = p.units % round;
-    const char* ns = getenv("NS"); const int NS = ns ? atoi(ns) : 99;
-    split(p, rest > 0 && rest <= round / 2 ? (round / rest < NS ? round / rest : NS) : 1, tiles, p.units < round ? 4 : 2);
+    const bool worth = rest > 0 && rest <= round / 2 && tiles >= 16;
+    split(p, worth ? round / rest : 1, tiles, 4);
     p.whole = p.pieces > 1 ? p.units - rest : p.units;
     return true;
 }
@@ -1044,7 +1279,8 @@ bool plan(bool cache, int B, int max_rows, int max_kv, int Hq, int Hkv, int D, P
 template <int D, bool CACHE>
 hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
     Plan sp;
-    if (!plan(CACHE, p.B, p.max_rows, p.max_kv, p.Hq, p.Hkv, D, sp)) return hipErrorInvalidValue;
+    if (!plan(CACHE, p.causal, p.B, p.max_rows, p.max_kv, p.Hq, p.Hkv, D, sp))
+        return hipErrorInvalidValue;
     p.tile_rows = sp.tile_rows;
     p.units = sp.units;
     p.whole = sp.whole;
@@ -1063,9 +1299,9 @@ hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
                 attention_few_kernel<D, kFewWaves><<<grid, kFewWaves * 64, 0, stream>>>(p);
         }
     } else if (sp.waves == 8) {
-        attention_tile_kernel<D, CACHE, 8><<<grid, 512, 0, stream>>>(p);
+        if constexpr (D == 128) attention_wide_kernel<D, CACHE><<<grid, 512, 0, stream>>>(p);
     } else {
-        attention_tile_kernel<D, CACHE, 4><<<grid, 256, 0, stream>>>(p);
+        attention_tile_kernel<D, CACHE><<<grid, 256, 0, stream>>>(p);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.pieces == 1) return e;
@@ -1078,10 +1314,10 @@ hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
 
 }  // namespace
 
-bool attention_workspace(bool cache, int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D,
-                         size_t& bytes) {
+bool attention_workspace(bool cache, bool causal, int B, int T, int max_rows, int max_kv, int Hq,
+                         int Hkv, int D, size_t& bytes) {
     Plan p;
-    if (!plan(cache, B, max_rows < T ? max_rows : T, max_kv, Hq, Hkv, D, p)) return false;
+    if (!plan(cache, causal, B, max_rows < T ? max_rows : T, max_kv, Hq, Hkv, D, p)) return false;
     bytes = p.part_rows() * (size_t)(D + 2) * sizeof(float);
     return true;
 }

@@ -396,7 +396,7 @@ rudder_status_t check_ld(const char* f, const char* name, int ld, int heads, int
     return RUDDER_OK;
 }
 
-rudder_status_t check_attention(const char* f, bool cache, const void* Q, const void* O,
+rudder_status_t check_attention(const char* f, bool cache, bool causal, const void* Q, const void* O,
                                 const void* workspace, size_t workspace_bytes, int B, int T,
                                 int max_rows, int max_kv, int Hq, int Hkv, int D, int ldq,
                                 int ldo, float sm) {
@@ -423,7 +423,7 @@ rudder_status_t check_attention(const char* f, bool cache, const void* Q, const 
                     max_rows, Hq);
     if (B == 0 || T == 0 || max_rows == 0) return RUDDER_OK;
     size_t need = 0;
-    if (!rudder::attention_workspace(cache, B, T, max_rows, max_kv, Hq, Hkv, D, need))
+    if (!rudder::attention_workspace(cache, causal, B, T, max_rows, max_kv, Hq, Hkv, D, need))
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d sequences of max_rows=%d rows exceed a launch",
                     f, B, max_rows);
     if (need > 0 && (!workspace || workspace_bytes < need))
@@ -495,10 +495,11 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
         Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || (int64_t)B * Hkv > kMaxSequences ||
         (int64_t)max_rows * Hq > (1 << 26))
         return 0;
-    // one size for both calls
+    // one size for both calls, causal or not
     size_t bytes = 0, most = 0;
-    for (const bool cache : {false, true})
-        if (rudder::attention_workspace(cache, B, T, max_rows, max_kv, Hq, Hkv, D, bytes))
+    for (const int kind : {0, 1, 2})
+        if (rudder::attention_workspace(kind > 0, kind > 1, B, T, max_rows, max_kv, Hq, Hkv, D,
+                                        bytes))
             most = most > bytes ? most : bytes;
     return most;
 }
@@ -516,7 +517,7 @@ rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_sta
     if (max_pages <= 0 || num_pages <= 0)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: max_pages=%d and num_pages=%d must be positive",
                     f, max_pages, num_pages);
-    const rudder_status_t st = check_attention(f, true, Q, O, workspace, workspace_bytes, B, T,
+    const rudder_status_t st = check_attention(f, true, causal != 0, Q, O, workspace, workspace_bytes, B, T,
                                                max_rows, max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if (misaligned(codes))
@@ -540,7 +541,7 @@ rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, con
     if (!Q || !K || !V || !row_start || !kv_start || !kv_len || !O)
         return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
     if (Tkv < 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Tkv=%d must be >= 0", f, Tkv);
-    rudder_status_t st = check_attention(f, false, Q, O, workspace, workspace_bytes, B, T, max_rows,
+    rudder_status_t st = check_attention(f, false, false, Q, O, workspace, workspace_bytes, B, T, max_rows,
                                          max_kv, Hq, Hkv, D, ldq, ldo, sm);
     if (st != RUDDER_OK) return st;
     if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
