@@ -69,30 +69,34 @@ struct Problem {
     // take all of their keys; the others are split into `pieces` of `piece_tiles` tiles whose
     // results are joined.
     int tile_rows, units, whole, pieces, piece_tiles, most_tiles;
-    int last_first;     // 1: a pair's row tiles in descending order
+    int dies, run, tile_major, descending;         // their order, see place()
     float* part_o;      // [pieces][units - whole][rows of a unit][D]
     float2* part_ml;    // [pieces][units - whole][rows of a unit]
 };
 
-// Unit number -> row tile of a pair.  Workgroups go round robin to the eight dies: the tiles of a
-// pair, which read the same keys, are kept on one where the pairs divide evenly.  Causal tiles come
-// longest first.
-struct Place {
-    int h, b, tile;
-};
 // a / b of wave-uniform values, back in a scalar register (the division runs on the vector units)
 __device__ __forceinline__ int quotient(int a, int b) {
     return __builtin_amdgcn_readfirstlane(a / b);
 }
+
+// Unit number -> row tile of a pair.  Workgroups go round robin to the eight dies: where the pairs
+// divide by eight, the units of a pair, which read the same keys, are kept on one (dies = 8, else
+// 1).  A pair's tiles follow each other, causal ones, whose lengths differ, longest first
+// (descending = 1); where the keys of a die take at most half its L2 they go longest first over all its pairs
+// (tile_major = 1), which ends more evenly: 4096 causal rows of 16 heads over 4096 tokens 126 us, pair
+// by pair 162; over 16384 tokens, 2 x 4096 rows, 1077 against 918.  Chosen by arithmetic: a branch by
+// p.causal made two kernels of one and cost 50 registers.
+struct Place {
+    int h, b, tile;
+};
 __device__ __forceinline__ Place place(const Problem& p, int unit) {
-    const int pairs = p.Hkv * p.B, slot = unit / 8;
-    const bool even = pairs % 8 == 0;
-    const int pair = even ? unit % 8 + 8 * quotient(slot, p.tile_rows)
-                          : quotient(unit, p.tile_rows);
-    const int tile = (even ? slot : unit) - quotient(even ? slot : unit, p.tile_rows) * p.tile_rows;
+    const int slot = quotient(unit, p.dies), low = unit - slot * p.dies;
+    const int q = quotient(slot, p.run), r = slot - q * p.run;
+    const int pair = low + p.dies * (q + p.tile_major * (r - q));
+    const int up = r + p.tile_major * (q - r);
+    const int tile = up + p.descending * (p.tile_rows - 1 - 2 * up);
     const int b = quotient(pair, p.Hkv);
-    // arithmetic in place of a choice by p.causal, which would make two kernels of one
-    return {pair - b * p.Hkv, b, tile + p.last_first * (p.tile_rows - 1 - 2 * tile)};
+    return {pair - b * p.Hkv, b, tile};
 }
 
 // Sequence b's query rows and keys, clamped to the buffers whatever the arrays hold.
@@ -381,35 +385,92 @@ __device__ __forceinline__ void interleave() {
 // most tiles then need no exchange between lanes and no rescaling of O.
 constexpr float kLazy = 6.0f;
 
-// A lane's share of its query row: the row's output, or for a piece of the keys its partial result.
+// Orders a wave's LDS accesses of different lanes (the hardware keeps their order; this keeps the
+// compiler's).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The 32 query rows of a wave pass through LDS, so that global memory sees whole rows: a lane's
+// share of its row is 16 bytes in 32 (loads) or 8 in 16 (stores).  2 x 4192 rows of 16 heads over 128
+// keys 33.9 us without, of which 6.5 were the loads' and 10 the stores'.
 template <int D>
-__device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, int split, int unit,
-                                           int rest, int unit_rows, int unit_row, int t, int head,
-                                           int half, float m, float l,
-                                           const f32x16_acc (&o)[D / 32]) {
-    constexpr int kDT = D / 32;
-    const size_t out_row = (size_t)(s.r0 + t);
-    if (split >= 0) {
-        const size_t to = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
-        if (half == 0) p.part_ml[to] = make_float2(m, l);
-        float* d = p.part_o + to * D;
+struct RowSlab {
+    static constexpr int kStride = D * 2 + 16, kBytes = kWaveRows * kStride;
+    static constexpr int kPieces = D / 8, kRowsAtOnce = 64 / kPieces;
+
+    // Lane l's row (token t, head) for l < 32 -> the lanes' operands of the first product.
+    static __device__ __forceinline__ void load(const Problem& p, const Sequence& s, uint8_t* slab,
+                                                int t, int head, uint4 (&q)[D / 16]) {
+        const int lane = threadIdx.x & 63, piece = lane % kPieces;
+        uint4 x[kWaveRows / kRowsAtOnce];
 #pragma unroll
-        for (int dt = 0; dt < kDT; ++dt)
+        for (int i = 0; i < kWaveRows / kRowsAtOnce; ++i) {
+            const int r = i * kRowsAtOnce + lane / kPieces;
+            const int rt = __shfl(t, r), rh = __shfl(head, r);
+            x[i] = *reinterpret_cast<const uint4*>(p.Q + (size_t)(s.r0 + rt) * p.ldq +
+                                                   (size_t)rh * D + piece * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kWaveRows / kRowsAtOnce; ++i)
+            *reinterpret_cast<uint4*>(slab + (i * kRowsAtOnce + lane / kPieces) * kStride +
+                                      piece * 16) = x[i];
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            q[i] = *reinterpret_cast<const uint4*>(slab + (lane & 31) * kStride + (lane >> 5) * 16 +
+                                                   i * 32);
+    }
+
+    // O times f of the rows that are live.
+    static __device__ __forceinline__ void store(const Problem& p, const Sequence& s, uint8_t* slab,
+                                                 int t, int head, bool live, float f,
+                                                 const f32x16_acc (&o)[D / 32]) {
+        const int lane = threadIdx.x & 63, piece = lane % kPieces;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<float4*>(d + dt * 32 + g * 8 + half * 4) = make_float4(
-                    o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
+                *reinterpret_cast<uint2*>(slab + (lane & 31) * kStride +
+                                          (dt * 32 + g * 8 + (lane >> 5) * 4) * 2) =
+                    make_uint2(pack_bf16(o[dt][4 * g] * f, o[dt][4 * g + 1] * f),
+                               pack_bf16(o[dt][4 * g + 2] * f, o[dt][4 * g + 3] * f));
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < kWaveRows / kRowsAtOnce; ++i) {
+            const int r = i * kRowsAtOnce + lane / kPieces;
+            const int rt = __shfl(t, r), rh = __shfl(head, r), there = __shfl((int)live, r);
+            const uint4 x = *reinterpret_cast<const uint4*>(slab + r * kStride + piece * 16);
+            if (there)
+                *reinterpret_cast<uint4*>(p.O + (size_t)(s.r0 + rt) * p.ldo + (size_t)rh * D +
+                                          piece * 8) = x;
+        }
+    }
+};
+
+// A wave's rows: their outputs, or for a piece of the keys their partial results.  Every lane comes
+// here; `slab` is the wave's own.
+template <int D>
+__device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, uint8_t* slab,
+                                           int split, int unit, int rest, int unit_rows,
+                                           int unit_row, int t, int head, bool live, float m,
+                                           float l, const f32x16_acc (&o)[D / 32]) {
+    if (split < 0) {
+        RowSlab<D>::store(p, s, slab, t, head, live, row_factor(l), o);
         return;
     }
-    const float f = row_factor(l);
-    uint16_t* d = p.O + out_row * p.ldo + (size_t)head * D;
+    if (!live) return;
+    const int half = (threadIdx.x & 63) >> 5;
+    const size_t to = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
+    if (half == 0) p.part_ml[to] = make_float2(m, l);
+    float* d = p.part_o + to * D;
 #pragma unroll
-    for (int dt = 0; dt < kDT; ++dt)
+    for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<uint2*>(d + dt * 32 + g * 8 + half * 4) =
-                make_uint2(pack_bf16(o[dt][4 * g] * f, o[dt][4 * g + 1] * f),
-                           pack_bf16(o[dt][4 * g + 2] * f, o[dt][4 * g + 3] * f));
+            *reinterpret_cast<float4*>(d + dt * 32 + g * 8 + half * 4) = make_float4(
+                o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -419,6 +480,7 @@ template <int D, bool CACHE>
 __global__ void __launch_bounds__(256, 2)
 attention_tile_kernel(const Problem p) {
     using St = Stage<D, CACHE, 256>;
+    static_assert(4 * RowSlab<D>::kBytes <= St::kBytes, "a wave's rows fit beside a tile");
     constexpr int kRows = 4 * kWaveRows;
     constexpr int kKS = D / 16;                    // steps of the first product
     constexpr int kDT = D / 32;                    // channel tiles of the second
@@ -463,12 +525,11 @@ attention_tile_kernel(const Problem p) {
     // the softmax scale's sign goes to the query, so that exponents grow with the products
     float c = fabsf(p.sm) * kLog2e;
     {
-        const uint16_t* src = p.Q + (size_t)(s.r0 + t) * p.ldq + (size_t)head * D + half * 8;
+        // the second tile's place is free until a barrier has passed
+        RowSlab<D>::load(p, s, lds + St::kBytes + wave * RowSlab<D>::kBytes, t, head, q);
         const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < kKS; ++i) {
-            q[i] = make_uint4(0, 0, 0, 0);
-            if (live) q[i] = *reinterpret_cast<const uint4*>(src + i * 16);
             q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
         }
         uint32_t top = abs_max_bits<kKS>(q);
@@ -646,8 +707,9 @@ attention_tile_kernel(const Problem p) {
         }
     }
     l += __shfl_xor(l, 32);
-    if (!live) return;
-    write_rows<D>(p, s, split, unit, rest, kRows, row - tile_row * kRows, t, head, half, m, l, o);
+    __syncthreads();                               // the tiles have been read
+    write_rows<D>(p, s, lds + wave * RowSlab<D>::kBytes, split, unit, rest, kRows,
+                  row - tile_row * kRows, t, head, live, m, l, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -664,6 +726,7 @@ template <int D, bool CACHE>
 __global__ void __launch_bounds__(512, 2)
 attention_wide_kernel(const Problem p) {
     using St = Stage<D, CACHE, 512>;
+    static_assert(8 * RowSlab<D>::kBytes <= 2 * St::kBytes, "a wave's rows fit beside two tiles");
     constexpr int kRows = 8 * kWaveRows;
     constexpr int kKS = D / 16, kDT = D / 32;
     __shared__ __align__(16) uint8_t lds[4 * St::kBytes];
@@ -746,12 +809,11 @@ attention_wide_kernel(const Problem p) {
     // the softmax scale's sign goes to the query, so that exponents grow with the products
     float c = fabsf(p.sm) * kLog2e;
     {
-        const uint16_t* src = p.Q + (size_t)(s.r0 + t) * p.ldq + (size_t)head * D + half * 8;
+        // the third and fourth tile's places are free until a barrier has passed
+        RowSlab<D>::load(p, s, lds + 2 * St::kBytes + wave * RowSlab<D>::kBytes, t, head, q);
         const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < kKS; ++i) {
-            q[i] = make_uint4(0, 0, 0, 0);
-            if (live) q[i] = *reinterpret_cast<const uint4*>(src + i * 16);
             q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
         }
         uint32_t top = abs_max_bits<kKS>(q);
@@ -875,8 +937,8 @@ attention_wide_kernel(const Problem p) {
     }
     if (wave < 4) __syncthreads();                 // group B's last phase of products
     l += __shfl_xor(l, 32);
-    if (!live) return;
-    write_rows<D>(p, s, split, unit, rest, kRows, row - tile_row * kRows, t, head, half, m, l, o);
+    write_rows<D>(p, s, lds + wave * RowSlab<D>::kBytes, split, unit, rest, kRows,
+                  row - tile_row * kRows, t, head, live, m, l, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -1270,8 +1332,11 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
     // a round is what runs at once; what is left over after whole rounds is split into one more
     // (2 x 4192 rows over 12576 tokens, 544 units: 1188 us whole, 976 split)
     const int round = p.waves == 8 ? 256 : 512, rest = p.units % round;
-    const bool worth = rest > 0 && rest <= round / 2 && tiles >= 16;
-    split(p, worth ? round / rest : 1, tiles, 4);
+    // (short ones do not repay the join: 512 rows of 16 heads over 512 keys 22.4 us whole, 24.4 in
+    // two; 2 x 4192 rows over 512 keys 66 us whole, 60 with the last 32 of 1056 units in four)
+    const bool alone = p.units < round;
+    const bool worth = rest > 0 && rest <= round / 2 && tiles >= (alone ? 16 : 8);
+    split(p, worth ? round / rest : 1, tiles, alone ? 4 : 2);
     p.whole = p.pieces > 1 ? p.units - rest : p.units;
     return true;
 }
@@ -1286,7 +1351,11 @@ hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
     p.whole = sp.whole;
     p.pieces = sp.pieces;
     p.piece_tiles = sp.piece_tiles;
-    p.last_first = p.causal ? 1 : 0;
+    const int pairs = p.Hkv * p.B;
+    p.dies = pairs % 8 == 0 ? 8 : 1;
+    p.descending = p.causal ? 1 : 0;
+    p.tile_major = p.causal && (int64_t)(pairs / p.dies) * p.max_kv * (2 * D) <= (2 << 20) ? 1 : 0;
+    p.run = p.tile_major ? pairs / p.dies : p.tile_rows;
     p.most_tiles = (int)(((int64_t)p.max_kv + kPage - 1) / kPage);
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + sp.part_rows() * D);
