@@ -65,7 +65,8 @@ size_t rudder_cache_page_bytes(int Hkv, int D);
  *   D 64 or 128
  * Errors: INVALID_ARG for a null pointer, a negative or zero size, ldk or ldv
  * below Hkv * D or not a multiple of 8, K, V, codes or scales not 16-byte aligned;
- * UNSUPPORTED for D other than 64 or 128, B > 65535, Hkv > 4096.
+ * UNSUPPORTED for D other than 64 or 128, B > 65535, Hkv > 4096, more than
+ * 2^29 rows.
  */
 rudder_status_t rudder_cache_append(const uint16_t* K, const uint16_t* V,
                                     const int32_t* row_start, const int32_t* pos,
@@ -122,8 +123,9 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * not a multiple of 8, sm not finite, a workspace that is too small, Q, codes, O
  * or workspace not 16-byte aligned;
  * UNSUPPORTED for D other than 64 or 128, Hkv > 4096, B * Hkv > 65535,
- * max_rows * Hq > 2^26, or B * Hkv * ceil(max_rows * Hq / Hkv / 128) > 2^21
- * (give max_rows as it is, not a far larger bound).
+ * max_kv > 2^30, min(max_rows, T) * Hq > 2^26, or B * Hkv *
+ * ceil(max_rows * Hq / Hkv / 128) > 2^21 (give max_rows as it is, not a far
+ * larger bound).
  */
 rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_start,
                                        const int32_t* kv_len, const int32_t* page_table,

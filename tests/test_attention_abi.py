@@ -75,7 +75,8 @@ APPEND = dict(K=P, V=P, row_start=P, pos=P, table=P, B=2, T=4, max_rows=2, max_p
     (dict(T=-1), 1), (dict(max_rows=-1), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1),
     (dict(Hkv=0), 1), (dict(ldk=127), 1), (dict(ldk=120), 1), (dict(ldv=132), 1),
     (dict(K=P + 8), 1), (dict(codes=P + 1), 1), (dict(D=96), 2), (dict(B=65536), 2),
-    (dict(Hkv=5000, ldk=5000 * 64, ldv=5000 * 64), 2), (dict(B=0), 0), (dict(T=0), 0),
+    (dict(Hkv=5000, ldk=5000 * 64, ldv=5000 * 64), 2),
+    (dict(T=1 << 30, max_rows=1 << 30), 2), (dict(B=0), 0), (dict(T=0), 0),
     (dict(max_rows=0), 0),
 ])
 def test_append_refusals(r, kw, status):
@@ -104,7 +105,8 @@ BOTH = [
     (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(ldq=255), 1), (dict(ldq=248), 1),
     (dict(ldo=260), 1), (dict(sm=float("nan")), 1), (dict(sm=float("inf")), 1),
     (dict(Q=P + 8), 1), (dict(O=P + 2), 1), (dict(ws=P + 4), 1), (dict(D=80), 2),
-    (dict(B=70000), 2), (dict(B=40000), 2), (dict(max_rows=1 << 25), 2),
+    (dict(B=70000), 2), (dict(B=40000), 2), (dict(T=1 << 25, max_rows=1 << 25), 2),
+    (dict(max_kv=(1 << 30) + 1), 2),
     (dict(B=3000, T=1 << 20, max_rows=1 << 20), 2),
     (dict(B=0), 0), (dict(T=0), 0), (dict(max_rows=0), 0),
     (dict(max_kv=1 << 20, ws=None), 1), (dict(max_kv=1 << 20, wbytes=1000), 1),   # a workspace
@@ -137,16 +139,22 @@ def test_binding_checks_tensors(r):
     ok = dict(Q=q, row_start=i32, kv_len=i32, page_table=i32, codes=codes, scales=scales, B=2,
               T=T, max_rows=2, max_kv=100, max_pages=2, num_pages=3, Hq=H, Hkv=H, D=D, sm=0.1,
               causal=True, workspace=None, O=q.clone(), stream=0)
+    # addresses pass as they are: what is under test is the one tensor
+    addresses = {k: P for k in ("Q", "row_start", "kv_len", "page_table", "codes", "scales", "O")}
     for kw in (dict(Q=q.float()), dict(Q=q[:3]), dict(Q=q.transpose(0, 1)), dict(Q=q[..., ::2]),
                dict(row_start=i32.long()), dict(row_start=i32[:2]), dict(kv_len=i32[:1]),
                dict(page_table=i32[:3]), dict(page_table=i32[::2]), dict(codes=codes[:2]),
                dict(scales=scales[:2]), dict(scales=scales.double()), dict(O=q[:2]),
-               dict(ldq=2 * H * D)):
-        with pytest.raises(ValueError):
-            r.rudder_cache_attention(**{**ok, **kw})
-    with pytest.raises(ValueError):
-        r.rudder_matvec_w4(q.view(T, -1), None, torch.zeros(100, dtype=torch.uint8), scales, None,
-                           None, T, 32, 128, 64, 1, q, stream=0)
+               dict(Q=q, ldq=2 * H * D)):
+        with pytest.raises(ValueError, match="expected at least"):
+            r.rudder_cache_attention(**{**ok, **addresses, **kw})
+    with pytest.raises(ValueError, match="Wq.*expected at least"):
+        r.rudder_matvec_w4(P, None, torch.zeros(100, dtype=torch.uint8), P, None, None, T, 32, 128,
+                           64, 1, P, stream=0)
+    # host memory is not taken for device memory
+    for name in ("Q", "row_start", "codes", "O"):
+        with pytest.raises(ValueError, match=f"{name}: not on a GPU"):
+            r.rudder_cache_attention(**{**ok, **addresses, name: ok[name]})
     with pytest.raises(r.RudderError) as e:
-        r.rudder_cache_attention(**{**ok, "sm": float("nan")})
+        r.rudder_cache_attention(**{**ok, **addresses, "sm": float("nan")})
     assert e.value.status == r.RUDDER_ERR_INVALID_ARG

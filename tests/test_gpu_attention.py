@@ -89,6 +89,8 @@ def test_cache_attention(rudder, counts, lens, Hq, Hkv, D, causal):
 LARGE_CASES = [
     # counts, lens, Hq, Hkv, D, causal, heads
     ([300, 41], [1100, 1030], 4, 2, 128, False, [0, 3]),       # 256 rows a workgroup
+    ([300, 130, 200], [1100, 0, 63], 2, 2, 128, False, [0, 1]),
+    ([260, 300], [64, 1200], 1, 1, 128, False, [0]),
     ([1100, 700], [1025, 1500], 32, 32, 128, False, [0, 17, 31]),
     ([700], [1400], 96, 96, 64, True, [0, 1, 50, 95]),
     ([257, 513], [1100, 1600], 96, 48, 128, True, [0, 95]),

@@ -378,6 +378,8 @@ namespace {
 
 constexpr int kMaxSequences = 65535;
 constexpr int kMaxCacheHeads = 4096;
+constexpr int kMaxKeys = 1 << 30;          // key numbers and the tiles' ends stay below 2^31
+constexpr int kMaxAppendRows = 1 << 29;
 
 rudder_status_t check_heads(const char* f, int Hkv, int D) {
     if (Hkv <= 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Hkv=%d must be positive", f, Hkv);
@@ -418,9 +420,11 @@ rudder_status_t check_attention(const char* f, bool cache, bool causal, const vo
     if ((int64_t)B * Hkv > kMaxSequences)
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d with Hkv=%d exceeds %d", f, B, Hkv,
                     kMaxSequences);
-    if ((int64_t)max_rows * Hq > (1 << 26))
+    if ((int64_t)(max_rows < T ? max_rows : T) * Hq > (1 << 26))
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d with Hq=%d exceeds 2^26 rows", f,
                     max_rows, Hq);
+    if (max_kv > kMaxKeys)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_kv=%d exceeds %d", f, max_kv, kMaxKeys);
     if (B == 0 || T == 0 || max_rows == 0) return RUDDER_OK;
     size_t need = 0;
     if (!rudder::attention_workspace(cache, causal, B, T, max_rows, max_kv, Hq, Hkv, D, need))
@@ -459,6 +463,9 @@ rudder_status_t rudder_cache_append(const uint16_t* K, const uint16_t* V,
                     f);
     if (B > kMaxSequences)
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d exceeds %d", f, B, kMaxSequences);
+    if (max_rows > kMaxAppendRows && T > kMaxAppendRows)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d exceeds %d", f, max_rows,
+                    kMaxAppendRows);
     if (B == 0 || T == 0 || max_rows == 0) return ok();
     return from_hip(rudder::launch_cache_append(K, V, row_start, pos, page_table, B, T,
                                                 max_rows < T ? max_rows : T, max_pages, num_pages,
@@ -493,7 +500,7 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
                                         int D) {
     if (B <= 0 || T <= 0 || max_rows <= 0 || max_kv < 0 || Hkv <= 0 || Hkv > kMaxCacheHeads ||
         Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || (int64_t)B * Hkv > kMaxSequences ||
-        (int64_t)max_rows * Hq > (1 << 26))
+        (int64_t)(max_rows < T ? max_rows : T) * Hq > (1 << 26) || max_kv > kMaxKeys)
         return 0;
     // one size for both calls, causal or not
     size_t bytes = 0, most = 0;

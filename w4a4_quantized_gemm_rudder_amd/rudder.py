@@ -174,6 +174,16 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
+def _stream_for(stream, t) -> Optional[int]:
+    """As _stream; the current stream only for a tensor of the current device."""
+    if stream is None and t.__class__ is not int:
+        import torch
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {t.device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         return _current_stream()
@@ -280,7 +290,9 @@ def _arr(name, t, types: list, least: int) -> Optional[int]:
     if t is None or t.__class__ is int:
         return t
     if t.dtype in types and t.numel() >= least and t.is_contiguous():
-        return t.data_ptr()
+        if t.is_cuda:
+            return t.data_ptr()
+        raise ValueError(f"{name}: not on a GPU")
     raise ValueError(f"{name}: {t.dtype}, {t.numel()} elements, strides {t.stride()}: expected "
                      f"at least {least} contiguous elements of "
                      f"{' or '.join(str(d) for d in types)}")
@@ -300,6 +312,8 @@ def _rows(name, t, T: int, H: int, D: int, ld: Optional[int]):
         raise ValueError(f"{name}: {t.dtype}, shape {tuple(shape)}, strides {st}: expected at "
                          f"least {T} rows of {H} x {D} packed bf16 values"
                          + ("" if ld is None else f", {ld} apart"))
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not on a GPU")
     return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], H * D)
 
 
@@ -317,7 +331,7 @@ def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
     _check(lib.rudder_quantize_weights_grouped(
         _arr("W", W, _BF16, K * N), K, N, group,
         _arr("Wq", Wq, _U8, grouped_weight_bytes(K, N)),
-        _arr("g_scale", g_scale, _BF16, grouped_scale_count(K, N, group)), _stream(stream)))
+        _arr("g_scale", g_scale, _BF16, grouped_scale_count(K, N, group)), _stream_for(stream, W)))
 
 
 def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, K: int,
@@ -329,7 +343,7 @@ def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, 
         _arr("Wq", Wq, _U8, k_tiles * 64 * n_pad),
         _arr("g_scale", g_scale, _BF16, k_tiles * (128 // max(group, 1)) * n_pad),
         _arr("comp_a", comp_a, _F32, S * N), _arr("comp_b", comp_b, _F32, S * N), M, N, K, group,
-        S, _arr("Y", Y, _BF16, M * N), _stream(stream)))
+        S, _arr("Y", Y, _BF16, M * N), _stream_for(stream, X)))
 
 
 def cache_page_bytes(Hkv: int, D: int) -> int:
@@ -352,7 +366,7 @@ def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_ro
     _check(lib.rudder_cache_append(
         k, v, _arr("row_start", row_start, _I32, B + 1), _arr("pos", pos, _I32, B),
         _arr("page_table", page_table, _I32, B * max_pages), B, T, max_rows, max_pages, num_pages,
-        Hkv, D, ldk, ldv, c, s, _stream(stream)))
+        Hkv, D, ldk, ldv, c, s, _stream_for(stream, codes)))
 
 
 def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int, D: int, K_out,
@@ -362,7 +376,8 @@ def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int,
     size = n * Hkv * CACHE_PAGE * D
     _check(lib.rudder_cache_dequant(
         c, s, _arr("pages", pages, _I32, n), n, num_pages, Hkv, D,
-        _arr("K_out", K_out, _F32, size), _arr("V_out", V_out, _F32, size), _stream(stream)))
+        _arr("K_out", K_out, _F32, size), _arr("V_out", V_out, _F32, size),
+        _stream_for(stream, codes)))
 
 
 def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
@@ -391,7 +406,7 @@ def rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B: i
         q, _arr("row_start", row_start, _I32, B + 1), _arr("kv_len", kv_len, _I32, B),
         _arr("page_table", page_table, _I32, B * max_pages), c, s, B, T, max_rows, max_kv,
         max_pages, num_pages, Hq, Hkv, D, ldq, ldo, sm, int(causal), w, wbytes, o,
-        _stream(stream)))
+        _stream_for(stream, Q)))
 
 
 def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int, Tkv: int,
@@ -407,7 +422,7 @@ def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int,
     _check(lib.rudder_cross_attention(
         q, k, v, _arr("row_start", row_start, _I32, B + 1), _arr("kv_start", kv_start, _I32, B),
         _arr("kv_len", kv_len, _I32, B), B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk, ldv,
-        ldo, sm, w, wbytes, o, _stream(stream)))
+        ldo, sm, w, wbytes, o, _stream_for(stream, Q)))
 
 
 # ---------------------------------------------------------------------------
