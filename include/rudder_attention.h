@@ -101,12 +101,13 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * head h of Hq and its cached head h / (Hq / Hkv):
  *   o = sum_j softmax_j(sm * q . k_j) v_j,  j < kv, and where causal is
  *       not 0 also j <= kv - n + i
- * A row with no visible token gives zeros, a query row that is not finite NaN.
- * q . k is formed in integers, q rounded to units of 2^-14 of its row's
- * largest power of two (elements within 2^-7 of the largest are exact); the
- * softmax is in fp32, its weights rounded to fp16 for the product with the
- * codes of V, fp32 sums, one rounding to bf16.  V scales below 2^-80 count as
- * 2^-80.
+ * A row whose mask leaves nothing (kv = 0, or i in front of the first token)
+ * gives zeros whatever its query, any other query row that is not finite NaN.
+ * q enters q . k with an absolute error of at most 2^-15 of its row's largest
+ * power of two (2^-14 for an element of magnitude 255/128 times that power);
+ * the products with the codes are exact.  The softmax is in fp32, its weights
+ * rounded to fp16 for the product with the codes of V, fp32 sums, one rounding
+ * to bf16.  V scales below 2^-80 count as 2^-80.
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)

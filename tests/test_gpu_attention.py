@@ -154,6 +154,84 @@ def test_rows_that_are_not_finite(rudder, rows, ctx):
         ref.assert_within("O", got, want, bound)
 
 
+@pytest.mark.parametrize("rows,ctx", [(3, 2), (3, 0), (150, 100), (150, 0), (300, 2000)])
+def test_masked_rows_that_are_not_finite(rudder, rows, ctx):
+    """A row whose mask leaves nothing gives zeros whatever its query, in every kernel, also where
+    the sequence stands beside one that is split over its tokens."""
+    log(f"case masked, not finite rows={rows} ctx={ctx}")
+    g = torch.Generator().manual_seed(36)
+    D, lens = 128, [ctx, 4000]
+    codes, scales, table = _cache(g, lens, 1, D)
+    q = torch.full((2 * rows, 1, D), float("nan"), dtype=torch.bfloat16)
+    q[rows:] = torch.randn(rows, 1, D, generator=g).to(torch.bfloat16)
+    starts = _starts([rows, rows])
+    for causal in (False, True):
+        got = _run_cache(rudder, q, starts, lens, table, codes, scales, 0.1, causal).cpu()
+        none = rows if ctx == 0 else max(rows - ctx, 0) if causal else 0
+        assert not got[:none].any()
+        assert torch.isnan(got[none:rows]).all()
+        assert torch.isfinite(got[rows:]).all()
+
+
+@pytest.mark.parametrize("sm", [0.0, -2.0])
+@pytest.mark.parametrize("rows,causal", [(2, True), (40, True), (300, False)])
+def test_scales_of_the_softmax(rudder, rows, causal, sm):
+    """A softmax scale of zero weighs the visible tokens alike, a negative one turns them round."""
+    log(f"case softmax scale {sm} rows={rows}")
+    g = torch.Generator().manual_seed(37)
+    D, lens = 128, [1100]
+    codes, scales, table = _cache(g, lens, 1, D)
+    q = torch.randn(rows, 1, D, generator=g).to(torch.bfloat16)
+    starts = _starts([rows])
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, causal)
+    got = _run_cache(rudder, q, starts, lens, table, codes, scales, sm, causal)
+    ref.assert_within("O", got, want, bound)
+
+
+@pytest.mark.parametrize("rows,causal", [(1, True), (30, True), (280, False)])
+def test_pages_and_rows_far_apart(rudder, rows, causal):
+    """Pages behind 4 GiB of codes, and query and output rows 2^25 elements apart (280 of them
+    span 17 GiB): offsets pass 32 bits."""
+    log(f"case far apart rows={rows}")
+    g = torch.Generator().manual_seed(38)
+    Hkv, D, ctx, far = 32, 128, 1100, 8400                     # pages of 512 KiB
+    small_codes, small_scales, small_table = _cache(g, [ctx], Hkv, D)
+    n = len(small_codes)
+    codes = torch.zeros(far + n, Hkv, 2, PAGE * D, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(far + n, Hkv, 2, device="cuda")
+    codes[far:], scales[far:] = small_codes.cuda(), small_scales.cuda()
+    table = torch.where(small_table >= 0, small_table + far, small_table)
+    small = torch.randn(rows, Hkv, D, generator=g).to(torch.bfloat16)
+    apart = (1 << 25) if rows > 100 else (1 << 27)
+    wide = torch.empty((rows - 1) * apart + 2 * Hkv * D, dtype=torch.bfloat16, device="cuda")
+    q = wide.as_strided((rows, Hkv, D), (apart, D, 1))
+    out = wide.as_strided((rows, Hkv, D), (apart, D, 1), Hkv * D)
+    q.copy_(small.cuda())
+    starts, heads = _starts([rows]), [0, 31]
+    nb = rudder.attention_workspace_bytes(1, rows, rows, ctx, Hkv, Hkv, D)
+    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device="cuda")
+    rudder.rudder_cache_attention(q, starts.cuda(), torch.tensor([ctx], dtype=torch.int32).cuda(),
+                                  table.cuda(), codes, scales, 1, rows, rows, ctx, table.shape[1],
+                                  far + n, Hkv, Hkv, D, 0.1, causal, ws, out)
+    got = out.cpu()[:, heads]
+    want, bound = ref.cache_attention(small[:, heads], starts, [ctx], small_table,
+                                      small_codes[:, heads], small_scales[:, heads], 0.1, causal)
+    ref.assert_within("O", got, want, bound)
+    assert torch.equal(q.cpu(), small)
+    # the same pages again, written by an append over them
+    k = torch.randn(ctx, Hkv, D, generator=g).to(torch.bfloat16)
+    rudder.cache_append(k.cuda(), k.cuda(), _starts([ctx]).cuda(),
+                        torch.zeros(1, dtype=torch.int32).cuda(), table.cuda(), ctx, codes, scales)
+    pages = table[0, :(ctx + PAGE - 1) // PAGE].cuda()
+    K, V = rudder.cache_dequant(codes, scales, pages)
+    back = K[:, 31].reshape(-1, D)[:ctx].cpu()
+    # half a step of a block whose largest magnitude is below 6
+    assert (back - k[:, 31].float()).abs().max() <= 6 / 127 / 2 * (1 + 2.0 ** -20)
+    K, V = (x.transpose(1, 2).reshape(-1, Hkv, D)[:ctx] for x in (K, V))
+    assert torch.equal(K, V)                       # the slots behind ctx keep their old codes
+    assert not codes[:far].any()
+
+
 def test_long_tables(rudder):
     """More than 64 pages a wave and more than 64 pieces' worth of tiles: page numbers are
     fetched anew."""
@@ -337,6 +415,26 @@ def test_cross_attention(rudder, counts, lens, Hq, Hkv, D, packed):
     got = rudder.cross_attention(q.cuda(), dev[:, :Hkv], dev[:, Hkv:], starts.cuda(),
                                  kv_start.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
                                  max(counts), max(lens), sm)
+    ref.assert_within("O", got, want, bound)
+
+
+def test_cross_rows_far_apart(rudder):
+    """States whose rows are 2^24 elements apart, 200 of them over 6 GiB."""
+    log("case cross far apart")
+    g = torch.Generator().manual_seed(39)
+    H, D, L, apart = 2, 128, 200, 1 << 24
+    wide = torch.empty((L - 1) * apart + 2 * H * D, dtype=torch.bfloat16, device="cuda")
+    K = wide.as_strided((L, H, D), (apart, D, 1))
+    V = wide.as_strided((L, H, D), (apart, D, 1), H * D)
+    k = torch.randn(L, 2 * H, D, generator=g).to(torch.bfloat16)
+    K.copy_(k[:, :H].cuda())
+    V.copy_(k[:, H:].cuda())
+    q = torch.randn(140, H, D, generator=g).to(torch.bfloat16)
+    starts = _starts([140])
+    got = rudder.cross_attention(q.cuda(), K, V, starts.cuda(),
+                                 torch.zeros(1, dtype=torch.int32).cuda(),
+                                 torch.tensor([L], dtype=torch.int32).cuda(), 140, L, 0.1)
+    want, bound = ref.cross_attention(q, k[:, :H], k[:, H:], starts, torch.tensor([0]), [L], 0.1)
     ref.assert_within("O", got, want, bound)
 
 

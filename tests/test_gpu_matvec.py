@@ -47,6 +47,9 @@ def test_preparation_bit_exact(rudder, K, N, group):
     (1, 32, 1, 32), (1, 2048, 256, 128), (2, 96, 33, 32), (5, 320, 17, 64), (16, 1024, 100, 32),
     (17, 640, 48, 128), (40, 4096, 16, 64), (3, 8192, 31, 128), (1, 16384, 20, 32),
     (33, 256, 2050, 64),
+    # two and four channel tiles a workgroup, the last one not full
+    (1, 96, 24590, 32), (6, 128, 24577, 128), (9, 192, 6150, 64), (16, 96, 12300, 32),
+    (13, 384, 12289, 128), (30, 64, 12340, 64), (21, 160, 6177, 32),
 ])
 def test_product(rudder, M, K, N, group, comp):
     log(f"case matvec M={M} K={K} N={N} group={group} comp={comp}")
@@ -92,3 +95,20 @@ def test_rows_are_independent_and_nothing_else_is_written(rudder):
     assert torch.equal(got[keep], clean[keep])
     assert torch.isnan(got[2]).all()
     assert (buf[M * N:] == -3.0).all()
+
+
+def test_codes_far_apart(rudder):
+    """More than 4 GiB of codes: offsets pass 32 bits in preparation and product."""
+    K, N, group, last = 16384, 530011, 128, 100
+    log(f"case matvec far apart K={K} N={N}")
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(2, K, generator=g).to(torch.bfloat16)
+    end = (torch.randn(K, last, generator=g) * 0.02).to(torch.bfloat16)
+    W = torch.zeros(K, N, dtype=torch.bfloat16, device="cuda")
+    W[:, -last:] = end.cuda()
+    Wq, gs = rudder.quantize_weights_grouped(W, group)
+    assert Wq.numel() > 1 << 32
+    want, bound = ref.matvec(x, *ref.group_codes(end, group), group)
+    y = rudder.matvec_w4(x.cuda(), Wq, gs, N, group)
+    ref.assert_within("Y", y[:, -last:], want, bound)
+    assert not y[:, :-last].any()

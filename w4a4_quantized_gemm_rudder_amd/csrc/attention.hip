@@ -19,9 +19,11 @@
 //
 // Cache codes become fp16 operands: 0x6400 | (code ^ 0x80) is the fp16 value
 // 1152 + code, and one packed subtraction leaves the code, exactly.  q is
-// scaled by a power of two to a largest magnitude in [1, 2) and is then
-// exact in fp16, but for elements below 2^-7 of the largest, which keep an
-// absolute error of 2^-25 of it.  The K scale multiplies c.  The V scale sv is
+// scaled by a power of two to a largest magnitude in [1, 2) and is then exact
+// in fp16 down to 2^-17, and off by at most 2^-25 below.  The kernel for few
+// rows multiplies the codes of K as they are, in integers, by q as two digits
+// of 8 bits: its time is the codes' way from HBM, and what it spends beside
+// that on widening them would show.  The K scale multiplies c.  The V scale sv is
 // folded into the exponent: with t_j = z_j + log2(sv) and m the running
 // maximum of t, P_j = exp2(t_j - m) multiplies plain codes, and
 // l = sum P_j / sv.  P is rounded to fp16 (2^-11 relative, absolute 2^-33 below
@@ -534,7 +536,7 @@ attention_tile_kernel(const Problem p) {
         }
         uint32_t top = abs_max_bits<kKS>(q);
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
         if (CACHE) c *= to_f16<kKS>(q, top);
     }
 
@@ -818,7 +820,7 @@ attention_wide_kernel(const Problem p) {
         }
         uint32_t top = abs_max_bits<kKS>(q);
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
         if (CACHE) c *= to_f16<kKS>(q, top);
     }
 
@@ -1083,7 +1085,7 @@ attention_few_kernel(const Problem p) {
             q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
         }
         const uint32_t top = column_max(abs_max_bits<2 * kC>(q));
-        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // a row that is not finite
+        if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
         c *= to_digits<kC>(q, top, high, low);
     }
 
