@@ -159,29 +159,36 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None
+_raw_stream = _get_device = None
 
 
 def _current_stream() -> int:
     """Handle of torch's current stream on the current device."""
-    global _raw_stream
     if _raw_stream is None:
-        import torch
-        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        # the raw handle without a Stream object: a third of the time of current_stream()
-        _raw_stream = ((lambda: get(torch.cuda.current_device())) if get else
-                       (lambda: torch.cuda.current_stream().cuda_stream))
-    return _raw_stream()
+        _stream_getters()
+    return _raw_stream(_get_device())
+
+
+def _stream_getters() -> None:
+    global _raw_stream, _get_device
+    import torch
+    torch.cuda.init()
+    _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    # the raw handle without a Stream object: a third of the time of current_stream()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream_for(stream, t) -> Optional[int]:
     """As _stream; the current stream only for a tensor of the current device."""
-    if stream is None and t.__class__ is not int:
-        import torch
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {t.device}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    if stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        _stream_getters()
+    device = _get_device()
+    if t.__class__ is not int and t.get_device() != device:
+        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{device}")
+    return _raw_stream(device)
 
 
 def _stream(stream) -> Optional[int]:
