@@ -400,6 +400,7 @@ __device__ __forceinline__ void wave_sync() {
 template <int D>
 struct RowSlab {
     static constexpr int kStride = D * 2 + 16, kBytes = kWaveRows * kStride;
+    static constexpr int kPartBytes = kWaveRows * (D * 4 + 16);    // of partial rows in 32 bits
     static constexpr int kPieces = D / 8, kRowsAtOnce = 64 / kPieces;
 
     // Lane l's row (token t, head) for l < 32 -> the lanes' operands of the first product.
@@ -462,27 +463,45 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
         RowSlab<D>::store(p, s, slab, t, head, live, row_factor(l), o);
         return;
     }
-    if (!live) return;
-    const int half = (threadIdx.x & 63) >> 5;
-    const size_t to = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
-    if (half == 0) p.part_ml[to] = make_float2(m, l);
-    float* d = p.part_o + to * D;
+    // through LDS as well, a wave's partial rows lie behind each other (1500 rows of 16 heads of 128
+    // channels over 2048 keys, in two pieces: 51.6 us, 54.2 without)
+    constexpr int kStride = D * 4 + 16, kPieces = D / 4, kRowsAtOnce = 64 / kPieces;
+    const int lane = threadIdx.x & 63;
+    const size_t first = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
+    if (live && lane < kWaveRows) p.part_ml[first] = make_float2(m, l);
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<float4*>(d + dt * 32 + g * 8 + half * 4) = make_float4(
-                o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
+            *reinterpret_cast<float4*>(slab + (lane & 31) * kStride +
+                                       (dt * 32 + g * 8 + (lane >> 5) * 4) * 4) =
+                make_float4(o[dt][4 * g], o[dt][4 * g + 1], o[dt][4 * g + 2], o[dt][4 * g + 3]);
+    wave_sync();
+    // the wave's rows are consecutive, those that are not live the last ones
+    const int rows = __popcll(__ballot(live && lane < kWaveRows));
+    float* to = p.part_o + (first - (lane & 31)) * D + lane * 4;
+#pragma unroll
+    for (int i = 0; i < kWaveRows / kRowsAtOnce; ++i) {
+        const int r = i * kRowsAtOnce + lane / kPieces;
+        if (r < rows)
+            *reinterpret_cast<float4*>(to + i * 256) =
+                *reinterpret_cast<const float4*>(slab + r * kStride + lane % kPieces * 16);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // Many rows: 128 of them a workgroup, four waves of 32 that share the tiles through LDS.
 // ---------------------------------------------------------------------------
+// 64 channels leave room for three workgroups a compute unit: the exponentials and the codes'
+// widening weigh twice as much there as with 128, and a third wave fills what two leave of the
+// vector units, for four registers spilled outside of the loop (2 x 4096 causal rows of 24 heads over
+// 4096 tokens 168 us, with two 215; 8 x 2000 over 2000 131 against 154).
 template <int D, bool CACHE>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, D == 64 ? 3 : 2)
 attention_tile_kernel(const Problem p) {
     using St = Stage<D, CACHE, 256>;
     static_assert(4 * RowSlab<D>::kBytes <= St::kBytes, "a wave's rows fit beside a tile");
+    static_assert(4 * RowSlab<D>::kPartBytes <= 2 * St::kBytes, "and its results in both");
     constexpr int kRows = 4 * kWaveRows;
     constexpr int kKS = D / 16;                    // steps of the first product
     constexpr int kDT = D / 32;                    // channel tiles of the second
@@ -522,31 +541,6 @@ attention_tile_kernel(const Problem p) {
                           tile0 + (split < 0 ? p.most_tiles : p.piece_tiles));
     if (split >= 0 && tile0 * kPage >= s.kv) return;       // the join does not read this piece
 
-    uint4 q[kKS];
-    float l = 0.0f;                                // the lane's share of the sum of weights
-    // the softmax scale's sign goes to the query, so that exponents grow with the products
-    float c = fabsf(p.sm) * kLog2e;
-    {
-        // the second tile's place is free until a barrier has passed
-        RowSlab<D>::load(p, s, lds + St::kBytes + wave * RowSlab<D>::kBytes, t, head, q);
-        const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-        for (int i = 0; i < kKS; ++i) {
-            q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
-        }
-        uint32_t top = abs_max_bits<kKS>(q);
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
-        if (CACHE) c *= to_f16<kKS>(q, top);
-    }
-
-    f32x16_acc o[kDT];
-#pragma unroll
-    for (int i = 0; i < kDT; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -INFINITY, top_lsv = -INFINITY;
-
     int index = -1;
     // the next tile's page that lies in the pool, -1 behind the last tile
     auto next = [&]() {
@@ -572,6 +566,33 @@ attention_tile_kernel(const Problem p) {
             sv = sc[1];
         }
     };
+    load();                                        // on its way beside the query rows
+
+    uint4 q[kKS];
+    float l = 0.0f;                                // the lane's share of the sum of weights
+    // the softmax scale's sign goes to the query, so that exponents grow with the products
+    float c = fabsf(p.sm) * kLog2e;
+    {
+        // the second tile's place is free until a barrier has passed
+        RowSlab<D>::load(p, s, lds + St::kBytes + wave * RowSlab<D>::kBytes, t, head, q);
+        const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int i = 0; i < kKS; ++i) {
+            q[i] = make_uint4(q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip);
+        }
+        uint32_t top = abs_max_bits<kKS>(q);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
+        if (CACHE) c *= to_f16<kKS>(q, top);
+    }
+
+    f32x16_acc o[kDT];
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    float m = -INFINITY, top_lsv = -INFINITY;
+
     // scores of 32 keys: register j holds key 16 (j / 8) + 8 half + j % 8
     const int k_lane = (lane & 31) * St::kKStride + half * 16;
     const int v_lane = St::kKBytes + (lane & 31) * St::kVStride + half * 16;
@@ -597,7 +618,6 @@ attention_tile_kernel(const Problem p) {
 
     // Software pipeline over halves of tiles: while the weights of 32 keys are formed on the vector
     // units, the matrix cores work on the scores of the next 32 and the values of the last 32.
-    load();
     if (page >= 0) {
         uint8_t* cur = lds;                        // holds the tile at hand
         uint8_t* old = lds;                        // the one before
@@ -710,7 +730,7 @@ attention_tile_kernel(const Problem p) {
     }
     l += __shfl_xor(l, 32);
     __syncthreads();                               // the tiles have been read
-    write_rows<D>(p, s, lds + wave * RowSlab<D>::kBytes, split, unit, rest, kRows,
+    write_rows<D>(p, s, lds + wave * RowSlab<D>::kPartBytes, split, unit, rest, kRows,
                   row - tile_row * kRows, t, head, live, m, l, o);
 }
 
@@ -729,6 +749,7 @@ __global__ void __launch_bounds__(512, 2)
 attention_wide_kernel(const Problem p) {
     using St = Stage<D, CACHE, 512>;
     static_assert(8 * RowSlab<D>::kBytes <= 2 * St::kBytes, "a wave's rows fit beside two tiles");
+    static_assert(8 * RowSlab<D>::kPartBytes <= 4 * St::kBytes, "and its results in all four");
     constexpr int kRows = 8 * kWaveRows;
     constexpr int kKS = D / 16, kDT = D / 32;
     __shared__ __align__(16) uint8_t lds[4 * St::kBytes];
@@ -939,7 +960,7 @@ attention_wide_kernel(const Problem p) {
     }
     if (wave < 4) __syncthreads();                 // group B's last phase of products
     l += __shfl_xor(l, 32);
-    write_rows<D>(p, s, lds + wave * RowSlab<D>::kBytes, split, unit, rest, kRows,
+    write_rows<D>(p, s, lds + wave * RowSlab<D>::kPartBytes, split, unit, rest, kRows,
                   row - tile_row * kRows, t, head, live, m, l, o);
 }
 
@@ -1228,55 +1249,74 @@ attention_few_kernel(const Problem p) {
     }
 }
 
-// Joins the pieces of the split units in their order: one wave a row.  unit_rows: rows of a unit.
+// Joins the pieces of the split units in their order, D / 4 lanes a row.  unit_rows: rows of a unit.
+// A chain of dependent loads and little else: what the first pieces left is asked for beside the
+// sequence's place and length, which say how many of them there are (a token over 777 tokens, both
+// kernels: 10.4 us without, 9.4).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(256) attention_join_kernel(const Problem p, int unit_rows) {
-    const int lane = threadIdx.x & 63, rest = p.units - p.whole;
+    constexpr int kFirst = 8, kLanes = D / 4;      // pieces asked for at once; lanes a row
+    const int lane = threadIdx.x % kLanes, rest = p.units - p.whole;
+    const int r = (blockIdx.x * 256 + threadIdx.x) / kLanes;
+    if (r >= unit_rows) return;
+    const size_t stride = (size_t)rest * unit_rows, at = (size_t)blockIdx.y * unit_rows + r;
+    const float* po = p.part_o + at * D + lane * 4;
+    auto piece = [&](int i) {
+        return *reinterpret_cast<const float4*>(po + (size_t)i * stride * D);
+    };
+    float4 first[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+        first[i] = i < p.pieces ? piece(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto stats = [&](int i) {
+        return i < p.pieces ? p.part_ml[(size_t)i * stride + at] : make_float2(-INFINITY, 0.0f);
+    };
+    float2 ml = stats(lane);
     const Place u = place(p, p.whole + blockIdx.y);
     const Sequence s = sequence<CACHE>(p, u.b);
-    const int G = p.Hq / p.Hkv, r = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int G = p.Hq / p.Hkv;
     const int row = u.tile * unit_rows + r;
-    if (r >= unit_rows || row >= min(s.n, p.max_rows) * G) return;
+    if (row >= min(s.n, p.max_rows) * G) return;
     const int t = row / G, head = u.h * G + row % G;
-    const size_t stride = (size_t)rest * unit_rows, at = (size_t)blockIdx.y * unit_rows + r;
     const int used = min(p.pieces, ((s.kv + kPage - 1) / kPage + p.piece_tiles - 1) /
                                        p.piece_tiles);
-    // the pieces' maxima and sums, 64 at a time, one a lane
-    float m = -INFINITY, l = 0.0f, o[D / 64];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) o[j] = 0.0f;
-    for (int i0 = 0; i0 < used; i0 += 64) {
-        const int n = min(used - i0, 64);
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < n) ml = p.part_ml[(size_t)(i0 + lane) * stride + at];
+    // the pieces' maxima and sums, kLanes at a time, one a lane
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < used; i0 += kLanes) {
+        const int n = min(used - i0, kLanes);
+        if (i0) ml = stats(i0 + lane);
+        if (lane >= n) ml = make_float2(-INFINITY, 0.0f);          // nobody wrote these
         float top = fmaxf(m, ml.x);
 #pragma unroll
-        for (int k = 32; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+        for (int k = kLanes / 2; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
         const float base = top == -INFINITY ? 0.0f : top;
         const float w = __builtin_amdgcn_exp2f(ml.x - base);
         const float alpha = __builtin_amdgcn_exp2f(m - base);
         m = top;
         float sum = ml.y * w;
 #pragma unroll
-        for (int k = 32; k; k >>= 1) sum += __shfl_xor(sum, k);
+        for (int k = kLanes / 2; k; k >>= 1) sum += __shfl_xor(sum, k);
         l = fmaf(l, alpha, sum);
+        o = make_float4(o.x * alpha, o.y * alpha, o.z * alpha, o.w * alpha);
+        auto add = [&](float4 x, int i) {
+            const float wi = __shfl(w, i, kLanes);
+            o = make_float4(fmaf(x.x, wi, o.x), fmaf(x.y, wi, o.y), fmaf(x.z, wi, o.z),
+                            fmaf(x.w, wi, o.w));
+        };
+        int i = 0;
+        if (i0 == 0) {
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) o[j] *= alpha;
-        const float* po = p.part_o + ((size_t)i0 * stride + at) * D + lane * (D / 64);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float wi =
-                __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) o[j] = fmaf(po[(size_t)i * stride * D + j], wi, o[j]);
+            for (int f = 0; f < kFirst; ++f)
+                if (f < n) add(first[f], f);
+            i = kFirst;
         }
+#pragma unroll 8
+        for (; i < n; ++i) add(piece(i0 + i), i);
     }
     const float f = row_factor(l);
-    uint16_t* d = p.O + (size_t)(s.r0 + t) * p.ldo + (size_t)head * D + lane * (D / 64);
-    if (D == 128)
-        *reinterpret_cast<uint32_t*>(d) = pack_bf16(o[0] * f, o[D / 64 - 1] * f);
-    else
-        *d = (uint16_t)(pack_bf16(o[0] * f, 0.0f) & 0xFFFFu);
+    *reinterpret_cast<uint2*>(p.O + (size_t)(s.r0 + t) * p.ldo + (size_t)head * D + lane * 4) =
+        make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
 }
 
 // How a call's work is laid out (Problem's fields of the same names).
@@ -1331,13 +1371,22 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
     if (units > (1 << 21)) return false;
     p.tile_rows = (int)tile_rows;
     p.units = (int)units;
-    // a round is what runs at once; what is left over after whole rounds is split into one more
-    // (2 x 4192 rows over 12576 tokens, 544 units: 1188 us whole, 976 split)
-    const int round = p.waves == 8 ? 256 : 512, rest = p.units % round;
-    // (short ones do not repay the join: 512 rows of 16 heads over 512 keys 22.4 us whole, 24.4 in
-    // two; 2 x 4192 rows over 512 keys 66 us whole, 60 with the last 32 of 1056 units in four)
+    // A round is what runs at once.  What is left over after whole rounds, or all where it is less
+    // than one, is split over its keys where that repays the join (us, whole | split):
+    //   - less than a round, 16 heads: 128 channels, two pieces from 32 tiles (1500 rows over 1024
+    //     keys 38.8 | 42, over 2048 keys 71 | 52), four from 16 (900 rows, 1024 keys 38 | 29); 64
+    //     channels, whose rounds are larger, twice as many (2400 rows, 2048 keys 56 | 63, 4096 keys
+    //     100 | 84);
+    //   - behind whole rounds, little of it: from 8 tiles (2 x 4192 rows over 512 keys 66 | 60, over
+    //     12576 keys, 32 of 544 units, 1188 | 976); much: from 64 (288 of 1056 units of 64
+    //     channels, 2048 keys 85 | 95, 6000 keys 288 | 277); never causal ones, whose last units are the
+    //     shortest (3 x 2000 rows of 24 heads 88 | 98).
+    const int round = p.waves == 8 ? 256 : D == 64 ? 768 : 512, rest = p.units % round;
     const bool alone = p.units < round;
-    const bool worth = rest > 0 && rest <= round / 2 && tiles >= (alone ? 16 : 8);
+    const bool worth =
+        rest > 0 && rest <= round / 2 &&
+        (alone ? tiles >= 16 && round / rest * tiles >= (D == 64 ? 128 : 64)
+               : !causal && tiles >= (rest * 8 > round ? 64 : 8));
     split(p, worth ? round / rest : 1, tiles, alone ? 4 : 2);
     p.whole = p.pieces > 1 ? p.units - rest : p.units;
     return true;
@@ -1379,7 +1428,8 @@ hipError_t launch(Problem p, void* workspace, hipStream_t stream) {
     const int64_t rows = (int64_t)p.max_rows * (p.Hq / p.Hkv);
     const unsigned most = (unsigned)(rows < sp.unit_rows ? rows : sp.unit_rows);
     attention_join_kernel<D, CACHE>
-        <<<dim3((most + 3) / 4, p.units - p.whole), 256, 0, stream>>>(p, sp.unit_rows);
+        <<<dim3((most * (D / 4) + 255) / 256, p.units - p.whole), 256, 0, stream>>>(
+            p, sp.unit_rows);
     return hipGetLastError();
 }
 
