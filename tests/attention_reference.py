@@ -125,9 +125,9 @@ def rows_attention(q, k, v, visible, sm, p_half_step, q_step):
     error dz of the exponent, in numerator and denominator: 2 ln 2 dz.  dz: the fp32 product
     of D terms and its scaling, (D + 8) half steps of c sum |q k|; q's own rounding (q_step of the
     row's largest element, for the cache half a unit 2^-14 of the largest power of
-    two in the row, or one unit for the largest itself: 2^-15); three roundings at the exponent's own magnitude and that of
-    log2 of a scale (80 at most).  Then the absolute floor of weights held in fp16 (2^-33 of the
-    largest a key), and the rounding to bf16."""
+    two in the row, or one unit for the largest itself: 2^-15); three roundings at the exponent's
+    own magnitude and that of log2 of a scale (80 at most).  Then the absolute floor of weights
+    held in fp16 (2^-33 of the largest a key), and the rounding to bf16."""
     if not len(k):
         z = torch.zeros(len(q), v.shape[1], dtype=torch.float64)
         return z, z

@@ -84,10 +84,10 @@ __device__ __forceinline__ int quotient(int a, int b) {
 // Unit number -> row tile of a pair.  Workgroups go round robin to the eight dies: where the pairs
 // divide by eight, the units of a pair, which read the same keys, are kept on one (dies = 8, else
 // 1).  A pair's tiles follow each other, causal ones, whose lengths differ, longest first
-// (descending = 1); where the keys of a die take at most half its L2 they go longest first over all its pairs
-// (tile_major = 1), which ends more evenly: 4096 causal rows of 16 heads over 4096 tokens 126 us, pair
-// by pair 162; over 16384 tokens, 2 x 4096 rows, 1077 against 918.  Chosen by arithmetic: a branch by
-// p.causal made two kernels of one and cost 50 registers.
+// (descending = 1); where the keys of a die take at most half its L2 they go longest first over all
+// its pairs (tile_major = 1), which ends more evenly: 4096 causal rows of 16 heads over 4096 tokens
+// 126 us, pair by pair 162; over 16384 tokens, 2 x 4096 rows, 1077 against 918.  Chosen by
+// arithmetic: a branch by p.causal made two kernels of one and cost 50 registers.
 struct Place {
     int h, b, tile;
 };
@@ -395,8 +395,8 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // The 32 query rows of a wave pass through LDS, so that global memory sees whole rows: a lane's
-// share of its row is 16 bytes in 32 (loads) or 8 in 16 (stores).  2 x 4192 rows of 16 heads over 128
-// keys 33.9 us without, of which 6.5 were the loads' and 10 the stores'.
+// share of its row is 16 bytes in 32 (loads) or 8 in 16 (stores).  2 x 4192 rows of 16 heads over
+// 128 keys 33.9 us without, of which 6.5 were the loads' and 10 the stores'.
 template <int D>
 struct RowSlab {
     static constexpr int kStride = D * 2 + 16, kBytes = kWaveRows * kStride;
@@ -463,8 +463,8 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
         RowSlab<D>::store(p, s, slab, t, head, live, row_factor(l), o);
         return;
     }
-    // through LDS as well, a wave's partial rows lie behind each other (1500 rows of 16 heads of 128
-    // channels over 2048 keys, in two pieces: 51.6 us, 54.2 without)
+    // through LDS as well, a wave's partial rows lie behind each other (1500 rows of 16 heads of
+    // 128 channels over 2048 keys, in two pieces: 51.6 us, 54.2 without)
     constexpr int kStride = D * 4 + 16, kPieces = D / 4, kRowsAtOnce = 64 / kPieces;
     const int lane = threadIdx.x & 63;
     const size_t first = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
@@ -492,10 +492,17 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
 // ---------------------------------------------------------------------------
 // Many rows: 128 of them a workgroup, four waves of 32 that share the tiles through LDS.
 // ---------------------------------------------------------------------------
-// 64 channels leave room for three workgroups a compute unit: the exponentials and the codes'
-// widening weigh twice as much there as with 128, and a third wave fills what two leave of the
-// vector units, for four registers spilled outside of the loop (2 x 4096 causal rows of 24 heads over
-// 4096 tokens 168 us, with two 215; 8 x 2000 over 2000 131 against 154).
+// A wave's 32 rows meet 32 keys in 2 D / 16 products of 32 cycles; beside them stand, a lane, 16
+// exponentials of 16 cycles and about 80 vector instructions of 4 (scaling, maximum, sum, rounding,
+// the codes' share of widening).  The pipeline over halves of tiles lets the two overlap within a
+// wave, the second workgroup of the compute unit fills the barriers.  2 x 4192 rows of 16 heads of
+// 128 channels over 512 bf16 keys 57 us (510 TFLOP/s: eight tiles against one load and one store of
+// the rows, 69 MB); 2 x 96 rows over 33536 cached tokens 102 us (520, and 690 counting the quarter
+// of the rows that is empty).
+// 64 channels leave room for three workgroups a compute unit: the exponentials weigh twice as much
+// there as with 128, and a third wave fills what two leave of the vector units, for four registers
+// spilled outside of the loop (2 x 4096 causal rows of 24 heads over 4096 tokens 168 us, with two
+// 215; 8 x 2000 over 2000 131 against 154).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(256, D == 64 ? 3 : 2)
 attention_tile_kernel(const Problem p) {
@@ -740,10 +747,15 @@ attention_tile_kernel(const Problem p) {
 // A wave alternates between a phase of products (scores of the next tile, values of this one) and a
 // phase of vector work (weights of the next tile, staging of a later one).  Waves w and w + 4 share
 // a vector unit and a matrix core and are one phase apart, kept so by a barrier a phase: one has
-// the matrix core while the other has the vector unit.  Tile i lives in slot i % 4 of LDS: group A's
-// phases of tile i are 2 i (products: K of i + 1, V of i) and 2 i + 1 (stores i + 3), B's one later,
-// so that slot (i + 3) % 4 = (i - 1) % 4 was last read in phase 2 i - 1 and is first read in
+// the matrix core while the other has the vector unit.  Tile i lives in slot i % 4 of LDS: group
+// A's phases of tile i are 2 i (products: K of i + 1, V of i) and 2 i + 1 (stores i + 3), B's one
+// later, so that slot (i + 3) % 4 = (i - 1) % 4 was last read in phase 2 i - 1 and is first read in
 // 2 i + 4.
+// 2 x 4192 rows of 16 heads over 12576 cached tokens 920 us, 940 TFLOP/s (a library product of as
+// many operations 715 to 750): the matrix cores are busy 39% of the time, the vector units half of
+// it, LDS 28%; the longer of the two phases sets the pace.  Raised wave priorities, hints to the
+// scheduler and other pairs of waves measured the same or slower (1019, 1040 and 1112 against 1019
+// on one card).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(512, 2)
 attention_wide_kernel(const Problem p) {
@@ -973,7 +985,10 @@ attention_wide_kernel(const Problem p) {
 // of a K row are two product steps of 32 channels (lane quarter g: channels 64 c + 16 g + 8 e +
 // 0..7), the 16 bytes of a V row two steps of 32 tokens (16 g + 8 e + 0..7), and the key at row
 // r of score tile (e, a) is 16 (r / 4) + 8 e + 4 a + r % 4, so that the scores of tiles (e, 0)
-// and (e, 1) are the operand of step e.
+// and (e, 1) are the operand of step e.  48 rows over up to 8192 tokens, 8 heads of 128 channels:
+// 104 us, 5.3 TB/s, where reads of such pieces of 16 KB in random order and nothing else reach 5.6
+// to 5.9.  Scores from fp16 operands took 113 us, loads that stay in the caches 117, three waves a
+// vector unit, which spill, 163.
 typedef float f32x4_acc __attribute__((ext_vector_type(4)));
 typedef int i32x4_acc __attribute__((ext_vector_type(4)));
 
@@ -1228,7 +1243,8 @@ attention_few_kernel(const Problem p) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float wm = lm[w][r];
-            total = fmaf(ll[w][r], wm == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(wm - best), total);
+            total = fmaf(ll[w][r], wm == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(wm - best),
+                         total);
             const float4 x = *reinterpret_cast<const float4*>(&lo[w][r][d]);
             a.x += x.x;
             a.y += x.y;
@@ -1249,10 +1265,10 @@ attention_few_kernel(const Problem p) {
     }
 }
 
-// Joins the pieces of the split units in their order, D / 4 lanes a row.  unit_rows: rows of a unit.
-// A chain of dependent loads and little else: what the first pieces left is asked for beside the
-// sequence's place and length, which say how many of them there are (a token over 777 tokens, both
-// kernels: 10.4 us without, 9.4).
+// Joins the pieces of the split units in their order, D / 4 lanes a row; unit_rows: rows of a
+// unit.  A chain of dependent loads and little else: what the first pieces left is asked for beside
+// the sequence's place and length, which say how many of them there are (a token over 777 tokens,
+// both kernels: 10.4 us without, 9.4).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(256) attention_join_kernel(const Problem p, int unit_rows) {
     constexpr int kFirst = 8, kLanes = D / 4;      // pieces asked for at once; lanes a row
@@ -1346,7 +1362,8 @@ void split(Plan& p, int64_t wanted, int tiles, int least) {
 // 512 tokens 8.9 [1]; 777 tokens 12.2 [1], 10.6 [4]; 4096 tokens 17.8 [4], 14.1 [16]; 16384 tokens
 // 23.3 [16], 26 [32]; 65536 tokens 56 [32], 65 [64].  A single unit draws about 50 GB/s, so that up
 // to 4096 tiles one workgroup a unit is best and above two; from 256 (sequence, head) pairs on,
-// ragged lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135 [2]).
+// ragged lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135
+// [2]).
 // False for more workgroups than a launch takes.
 bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int Hkv, int D,
           Plan& p) {
@@ -1363,8 +1380,8 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
         return pairs * p.pieces <= (1 << 22);
     }
     // 256 rows a workgroup where every row sees long stretches of keys (128 channels: 2 x 4096 rows
-    // over 16384 tokens 1149 us, 1311 with 128; 4 x 1000 over 1000 50 against 55; causal 941 against
-    // 918, and with 64 channels 925 against 886)
+    // over 16384 tokens 1149 us, 1311 with 128; 4 x 1000 over 1000 50 against 55; causal 941
+    // against 918, and with 64 channels 925 against 886)
     p.waves = D == 128 && !causal && rows > 128 && tiles >= 16 ? 8 : 4;
     p.unit_rows = kWaveRows * p.waves;
     const int64_t tile_rows = (rows + p.unit_rows - 1) / p.unit_rows, units = tile_rows * pairs;
@@ -1373,21 +1390,22 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
     p.units = (int)units;
     // A round is what runs at once.  What is left over after whole rounds, or all where it is less
     // than one, is split over its keys where that repays the join (us, whole | split):
-    //   - less than a round, 16 heads: 128 channels, two pieces from 32 tiles (1500 rows over 1024
-    //     keys 38.8 | 42, over 2048 keys 71 | 52), four from 16 (900 rows, 1024 keys 38 | 29); 64
-    //     channels, whose rounds are larger, twice as many (2400 rows, 2048 keys 56 | 63, 4096 keys
-    //     100 | 84);
-    //   - behind whole rounds, little of it: from 8 tiles (2 x 4192 rows over 512 keys 66 | 60, over
-    //     12576 keys, 32 of 544 units, 1188 | 976); much: from 64 (288 of 1056 units of 64
-    //     channels, 2048 keys 85 | 95, 6000 keys 288 | 277); never causal ones, whose last units are the
-    //     shortest (3 x 2000 rows of 24 heads 88 | 98).
+    //   - less than a round, the sooner the fewer: with 16 heads of 128 channels two pieces from 32
+    //     tiles (1500 rows over 1024 keys 38.8 | 42, over 2048 keys 71 | 52), four from 16 (900
+    //     rows, 1024 keys 38 | 29), more from 4 (one row, 300 keys 13.6 | 11.6, 900 keys 29.6 |
+    //     12.0); 64 channels, whose rounds are larger, from twice as many (2400 rows, 2048 keys
+    //     56 | 63, 4096 keys 100 | 84);
+    //   - behind whole rounds, little of it: from 8 tiles (2 x 4192 rows over 512 keys 66 | 60,
+    //     over 12576 keys, 32 of 544 units, 1188 | 976); much: from 64 (288 of 1056 units of 64
+    //     channels, 2048 keys 85 | 95, 6000 keys 288 | 277); never causal ones, whose last units
+    //     are the shortest (3 x 2000 rows of 24 heads 88 | 98).
     const int round = p.waves == 8 ? 256 : D == 64 ? 768 : 512, rest = p.units % round;
     const bool alone = p.units < round;
     const bool worth =
         rest > 0 && rest <= round / 2 &&
-        (alone ? tiles >= 16 && round / rest * tiles >= (D == 64 ? 128 : 64)
+        (alone ? tiles >= 4 && round / rest * tiles >= (D == 64 ? 128 : 64)
                : !causal && tiles >= (rest * 8 > round ? 64 : 8));
-    split(p, worth ? round / rest : 1, tiles, alone ? 4 : 2);
+    split(p, worth ? round / rest : 1, tiles, 2);
     p.whole = p.pieces > 1 ? p.units - rest : p.units;
     return true;
 }

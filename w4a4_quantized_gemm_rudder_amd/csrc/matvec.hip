@@ -46,8 +46,8 @@ __global__ void quantize_weights_grouped_kernel(const uint16_t* __restrict__ W, 
     const uint32_t sb = float_to_bf16_bits((float)((double)amax / 7.0));
     const float inv = step_reciprocal(bf16_bits_to_float(sb));
     const int groups = kTileK / group;             // of a tile
-    g_scale[(((size_t)(n / kTileN) * k_tiles + g / groups) * kTileN + (n % kTileN) / 4 * 4) * groups +
-            (g % groups) * 4 + n % 4] = (uint16_t)sb;
+    const size_t of_tile = ((size_t)(n / kTileN) * k_tiles + g / groups) * kTileN * groups;
+    g_scale[of_tile + (n % kTileN) / 4 * 4 * groups + (g % groups) * 4 + n % 4] = (uint16_t)sb;
     // a dword holds k = 32 * step + 8 * quarter + 0..7: code 2p in nibble p, 2p + 1 in p + 4
     for (int k = k0; k < k0 + group; k += 8) {
         uint32_t word = 0;
@@ -222,8 +222,9 @@ matvec_w4_kernel(const uint16_t* __restrict__ X, const uint8_t* __restrict__ sid
 
 // Waves and channel tiles a workgroup, measured over K 2048..16384, N 2048..24576 and M 1..16:
 //   - up to 8 rows, 8 waves and one tile (K = 4096, N = 12288, M = 1: 6.7 us; 16 waves 7.2); from
-//     K = 8192 on 16 waves, which divide the longer loop (K = 16384, N = 4096: 8.6 against 10.8 us);
-//     from 1536 tiles on two share the activations (K = 4096, N = 24576: 10.6 against 11.2 us);
+//     K = 8192 on 16 waves, which divide the longer loop (K = 16384, N = 4096: 8.6 against 10.8
+//     us); from 1536 tiles on two share the activations (K = 4096, N = 24576: 10.6 against 11.2
+//     us);
 //   - more rows make the activations the larger part of what a workgroup reads, so two tiles share
 //     them from 384 tiles on (M = 16, K = 16384, N = 8192: 17.3 against 19.6 us) and four from 768
 //     on (K = 8192, N = 12288: 13.9 against 15.3 us); below, the compute units would run short.
