@@ -30,7 +30,7 @@
 // 2^-22); the sum l is formed from the unrounded values.
 #include <cmath>
 
-#include "rudder_internal.h"
+#include "rudder_operators.h"
 
 namespace rudder {
 namespace {

@@ -11,7 +11,7 @@
 // rescaled, c' = rne(c * fl32(s / s')).  One workgroup owns one (page, head,
 // K|V), so that maximum, rescaling and writing need no other synchronization.
 // Both kernels move bytes and compute next to nothing.
-#include "rudder_internal.h"
+#include "rudder_operators.h"
 
 namespace rudder {
 namespace {

@@ -16,7 +16,7 @@
 // in fp32, once per group.  The difference cancels: each of the two sums is
 // rounded in fp32 at a magnitude up to about 40 times that of the result, an
 // error of a few 2^-19 relative, 2^-10 of the rounding of the bf16 output.
-#include "rudder_internal.h"
+#include "rudder_operators.h"
 
 namespace rudder {
 namespace {

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "rudder_internal.h"
+#include "rudder_operators.h"
 
 namespace {
 
