@@ -29,9 +29,9 @@
  *           tokens 64 i .. 64 i + 63
  * A value is fl32(code * scale).  Pages belong to the caller: sequences may
  * share pages that no append writes to.
- * Undefined behaviour (not checked): non-finite keys, values or scales, two
- * sequences of one append call that write to the same page, overlapping
- * buffers.
+ * Undefined results (not checked; no access leaves the buffers): non-finite
+ * keys, values or scales, sequences of one append call that write to the same
+ * page, or one that lists it twice, overlapping buffers.
  */
 #ifndef RUDDER_ATTENTION_H
 #define RUDDER_ATTENTION_H

@@ -158,3 +158,23 @@ def test_binding_checks_tensors(r):
     with pytest.raises(r.RudderError) as e:
         r.rudder_cache_attention(**{**ok, **addresses, "sm": float("nan")})
     assert e.value.status == r.RUDDER_ERR_INVALID_ARG
+
+
+def test_binding_checks_arguments(r):
+    """What is neither a tensor nor an address, sizes that are no 32-bit integers, tensors without
+    memory and wrong argument counts are Python errors, and nothing is called."""
+    ok = dict(X=P, stream_id=None, Wq=P, g_scale=P, comp_a=None, comp_b=None, M=0, N=64, K=128,
+              group=64, S=1, Y=P, stream=0)
+    r.rudder_matvec_w4(**ok)
+    for kw, error in ((dict(X="rows"), TypeError), (dict(X=3.5), TypeError),
+                      (dict(M=1 << 32), OverflowError), (dict(N=-(1 << 40)), OverflowError),
+                      (dict(K=128.0), TypeError), (dict(X=-1 << 70), OverflowError),
+                      (dict(X=torch.empty(0, 128, dtype=torch.bfloat16, device="meta")),
+                       ValueError)):
+        with pytest.raises(error):
+            r.rudder_matvec_w4(**{**ok, **kw})
+    with pytest.raises(TypeError):
+        r._load_bind().matvec_w4(P, None)
+    with pytest.raises(ImportError):
+        r._load_bind().use("/nowhere/librudder.so")
+    r.rudder_matvec_w4(**ok)

@@ -3,7 +3,9 @@
 Every translation unit under csrc/ is compiled for gfx950 only, with fp
 contraction off (the epilogue's single fma is explicit) and packed-fp32
 instruction selection disabled, then linked into one shared library next to
-this file (_lib/librudder.so).
+this file (_lib/librudder.so).  csrc/bind.cpp, host code, becomes the Python
+module that checks and passes on the arguments of small calls
+(_lib/rudder_bind.so).
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 GEN_DIR = os.path.join(BUILD_DIR, "gen")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "librudder.so")
+BIND_PATH = os.path.join(LIB_DIR, "rudder_bind.so")
 ARCH = os.environ.get("RUDDER_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -63,13 +66,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_bind() -> str:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BIND_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{INCLUDE}", "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(base, "include"), os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+           f"-L{os.path.join(base, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     generate_tables()
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        bind = ex.submit(build_bind)
         objs = list(ex.map(_compile, srcs))
+        bind.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

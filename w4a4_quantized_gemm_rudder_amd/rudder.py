@@ -29,6 +29,7 @@ from typing import Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "librudder.so")
+BIND_PATH = os.path.join(HERE, "_lib", "rudder_bind.so")
 
 CODES_INT = 0       # int4 split-nibble / int8 codes (int8 matrix cores)
 CODES_E2M3 = 1      # codes held as FP6 E2M3 (8-bit codes as two digit planes); f8f6f4 MFMA
@@ -55,6 +56,7 @@ EXPORTED = (
 )
 
 _lib: Optional[ctypes.CDLL] = None
+_bind = None
 
 
 class RudderError(RuntimeError):
@@ -68,11 +70,6 @@ def load_library() -> ctypes.CDLL:
     global _lib
     if _lib is not None:
         return _lib
-    import torch
-    for types, names in ((_BF16, (torch.bfloat16, torch.int16, torch.uint16)),
-                         (_F32, (torch.float32,)), (_I32, (torch.int32,)), (_I8, (torch.int8,)),
-                         (_U8, (torch.uint8,))):
-        types[:] = names
     if not os.path.exists(LIB_PATH):
         raise RudderError(RUDDER_ERR_HIP,
                           f"{LIB_PATH} not found: build it with __graft_entry__.build() "
@@ -141,6 +138,24 @@ def load_library() -> ctypes.CDLL:
     return lib
 
 
+def _load_bind():
+    """The module that checks and passes on the arguments of the operators between
+    the linears, bound to the loaded library; raises if it has not been built."""
+    global _bind
+    import importlib.util
+    import torch  # noqa: F401  (its libraries come first)
+    load_library()
+    if not os.path.exists(BIND_PATH):
+        raise RudderError(RUDDER_ERR_HIP,
+                          f"{BIND_PATH} not found: build it with __graft_entry__.build() "
+                          "or python -m w4a4_quantized_gemm_rudder_amd.build")
+    spec = importlib.util.spec_from_file_location("rudder_bind", BIND_PATH)
+    bind = importlib.util.module_from_spec(spec)
+    bind.use(LIB_PATH)
+    _bind = bind
+    return bind
+
+
 def _check(status: int) -> None:
     if status:
         lib = load_library()
@@ -186,7 +201,7 @@ def _stream_for(stream, t) -> Optional[int]:
     if _raw_stream is None:
         _stream_getters()
     device = _get_device()
-    if t.__class__ is not int and t.get_device() != device:
+    if t is not None and t.__class__ is not int and t.get_device() != device:
         raise ValueError(f"tensors on {t.device}, but the current device is cuda:{device}")
     return _raw_stream(device)
 
@@ -282,47 +297,10 @@ def rudder_stream_sq_error(Y, Yref, stream_id, M: int, N: int, S: int, workspace
 
 # ---------------------------------------------------------------------------
 # Few-row products, cache and attention (include/rudder_attention.h).  Tensors
-# are checked for their type and size against the sizes passed; device
+# are checked for their type, layout and size against the sizes passed, in
+# csrc/bind.cpp: in Python that took as long as the smallest calls.  Device
 # addresses (ints) pass through unchecked.
 # ---------------------------------------------------------------------------
-
-# torch types an argument may have; filled when the library is loaded (importing
-# this module does not import torch)
-_BF16, _F32, _I32, _I8, _U8 = [], [], [], [], []
-
-
-def _arr(name, t, types: list, least: int) -> Optional[int]:
-    """Device address of a contiguous tensor of one of the named types with at
-    least that many elements (None -> NULL)."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype in types and t.numel() >= least and t.is_contiguous():
-        if t.is_cuda:
-            return t.data_ptr()
-        raise ValueError(f"{name}: not on a GPU")
-    raise ValueError(f"{name}: {t.dtype}, {t.numel()} elements, strides {t.stride()}: expected "
-                     f"at least {least} contiguous elements of "
-                     f"{' or '.join(str(d) for d in types)}")
-
-
-def _rows(name, t, T: int, H: int, D: int, ld: Optional[int]):
-    """(address, row distance) of T rows of H heads of D values: [T, H, D] or
-    [T, H * D], a row's values packed, rows any distance apart."""
-    if t is None or t.__class__ is int:
-        return t, H * D if ld is None else ld
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        packed = shape[1] == H and shape[2] == D and st[2] == 1 and (st[1] == D or H == 1)
-    else:
-        packed = len(shape) == 2 and shape[1] == H * D and st[1] == 1
-    if not packed or shape[0] < T or t.dtype not in _BF16 or (ld is not None and ld != st[0]):
-        raise ValueError(f"{name}: {t.dtype}, shape {tuple(shape)}, strides {st}: expected at "
-                         f"least {T} rows of {H} x {D} packed bf16 values"
-                         + ("" if ld is None else f", {ld} apart"))
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not on a GPU")
-    return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], H * D)
-
 
 def grouped_weight_bytes(K: int, N: int) -> int:
     return int(load_library().rudder_grouped_weight_bytes(K, N))
@@ -334,57 +312,36 @@ def grouped_scale_count(K: int, N: int, group: int) -> int:
 
 def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
                                     stream=None) -> None:
-    lib = _lib or load_library()
-    _check(lib.rudder_quantize_weights_grouped(
-        _arr("W", W, _BF16, K * N), K, N, group,
-        _arr("Wq", Wq, _U8, grouped_weight_bytes(K, N)),
-        _arr("g_scale", g_scale, _BF16, grouped_scale_count(K, N, group)), _stream_for(stream, W)))
+    bind = _bind or _load_bind()
+    _check(bind.quantize_weights_grouped(W, K, N, group, Wq, g_scale, _stream_for(stream, W)))
 
 
 def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, K: int,
                      group: int, S: int, Y, stream=None) -> None:
-    lib = _lib or load_library()
-    n_pad, k_tiles = (N + 15) // 16 * 16, (K + 127) // 128
-    _check(lib.rudder_matvec_w4(
-        _arr("X", X, _BF16, M * K), _arr("stream_id", stream_id, _U8, M),
-        _arr("Wq", Wq, _U8, k_tiles * 64 * n_pad),
-        _arr("g_scale", g_scale, _BF16, k_tiles * (128 // max(group, 1)) * n_pad),
-        _arr("comp_a", comp_a, _F32, S * N), _arr("comp_b", comp_b, _F32, S * N), M, N, K, group,
-        S, _arr("Y", Y, _BF16, M * N), _stream_for(stream, X)))
+    bind = _bind or _load_bind()
+    _check(bind.matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y,
+                          _stream_for(stream, X)))
 
 
 def cache_page_bytes(Hkv: int, D: int) -> int:
     return int(load_library().rudder_cache_page_bytes(Hkv, D))
 
 
-def _cache(codes, scales, num_pages: int, Hkv: int, D: int):
-    blocks = num_pages * Hkv * 2
-    return (_arr("codes", codes, _I8, blocks * CACHE_PAGE * D),
-            _arr("scales", scales, _F32, blocks))
-
-
 def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_rows: int,
                         max_pages: int, num_pages: int, Hkv: int, D: int, codes, scales,
                         stream=None, ldk=None, ldv=None) -> None:
-    lib = _lib or load_library()
-    k, ldk = _rows("K", K, T, Hkv, D, ldk)
-    v, ldv = _rows("V", V, T, Hkv, D, ldv)
-    c, s = _cache(codes, scales, num_pages, Hkv, D)
-    _check(lib.rudder_cache_append(
-        k, v, _arr("row_start", row_start, _I32, B + 1), _arr("pos", pos, _I32, B),
-        _arr("page_table", page_table, _I32, B * max_pages), B, T, max_rows, max_pages, num_pages,
-        Hkv, D, ldk, ldv, c, s, _stream_for(stream, codes)))
+    """K, V: [T, Hkv, D] or [T, Hkv * D], rows any distance apart."""
+    bind = _bind or _load_bind()
+    _check(bind.cache_append(K, V, row_start, pos, page_table, B, T, max_rows, max_pages,
+                             num_pages, Hkv, D, codes, scales, _stream_for(stream, codes), ldk,
+                             ldv))
 
 
 def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int, D: int, K_out,
                          V_out, stream=None) -> None:
-    lib = _lib or load_library()
-    c, s = _cache(codes, scales, num_pages, Hkv, D)
-    size = n * Hkv * CACHE_PAGE * D
-    _check(lib.rudder_cache_dequant(
-        c, s, _arr("pages", pages, _I32, n), n, num_pages, Hkv, D,
-        _arr("K_out", K_out, _F32, size), _arr("V_out", V_out, _F32, size),
-        _stream_for(stream, codes)))
+    bind = _bind or _load_bind()
+    _check(bind.cache_dequant(codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out,
+                              _stream_for(stream, codes)))
 
 
 def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
@@ -393,43 +350,25 @@ def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: in
                                                                D))
 
 
-def _workspace(t):
-    """(address, bytes) of a workspace tensor."""
-    if t is None or t.__class__ is int:
-        return t, 0 if t is None else (1 << 63) - 1
-    return _arr("workspace", t, _U8, 0), t.numel()
-
-
 def rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B: int, T: int,
                            max_rows: int, max_kv: int, max_pages: int, num_pages: int, Hq: int,
                            Hkv: int, D: int, sm: float, causal: bool, workspace, O, stream=None,
                            ldq=None, ldo=None) -> None:
-    lib = _lib or load_library()
-    q, ldq = _rows("Q", Q, T, Hq, D, ldq)
-    o, ldo = _rows("O", O, T, Hq, D, ldo)
-    c, s = _cache(codes, scales, num_pages, Hkv, D)
-    w, wbytes = _workspace(workspace)
-    _check(lib.rudder_cache_attention(
-        q, _arr("row_start", row_start, _I32, B + 1), _arr("kv_len", kv_len, _I32, B),
-        _arr("page_table", page_table, _I32, B * max_pages), c, s, B, T, max_rows, max_kv,
-        max_pages, num_pages, Hq, Hkv, D, ldq, ldo, sm, int(causal), w, wbytes, o,
-        _stream_for(stream, Q)))
+    """Q, O: [T, Hq, D] or [T, Hq * D], rows any distance apart."""
+    bind = _bind or _load_bind()
+    _check(bind.cache_attention(Q, row_start, kv_len, page_table, codes, scales, B, T, max_rows,
+                                max_kv, max_pages, num_pages, Hq, Hkv, D, sm, causal, workspace,
+                                O, _stream_for(stream, Q), ldq, ldo))
 
 
 def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int, Tkv: int,
                            max_rows: int, max_kv: int, Hq: int, Hkv: int, D: int, sm: float,
                            workspace, O, stream=None, ldq=None, ldk=None, ldv=None,
                            ldo=None) -> None:
-    lib = _lib or load_library()
-    q, ldq = _rows("Q", Q, T, Hq, D, ldq)
-    k, ldk = _rows("K", K, Tkv, Hkv, D, ldk)
-    v, ldv = _rows("V", V, Tkv, Hkv, D, ldv)
-    o, ldo = _rows("O", O, T, Hq, D, ldo)
-    w, wbytes = _workspace(workspace)
-    _check(lib.rudder_cross_attention(
-        q, k, v, _arr("row_start", row_start, _I32, B + 1), _arr("kv_start", kv_start, _I32, B),
-        _arr("kv_len", kv_len, _I32, B), B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk, ldv,
-        ldo, sm, w, wbytes, o, _stream_for(stream, Q)))
+    bind = _bind or _load_bind()
+    _check(bind.cross_attention(Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows, max_kv,
+                                Hq, Hkv, D, sm, workspace, O, _stream_for(stream, Q), ldq, ldk,
+                                ldv, ldo))
 
 
 # ---------------------------------------------------------------------------
