@@ -1042,7 +1042,10 @@ attention_few_kernel(const Problem p) {
     __shared__ float lo[WAVES][16][D + 4];
     __shared__ float lm[WAVES][16], ll[WAVES][16];
 
-    const int unit = quotient(blockIdx.x, p.pieces), split = blockIdx.x - unit * p.pieces;
+    // all pairs' first pieces, then the second ones: every die has its share of each, and short
+    // sequences, which have no last pieces, end the launch early (768 pairs, up to 8192 tokens, two
+    // pieces: 227 us pair by pair, 211)
+    const int split = quotient(blockIdx.x, p.units), unit = blockIdx.x - split * p.units;
     const int b = quotient(unit, p.Hkv), h = unit - b * p.Hkv;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -1358,12 +1361,16 @@ void split(Plan& p, int64_t wanted, int tiles, int least) {
 }
 
 // Enough workgroups for the 256 compute units where sequences, heads and query rows give fewer.
-// Few rows, measured with 16 heads of 128 channels, one sequence (us, pieces a head in brackets):
-// 512 tokens 8.9 [1]; 777 tokens 12.2 [1], 10.6 [4]; 4096 tokens 17.8 [4], 14.1 [16]; 16384 tokens
-// 23.3 [16], 26 [32]; 65536 tokens 56 [32], 65 [64].  A single unit draws about 50 GB/s, so that up
-// to 4096 tiles one workgroup a unit is best and above two; from 256 (sequence, head) pairs on,
-// ragged lengths want shorter pieces (48 sequences of up to 8192 tokens, 8 heads: 110 [3], 135
-// [2]).
+// Few rows, 128 channels, in us with the pieces of a (sequence, head) pair in brackets; a compute
+// unit draws about 50 GB/s, a join costs about 2 us:
+//   - short stretches, and what is short for many pairs, stay whole: 16 pairs, 512 tokens 9.2 [1],
+//     9.1 [8]; up to 777 tokens of 192 pairs 12.9 [1], 15.2 [2], up to 2048 of 256 23.8 [1], 30.0
+//     [4], up to 1500 of 384 29.6 [1], 31.2 [2];
+//   - else one workgroup a unit up to 4096 tiles, above two, but pieces of two tiles and more, and
+//     of four where that makes more than eight: 16 pairs, 777 tokens 10.2 [4], 9.5 [8]; 2048 tokens
+//     9.9 [8], 12.0 [16]; 65536 tokens 56 [32], 65 [64];
+//   - from 256 pairs on four a unit and three a pair at least, for ragged lengths: up to 8192
+//     tokens of 384 pairs 129 [1], 109 [3], of 768 211 [2], 204 [3].
 // False for more workgroups than a launch takes.
 bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int Hkv, int D,
           Plan& p) {
@@ -1375,8 +1382,12 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
         p.unit_rows = kFewRows;
         p.tile_rows = 1;
         p.units = (int)pairs;
-        const int64_t want = pairs >= 256 ? 1024 : pairs * tiles <= 4096 ? 256 : 512;
-        split(p, tiles * D <= 8 * 128 ? 1 : (want + pairs - 1) / pairs, tiles, kFewWaves);
+        const bool whole = tiles * D <= 8 * 128 ||
+                           (pairs >= 128 && tiles <= (pairs <= 256 ? pairs / 6 : 24));
+        const int64_t want = pairs >= 256 ? (pairs > 341 ? 3 * pairs : 1024)
+                                          : pairs * tiles <= 4096 ? 256 : 512;
+        const int64_t most = tiles / 4 > 8 ? tiles / 4 : 8, each = (want + pairs - 1) / pairs;
+        split(p, whole ? 1 : each < most ? each : most, tiles, 2);
         return pairs * p.pieces <= (1 << 22);
     }
     // 256 rows a workgroup where every row sees long stretches of keys (128 channels: 2 x 4096 rows
