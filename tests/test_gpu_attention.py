@@ -232,6 +232,41 @@ def test_pages_and_rows_far_apart(rudder, rows, causal):
     assert not codes[:far].any()
 
 
+@pytest.mark.parametrize("D,causal", [(64, True), (128, False), (128, True)])
+def test_loose_bounds(rudder, D, causal):
+    """max_rows and max_kv far above what the sequences hold, and sequences of very different
+    lengths beside each other: other kernels and splits, the same results within the bounds."""
+    log(f"case loose bounds D={D} causal={causal}")
+    g = torch.Generator().manual_seed(40)
+    counts, lens = [1, 5, 0, 40, 3], [1, 700, 64, 2100, 3]
+    codes, scales, table = _cache(g, lens, 2, D)
+    starts = _starts(counts)
+    q = torch.randn(int(starts[-1]), 4, D, generator=g).to(torch.bfloat16)
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, 0.1, causal)
+    for max_rows, max_kv in ((40, 2100), (49, 100000), (1 << 20, 1 << 20), (129, 2304)):
+        got = _run_cache(rudder, q, starts, lens, table, codes, scales, 0.1, causal, max_rows,
+                         max_kv)
+        ref.assert_within(f"O {max_rows} {max_kv}", got, want, bound)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_tokens(rudder, D):
+    """Single tokens of many sequences with ragged contexts: whole stretches, two pieces and three
+    a pair."""
+    g = torch.Generator().manual_seed(41)
+    for B, H, ctx in ((20, 8, 300), (24, 12, 2100), (90, 5, 1800)):
+        log(f"case many tokens D={D} B={B} H={H} ctx={ctx}")
+        lens = torch.randint(1, ctx + 1, (B,), generator=g).tolist()
+        lens[3], lens[4] = ctx, 0
+        codes, scales, table = _cache(g, lens, H, D)
+        starts = _starts([1] * B)
+        q = torch.randn(B, H, D, generator=g).to(torch.bfloat16)
+        heads = [0, H - 1]
+        want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, 0.1, True, heads)
+        got = _run_cache(rudder, q, starts, lens, table, codes, scales, 0.1, True)
+        ref.assert_within("O", got[:, heads], want[:, heads], bound[:, heads])
+
+
 def test_long_tables(rudder):
     """More than 64 pages a wave and more than 64 pieces' worth of tiles: page numbers are
     fetched anew."""
