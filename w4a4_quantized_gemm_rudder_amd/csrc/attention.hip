@@ -751,11 +751,11 @@ attention_tile_kernel(const Problem p) {
 // A's phases of tile i are 2 i (products: K of i + 1, V of i) and 2 i + 1 (stores i + 3), B's one
 // later, so that slot (i + 3) % 4 = (i - 1) % 4 was last read in phase 2 i - 1 and is first read in
 // 2 i + 4.
-// 2 x 4192 rows of 16 heads over 12576 cached tokens 920 us, 940 TFLOP/s (a library product of as
-// many operations 715 to 750): the matrix cores are busy 39% of the time, the vector units half of
-// it, LDS 28%; the longer of the two phases sets the pace.  Raised wave priorities, hints to the
-// scheduler and other pairs of waves measured the same or slower (1019, 1040 and 1112 against 1019
-// on one card).
+// 2 x 4192 rows of 16 heads over 12576 cached tokens 920 to 940 us, 930 TFLOP/s (a library product
+// of as many operations 715 to 750): the matrix cores are busy 39% of the time, the vector units
+// half of it, LDS 28%; the longer of the two phases sets the pace.  Raised wave priorities, hints
+// to the scheduler and other pairs of waves measured the same or slower (1019, 1040 and 1112
+// against 1019 on one card).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(512, 2)
 attention_wide_kernel(const Problem p) {
