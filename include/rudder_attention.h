@@ -144,7 +144,8 @@ rudder_status_t rudder_cache_attention(const uint16_t* Q, const int32_t* row_sta
  *   kv_start  int32 [B]: sequence b's first key row (a padded batch has
  *             b * length, a packed one the sums of the lengths)
  *   kv_len    int32 [B]: its keys; rows behind them are not read
- * Products in bf16 with fp32 sums, the softmax weights rounded to bf16.
+ * Products in bf16 with fp32 sums, the softmax weights as the sum of two bf16
+ * numbers (2^-16 relative).
  * Errors: as rudder_cache_attention, also for K, V, ldk, ldv, Tkv < 0.
  */
 rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, const uint16_t* V,

@@ -1,0 +1,63 @@
+"""Cross attention where its roundings and its checks of a row show: weights that cancel, softmax
+scales of zero, below zero and of any size, queries that are not finite, single rows with strides
+of their own; on the kernels of 128 and of 256 rows a workgroup, whole and split over the keys."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+from gpu_harness import log
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rudder():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    from w4a4_quantized_gemm_rudder_amd import rudder as r
+    r.load_library()
+    return r
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def _cross(rudder, q, k, v, counts, lens, sm, max_kv=None):
+    starts = _i32([0] + counts).cumsum(0).to(torch.int32)
+    kv_start = _i32([0] + lens).cumsum(0).to(torch.int32)[:-1]
+    got = rudder.cross_attention(q.cuda(), k.cuda(), v.cuda(), starts.cuda(), kv_start.cuda(),
+                                 _i32(lens).cuda(), max(counts),
+                                 max(lens) if max_kv is None else max_kv, sm)
+    return got.cpu(), starts, kv_start
+
+
+# rows a sequence, bound on the keys, D: one tile of 128 rows, tiles split over the keys, 256 rows
+# a workgroup (128 channels, over 128 rows, 16 tiles of keys and more)
+KERNELS = [(1, 64, 64), (40, 64, 128), (3, 2000, 64), (140, 300, 128), (300, 1200, 128)]
+
+
+@pytest.mark.parametrize("rows,max_kv,D", KERNELS)
+def test_weights_keep_their_bits(rudder, rows, max_kv, D):
+    """Values of +1 and -1 in equal shares under weights that differ by a few percent: the outputs
+    are differences of weights, so that a weight's rounding shows in them, not beside the
+    outputs' own.  Weights count with half a step of 2^-16: the rounding of a rounding's rest."""
+    log(f"case weights rows={rows} max_kv={max_kv} D={D}")
+    g = torch.Generator().manual_seed(81)
+    counts, lens, H = [rows, max(rows - 1, 1)], [2, 48], 2
+    q = torch.randn(sum(counts), H, D, generator=g).to(torch.bfloat16)
+    k = (torch.randn(sum(lens), H, D, generator=g) * 0.1).to(torch.bfloat16)
+    sign = torch.ones(sum(lens), 1, D)
+    sign[::2] = -1.0
+    v = (sign * torch.where(torch.arange(D) % 2 > 0, 1.0, -1.0)).expand(-1, H, -1)
+    v = v.contiguous().to(torch.bfloat16)
+    sm = 1 / math.sqrt(D)
+    got, starts, kv_start = _cross(rudder, q, k, v, counts, lens, sm, max_kv)
+    for b, n in enumerate(lens):
+        r0, r1, k0 = int(starts[b]), int(starts[b + 1]), int(kv_start[b])
+        for h in range(H):
+            want, bound = ref.rows_attention(
+                q[r0:r1, h].double(), k[k0:k0 + n, h].double(), v[k0:k0 + n, h].double(),
+                torch.ones(r1 - r0, n, dtype=torch.bool), sm, ref.BF16 ** 2, 0.0)
+            ref.assert_within(f"O {b} {h}", got[r0:r1, h], want, bound)

@@ -27,7 +27,8 @@
 // folded into the exponent: with t_j = z_j + log2(sv) and m the running
 // maximum of t, P_j = exp2(t_j - m) multiplies plain codes, and
 // l = sum P_j / sv.  P is rounded to fp16 (2^-11 relative, absolute 2^-33 below
-// 2^-22); the sum l is formed from the unrounded values.
+// 2^-22), an eighth of what the output's rounding to bf16 adds; the sum l is formed from the
+// unrounded values.  Products with bf16 states take P as the sum of two bf16 numbers.
 #include <cmath>
 
 #include "rudder_operators.h"
@@ -152,6 +153,19 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     union { f16x2_t v; uint32_t u; } r;
     r.v = (f16x2_t){(_Float16)a, (_Float16)b};
     return r.u;
+}
+
+// Weights as operands: for the cache in fp16.  For states in bf16, whose 8 bits alone would put as
+// much into the outputs as their own rounding does (error 2.3e-3 against 1.7e-3 of their norm): a
+// second operand holds what that rounding left, in bf16 again, so that a weight is off by 2^-16 of
+// itself.  It costs half as many products again (2 x 4192 rows of 16 heads of 128 channels over 512
+// keys 67 us, 56 without).
+template <bool CACHE>
+__device__ __forceinline__ uint32_t pack_weights(float a, float b, uint32_t& rest) {
+    if (CACHE) return pack_f16(a, b);
+    const uint32_t w = pack_bf16(a, b);
+    rest = pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xFFFF0000u));
+    return w;
 }
 
 // Largest magnitude bits of a lane's share of a query row (NaN patterns are the largest).
@@ -499,8 +513,8 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
 // exponentials of 16 cycles and about 80 vector instructions of 4 (scaling, maximum, sum, rounding,
 // the codes' share of widening).  The pipeline over halves of tiles lets the two overlap within a
 // wave, the second workgroup of the compute unit fills the barriers.  2 x 4192 rows of 16 heads of
-// 128 channels over 512 bf16 keys 57 us (510 TFLOP/s: eight tiles against one load and one store of
-// the rows, 69 MB); 2 x 96 rows over 33536 cached tokens 102 us (520, and 690 counting the quarter
+// 128 channels over 512 bf16 keys 67 us (435 TFLOP/s: eight tiles against one load and one store of
+// the rows, 69 MB, and half as many products again as are counted here); 2 x 96 rows over 33536 cached tokens 102 us (520, and 690 counting the quarter
 // of the rows that is empty).
 // 64 channels leave room for three workgroups a compute unit: the exponentials weigh twice as much
 // there as with 128, and a third wave fills what two leave of the vector units, for four registers
@@ -618,13 +632,19 @@ attention_tile_kernel(const Problem p) {
                                                            i * 32), q[i], z);
         return z;
     };
-    uint4 pend0 = make_uint4(0, 0, 0, 0), pend1 = pend0;   // P of the 32 keys before
+    // P of the 32 keys before, and its rest (states)
+    uint4 pend0 = make_uint4(0, 0, 0, 0), pend1 = pend0, rest0 = pend0, rest1 = pend0;
+    auto nothing_pending = [&]() { pend0 = pend1 = rest0 = rest1 = make_uint4(0, 0, 0, 0); };
     auto weigh = [&](const uint8_t* tile, int hf) {        // O += V P of these
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt) {
             const uint8_t* v = tile + v_lane + dt * 32 * St::kVStride + hf * 64;
-            o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(v), pend0, o[dt]);
-            o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(v + 32), pend1, o[dt]);
+            const uint4 v0 = *reinterpret_cast<const uint4*>(v);
+            const uint4 v1 = *reinterpret_cast<const uint4*>(v + 32);
+            o[dt] = mma<CACHE>(v0, pend0, o[dt]);
+            if (!CACHE) o[dt] = mma<CACHE>(v0, rest0, o[dt]);
+            o[dt] = mma<CACHE>(v1, pend1, o[dt]);
+            if (!CACHE) o[dt] = mma<CACHE>(v1, rest1, o[dt]);
         }
     };
 
@@ -665,7 +685,7 @@ attention_tile_kernel(const Problem p) {
             top = fmaf(cz, top, lsv);              // -inf: nothing visible
             if (__any(top > m + kLazy)) {
                 weigh(before, before_hf);          // still under the old maximum
-                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+                nothing_pending();
                 const float m_new = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
                 const float alpha = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
                 m = m_new;
@@ -689,18 +709,20 @@ attention_tile_kernel(const Problem p) {
             f32x16_acc zn = ahead();
             weigh(before, before_hf);
             float sum = 0.0f;
-            uint32_t w[8];
+            uint32_t w[8], r[8] = {};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float a = __builtin_amdgcn_exp2f(fmaf(cz, z[2 * j], shift));
                 const float e = __builtin_amdgcn_exp2f(fmaf(cz, z[2 * j + 1], shift));
                 sum += a + e;
-                w[j] = CACHE ? pack_f16(a, e) : pack_bf16(a, e);
+                w[j] = pack_weights<CACHE>(a, e, r[j]);
             }
-            interleave<2 * kDT + kKS>();
+            interleave<(CACHE ? 2 : 4) * kDT + kKS>();
             l = fmaf(sum, apart ? 0.0f : sv_inv, l);
             pend0 = make_uint4(w[0], w[1], w[2], w[3]);
             pend1 = make_uint4(w[4], w[5], w[6], w[7]);
+            rest0 = make_uint4(r[0], r[1], r[2], r[3]);
+            rest1 = make_uint4(r[4], r[5], r[6], r[7]);
             z = zn;
         };
         for (;;) {
@@ -723,7 +745,7 @@ attention_tile_kernel(const Problem p) {
             else if (mine) {
                 step(1, [&]() { return z; }, cur, 0);
                 weigh(cur, 1);                     // the wave's last keys
-                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+                nothing_pending();
             }
             if (!more) break;
             old = cur;
@@ -871,7 +893,7 @@ attention_wide_kernel(const Problem p) {
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    uint4 pk[4];
+    uint4 pk[4], rest_k[4];                        // P, and its rest (states)
     float m = -INFINITY, top_lsv = -INFINITY;
     const int k_lane = (lane & 31) * St::kKStride + half * 16;
     const int v_lane = St::kKBytes + (lane & 31) * St::kVStride + half * 16;
@@ -909,10 +931,12 @@ attention_wide_kernel(const Problem p) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                for (int dt = 0; dt < kDT; ++dt)
-                    o[dt] = mma<CACHE>(*reinterpret_cast<const uint4*>(
-                                           vt + v_lane + dt * 32 * St::kVStride + ks * 32),
-                                       pk[ks], o[dt]);
+                for (int dt = 0; dt < kDT; ++dt) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        vt + v_lane + dt * 32 * St::kVStride + ks * 32);
+                    o[dt] = mma<CACHE>(v, pk[ks], o[dt]);
+                    if (!CACHE) o[dt] = mma<CACHE>(v, rest_k[ks], o[dt]);
+                }
         __syncthreads();
         if (!more) break;
         // Phase of vector work: tile i + 3 to LDS, the one behind on its way, weights of i + 1.
@@ -964,16 +988,17 @@ attention_wide_kernel(const Problem p) {
             float sum = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                uint32_t w[4];
+                uint32_t w[4], left[4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = (ks & 1) * 8 + 2 * j;
                     const float a = __builtin_amdgcn_exp2f(fmaf(cz, z[ks >> 1][r], shift));
                     const float e = __builtin_amdgcn_exp2f(fmaf(cz, z[ks >> 1][r + 1], shift));
                     sum += a + e;
-                    w[j] = CACHE ? pack_f16(a, e) : pack_bf16(a, e);
+                    w[j] = pack_weights<CACHE>(a, e, left[j]);
                 }
                 pk[ks] = make_uint4(w[0], w[1], w[2], w[3]);
+                rest_k[ks] = make_uint4(left[0], left[1], left[2], left[3]);
             }
             l = fmaf(sum, apart ? 0.0f : 1.0f / svc, l);
         }
