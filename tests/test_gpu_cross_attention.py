@@ -61,3 +61,53 @@ def test_weights_keep_their_bits(rudder, rows, max_kv, D):
                 q[r0:r1, h].double(), k[k0:k0 + n, h].double(), v[k0:k0 + n, h].double(),
                 torch.ones(r1 - r0, n, dtype=torch.bool), sm, ref.BF16 ** 2, 0.0)
             ref.assert_within(f"O {b} {h}", got[r0:r1, h], want, bound)
+
+
+@pytest.mark.parametrize("scale,sm", [(1.0, 0.0), (1.0, -2.0), (30.0, 0.3), (1e30, 1e-31),
+                                      (1e30, 0.0), (1e-30, 1e29), (0.0, 0.1)])
+@pytest.mark.parametrize("rows,max_kv,D", KERNELS)
+def test_scales_of_softmax_and_queries(rudder, rows, max_kv, D, scale, sm):
+    """Softmax scales of zero and below, near one-hot rows, rows of zeros and rows near the type's
+    ends, beside a sequence without states: a scale of zero weighs the states alike however large
+    the queries are."""
+    log(f"case cross scale={scale} sm={sm} rows={rows} max_kv={max_kv} D={D}")
+    g = torch.Generator().manual_seed(82)
+    counts, lens, H = [rows, 1, rows], [min(max_kv, 70), 0, max_kv], 2
+    q = (torch.randn(sum(counts), 2 * H, D, generator=g) * scale).to(torch.bfloat16)
+    k = torch.randn(sum(lens), H, D, generator=g).to(torch.bfloat16)
+    v = torch.randn(sum(lens), H, D, generator=g).to(torch.bfloat16)
+    got, starts, kv_start = _cross(rudder, q, k, v, counts, lens, sm)
+    want, bound = ref.cross_attention(q, k, v, starts, kv_start, lens, sm)
+    ref.assert_within("O", got, want, bound)
+    if sm == 0.0:                                  # plain means
+        for b, n in enumerate(lens):
+            if n:
+                at = int(kv_start[b])
+                mean = v[at:at + n].double().mean(0).repeat_interleave(2, 0)
+                rows_b = got[int(starts[b]):int(starts[b + 1])].double()
+                assert (rows_b - mean).abs().max() <= 2 * ref.BF16 * float(mean.abs().max())
+
+
+@pytest.mark.parametrize("sm", [0.1, -0.1, 0.0])
+@pytest.mark.parametrize("rows,max_kv,D", [(3, 64, 64), (40, 64, 128), (3, 2000, 64),
+                                           (140, 300, 128), (300, 1200, 128)])
+def test_queries_that_are_not_finite(rudder, rows, max_kv, D, sm):
+    """A query row with a NaN, an infinity of either sign or both gives NaN in its row and head
+    and leaves the others; one of a sequence without states gives zeros."""
+    log(f"case cross not finite rows={rows} max_kv={max_kv} D={D} sm={sm}")
+    g = torch.Generator().manual_seed(83)
+    counts, lens, H = [rows, 2], [max_kv, 0], 2
+    q = torch.randn(sum(counts), H, D, generator=g).to(torch.bfloat16)
+    k = torch.randn(sum(lens), H, D, generator=g).to(torch.bfloat16)
+    v = torch.randn(sum(lens), H, D, generator=g).to(torch.bfloat16)
+    clean, bad = q.clone(), [(0, 0, math.nan), (1, 1, math.inf), (2, 0, -math.inf)]
+    for r, h, x in bad:
+        q[r, h, 7 * r] = x
+    q[rows], q[rows + 1, 0, 3] = math.nan, -math.inf
+    got, starts, kv_start = _cross(rudder, q, k, v, counts, lens, sm)
+    assert not got[rows:].any()
+    want, bound = ref.cross_attention(clean, k, v, starts, kv_start, lens, sm)
+    for r, h, _ in bad:
+        assert torch.isnan(got[r, h]).all(), (r, h)
+        got[r, h], want[r, h], bound[r, h] = 0.0, 0.0, 0.0
+    ref.assert_within("O", got, want, bound)

@@ -48,6 +48,10 @@ constexpr float kPShift = 8.0f;                    // cache: P and its sums are 
 // Smallest V scale the exponent takes: smaller ones (an all-zero block's 0) are read as this.
 constexpr float kMinVScale = 8.271806125530277e-25f;   // 2^-80
 
+// Smallest factor of a score over the cache: c or a K scale of 0 must leave masked scores at -inf.
+// Codes times scaled queries stay below 2^30, so that the exponents it makes are zeros.
+constexpr float kMinScale = 1e-30f;
+
 struct Problem {
     const uint16_t* Q;
     const int32_t* row_start;
@@ -199,6 +203,16 @@ __device__ __forceinline__ float to_f16(uint4 (&q)[N], uint32_t top) {
         q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// Scores of bf16 queries may be of any size, and a factor c of 0 must still leave masked ones at
+// -inf: there the query becomes 0 and the factor 1.
+template <int N>
+__device__ __forceinline__ float scale_of_zero(uint4 (&q)[N], float c) {
+    if (c != 0.0f) return c;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    return 1.0f;
 }
 
 // A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), as integers
@@ -609,7 +623,10 @@ attention_tile_kernel(const Problem p) {
         uint32_t top = abs_max_bits<kKS>(q);
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
-        if (CACHE) c *= to_f16<kKS>(q, top);
+        if (CACHE)
+            c *= to_f16<kKS>(q, top);
+        else
+            c = scale_of_zero<kKS>(q, c);
     }
 
     f32x16_acc o[kDT];
@@ -658,8 +675,7 @@ attention_tile_kernel(const Problem p) {
         int at = next_at;
         float cz = 0.0f, lsv = 0.0f, sv_inv = 1.0f;
         auto scales = [&]() {
-            // c or a K scale of 0 must leave masked scores at -inf
-            cz = fmaxf(CACHE ? c * sk : c, 1e-30f);
+            cz = CACHE ? fmaxf(c * sk, kMinScale) : c;
             const float svc = CACHE ? fmaxf(sv, kMinVScale) : 1.0f;
             lsv = CACHE ? __builtin_amdgcn_logf(svc) : 0.0f;       // log2
             sv_inv = CACHE ? 1.0f / svc : 1.0f;
@@ -885,7 +901,10 @@ attention_wide_kernel(const Problem p) {
         uint32_t top = abs_max_bits<kKS>(q);
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         if (top >= 0x7F80u && limit > 0) l = __uint_as_float(0x7FC00000u);    // not finite
-        if (CACHE) c *= to_f16<kKS>(q, top);
+        if (CACHE)
+            c *= to_f16<kKS>(q, top);
+        else
+            c = scale_of_zero<kKS>(q, c);
     }
 
     f32x16_acc o[kDT], z[2];
@@ -945,8 +964,7 @@ attention_wide_kernel(const Problem p) {
         now = ahead;
         if (ahead) {
             const float2 sc = lds_scale[(i + 1) & 3];
-            // c or a K scale of 0 must leave masked scores at -inf
-            const float cz = fmaxf(CACHE ? c * sc.x : c, 1e-30f);
+            const float cz = CACHE ? fmaxf(c * sc.x, kMinScale) : c;
             const float svc = CACHE ? fmaxf(sc.y, kMinVScale) : 1.0f;
             const float lsv = CACHE ? __builtin_amdgcn_logf(svc) : 0.0f;       // log2
             if (at + kPage > least)                // some row does not see all of the tile
@@ -1169,8 +1187,7 @@ attention_few_kernel(const Problem p) {
 
     while (page >= 0) {
         const int at = tile * kPage;
-        // c or a K scale of 0 must leave masked scores at -inf
-        const float cz = fmaxf(c * sk, 1e-30f), svc = fmaxf(sv, kMinVScale);
+        const float cz = fmaxf(c * sk, kMinScale), svc = fmaxf(sv, kMinVScale);
         const float lsv = __builtin_amdgcn_logf(svc), sv_inv = 1.0f / svc;
         // 256 * (high digits . K) + (low digits . K): |sums| < 2^30 for D = 128
         i32x4_acc zi[4];
