@@ -488,3 +488,20 @@ def test_cross_bounds(rudder):
     want, bound = ref.cross_attention(q, kv[:, :H], kv[:, H:], starts, torch.tensor([90, 0]),
                                       [10, 0], 0.1)
     ref.assert_within("O", got, want, bound)
+
+
+@pytest.mark.parametrize("rows,causal", [(2, True), (40, True), (300, False)])
+@pytest.mark.parametrize("power,sm_power", [(-108, 107), (-120, 118), (-131, 126)])
+def test_smallest_queries(rudder, rows, causal, power, sm_power):
+    """Rows down to the type's subnormal numbers under softmax scales to match: they keep the bits
+    that their type has, in every kernel."""
+    log(f"case smallest queries 2^{power} rows={rows}")
+    g = torch.Generator().manual_seed(43)
+    D, lens = 128, [1100]
+    codes, scales, table = _cache(g, lens, 1, D)
+    q = (torch.randn(rows, 2, D, generator=g).double() * 2.0 ** power).to(torch.bfloat16)
+    assert q.abs().max() > 0
+    starts, sm = _starts([rows]), 2.0 ** sm_power
+    want, bound = ref.cache_attention(q, starts, lens, table, codes, scales, sm, causal)
+    got = _run_cache(rudder, q, starts, lens, table, codes, scales, sm, causal)
+    ref.assert_within("O", got, want, bound)

@@ -187,11 +187,11 @@ __device__ __forceinline__ uint32_t abs_max_bits(const uint4 (&q)[N]) {
 }
 
 // A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), to fp16 times
-// 2^-e.  Returns 2^e.
+// 2^-e.  Returns 2^e.  Between -120 and 120: rows below keep their last bit, 2^-133, above fp16's
+// 2^-24, rows above stay below its largest number.
 template <int N>
 __device__ __forceinline__ float to_f16(uint4 (&q)[N], uint32_t top) {
-    const int field = (int)(top >> 7);
-    const int e = field == 0 ? 0 : min(max(field - 127, -120), 120);
+    const int e = min(max((int)(top >> 7) - 127, -120), 120);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -217,13 +217,12 @@ __device__ __forceinline__ float scale_of_zero(uint4 (&q)[N], float c) {
 
 // A query row whose largest magnitude has the bf16 bits `top` = f * 2^e, f in [1, 2), as integers
 // q * 2^(14 - e) in [-32639, 32639] and these as two digits, 256 * high + low: N pairs of 16 bytes
-// (16 channels) become one of each.  Returns 2^(e - 14).
+// (16 channels) become one of each.  Returns 2^(e - 14).  Subnormal rows count as e = -126, which
+// leaves them exact.
 template <int N>
 __device__ __forceinline__ float to_digits(const uint4 (&q)[2 * N], uint32_t top, uint4 (&high)[N],
                                            uint4 (&low)[N]) {
-    const int field = (int)(top >> 7);
-    const int e = min(max(field - 127, -110), 127);
-    const float up = __uint_as_float((uint32_t)(127 + min(14 - e, 127)) << 23);
+    const int e = min(max((int)(top >> 7) - 127, -126), 127);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         uint32_t hw[4], lw[4];
@@ -236,7 +235,7 @@ __device__ __forceinline__ float to_digits(const uint4 (&q)[2 * N], uint32_t top
             int h[4], l[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int x = quantize_clamped(f[j] * up, 32639.0f);
+                const int x = quantize_clamped(__builtin_amdgcn_ldexpf(f[j], 14 - e), 32639.0f);
                 h[j] = (x + 128) >> 8;
                 l[j] = x - 256 * h[j];
             }
@@ -246,7 +245,7 @@ __device__ __forceinline__ float to_digits(const uint4 (&q)[2 * N], uint32_t top
         high[i] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         low[i] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
-    return __uint_as_float((uint32_t)(127 + max(e - 14, -126)) << 23);
+    return __builtin_amdgcn_ldexpf(1.0f, e - 14);
 }
 
 // What turns a row's sum of P * code (or P * v) into its output: 0 where no key is visible.
