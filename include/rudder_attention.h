@@ -111,7 +111,8 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)
- *   sm       the softmax scale, e.g. 1 / sqrt(D)
+ *   sm       the softmax scale, e.g. 1 / sqrt(D); sm times a row's largest element
+ *            stays below 2^127
  *   workspace, workspace_bytes  at least rudder_attention_workspace_bytes(...)
  *            bytes (NULL if 0)
  *   B, T, max_rows, max_kv >= 0 (B, T or max_rows 0 is a no-op), Hq a multiple
@@ -121,7 +122,8 @@ size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, 
  * anything but the arguments.
  * Errors: INVALID_ARG for a null required pointer, negative sizes, Hq or Hkv
  * <= 0, Hq % Hkv != 0, max_pages or num_pages <= 0, ldq or ldo below Hq * D or
- * not a multiple of 8, sm not finite, a workspace that is too small, Q, codes, O
+ * not a multiple of 8, sm not finite or beyond 2^127 in magnitude, a workspace
+ * that is too small, Q, codes, O
  * or workspace not 16-byte aligned;
  * UNSUPPORTED for D other than 64 or 128, Hkv > 4096, B * Hkv > 65535,
  * max_kv > 2^30, min(max_rows, T) * Hq > 2^26, or B * Hkv *

@@ -178,3 +178,10 @@ def test_binding_checks_arguments(r):
     with pytest.raises(ImportError):
         r._load_bind().use("/nowhere/librudder.so")
     r.rudder_matvec_w4(**ok)
+
+
+@pytest.mark.parametrize("sm,status", [(3e38, 1), (-3e38, 1), (2.0 ** 127, 0), (-2.0 ** 127, 0)])
+def test_largest_softmax_scales(r, sm, status):
+    """The kernels' scale is sm * log2(e): what would make it infinite is refused."""
+    for name, args in (("rudder_cache_attention", CACHE), ("rudder_cross_attention", CROSS)):
+        assert _status(r, name, args, dict(sm=sm, B=0)) == status

@@ -381,6 +381,7 @@ constexpr int kMaxSequences = 65535;
 constexpr int kMaxCacheHeads = 4096;
 constexpr int kMaxKeys = 1 << 30;          // key numbers and the tiles' ends stay below 2^31
 constexpr int kMaxAppendRows = 1 << 29;
+constexpr float kMaxSoftmaxScale = 0x1p127f;
 
 rudder_status_t check_heads(const char* f, int Hkv, int D) {
     if (Hkv <= 0) return fail(RUDDER_ERR_INVALID_ARG, "%s: Hkv=%d must be positive", f, Hkv);
@@ -413,7 +414,9 @@ rudder_status_t check_attention(const char* f, bool cache, bool causal, const vo
                     Hq, Hkv);
     if ((st = check_ld(f, "ldq", ldq, Hq, D)) != RUDDER_OK) return st;
     if ((st = check_ld(f, "ldo", ldo, Hq, D)) != RUDDER_OK) return st;
-    if (!(sm - sm == 0.0f)) return fail(RUDDER_ERR_INVALID_ARG, "%s: sm must be finite", f);
+    // the kernels multiply it by log2(e)
+    if (!(sm >= -kMaxSoftmaxScale && sm <= kMaxSoftmaxScale))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: sm must be finite and at most 2^127", f);
     if (misaligned(Q) || misaligned(O) || misaligned(workspace))
         return fail(RUDDER_ERR_INVALID_ARG, "%s: Q, O and workspace must be 16-byte aligned", f);
     if (B > kMaxSequences)
