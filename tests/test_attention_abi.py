@@ -185,3 +185,68 @@ def test_largest_softmax_scales(r, sm, status):
     """The kernels' scale is sm * log2(e): what would make it infinite is refused."""
     for name, args in (("rudder_cache_attention", CACHE), ("rudder_cross_attention", CROSS)):
         assert _status(r, name, args, dict(sm=sm, B=0)) == status
+
+
+def _calls(r):
+    """Every call of the operators between the linears with addresses in all places, and the names
+    of its device arrays."""
+    T, H, D, P_ = 4, 2, 64, P
+    row = dict(row_start=P_, B=2, T=T, max_rows=2)
+    cache = dict(page_table=P_, codes=P_, scales=P_, max_pages=2, num_pages=3)
+    return [
+        (r.rudder_quantize_weights_grouped, dict(W=P_, K=128, N=0, group=64, Wq=P_, g_scale=P_),
+         ("W", "Wq", "g_scale")),
+        (r.rudder_matvec_w4,
+         dict(X=P_, stream_id=P_, Wq=P_, g_scale=P_, comp_a=P_, comp_b=P_, M=0, N=64, K=128,
+              group=64, S=1, Y=P_), ("X", "stream_id", "Wq", "g_scale", "comp_a", "comp_b", "Y")),
+        (r.rudder_cache_append, dict(K=P_, V=P_, pos=P_, Hkv=H, D=D, **{**row, "B": 0}, **cache),
+         ("K", "V", "row_start", "pos", "page_table", "codes", "scales")),
+        (r.rudder_cache_dequant, dict(codes=P_, scales=P_, pages=P_, n=0, num_pages=3, Hkv=H, D=D,
+                                      K_out=P_, V_out=P_),
+         ("codes", "scales", "pages", "K_out", "V_out")),
+        (r.rudder_cache_attention,
+         dict(Q=P_, kv_len=P_, max_kv=100, Hq=H, Hkv=H, D=D, sm=0.1, causal=True, workspace=P_,
+              O=P_, **{**row, "B": 0}, **cache),
+         ("Q", "row_start", "kv_len", "page_table", "codes", "scales", "workspace", "O")),
+        (r.rudder_cross_attention,
+         dict(Q=P_, K=P_, V=P_, kv_start=P_, kv_len=P_, Tkv=T, max_kv=100, Hq=H, Hkv=H, D=D,
+              sm=0.1, workspace=P_, O=P_, **{**row, "B": 0}),
+         ("Q", "K", "V", "row_start", "kv_start", "kv_len", "workspace", "O")),
+    ]
+
+
+def _like(name, device):
+    """A tensor for that argument, large enough, of a device that need not be there."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    kind = {"Wq": torch.uint8, "stream_id": torch.uint8, "workspace": torch.uint8,
+            "comp_a": torch.float32, "comp_b": torch.float32, "scales": torch.float32,
+            "K_out": torch.float32, "V_out": torch.float32, "codes": torch.int8,
+            "row_start": torch.int32, "pos": torch.int32, "page_table": torch.int32,
+            "kv_len": torch.int32, "kv_start": torch.int32, "pages": torch.int32}
+    shape = ((4, 2, 64) if name in ("Q", "K", "V", "O") else (1 << 20,))
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        return torch.empty(shape, dtype=kind.get(name, torch.bfloat16), device=device)
+
+
+def test_binding_refuses_tensors_of_another_device(r, monkeypatch):
+    """Every device array has to lie on the current device, whether a stream is given or not."""
+    monkeypatch.setattr(r, "_get_device", lambda: 0)
+    monkeypatch.setattr(r, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    for call, args, names in _calls(r):
+        for name in names:
+            for stream in ({}, {"stream": 0}):
+                with pytest.raises(ValueError, match=f"{name}: on cuda:1.*cuda:0"):
+                    call(**{**args, **stream, name: _like(name, "cuda:1")})
+            # one of the current device passes the binding; without memory it is a null pointer
+            try:
+                call(**{**args, name: _like(name, "cuda:0")})
+            except r.RudderError as e:
+                assert "null pointer" in str(e) or "compensation" in str(e)
+
+    class Stream:
+        cuda_stream, device_index = 0, 1
+
+    for call, args, _ in _calls(r):
+        with pytest.raises(ValueError, match="stream of cuda:1.*cuda:0"):
+            call(**args, stream=Stream())

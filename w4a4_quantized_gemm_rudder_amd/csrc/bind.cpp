@@ -5,7 +5,8 @@
 // tensors in Python and converting two dozen arguments took as long (K = N =
 // 2048, one row: 6.0 us a call, now 4.4).  Tensors are checked for their type,
 // layout, place and size against the sizes passed; device addresses (ints)
-// pass through unchecked, None is a null pointer.
+// pass through unchecked, None is a null pointer.  The first argument of every
+// call is the number of the current device, where all tensors have to lie.
 #include <Python.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -50,7 +51,10 @@ class Args {
   public:
     Args(const char* call, PyObject* const* args, Py_ssize_t n, Py_ssize_t expected)
         : args_(args) {
-        if (n == expected && lib.matvec_w4) return;
+        if (n == expected && lib.matvec_w4) {
+            device_ = integer();
+            return;
+        }
         PyErr_Format(PyExc_TypeError, "%s: %zd arguments, expected %zd%s", call, n, expected,
                      lib.matvec_w4 ? "" : " (and a library)");
         throw Failure{};
@@ -91,7 +95,19 @@ class Args {
         return o == Py_None ? nullptr : address(o);
     }
 
+    // A tensor's memory on the current device.
+    void* place(const char* name, const at::Tensor& t) {
+        if (t.is_cuda() && t.get_device() == device_) return t.data_ptr();
+        if (t.is_cuda())
+            PyErr_Format(PyExc_ValueError, "%s: on cuda:%d, but the current device is cuda:%d",
+                         name, (int)t.get_device(), device_);
+        else
+            PyErr_Format(PyExc_ValueError, "%s: not on a GPU", name);
+        throw Failure{};
+    }
+
   private:
+    int device_ = -1;
     PyObject* const* args_;
     Py_ssize_t at_ = 0;
 };
@@ -104,12 +120,6 @@ bool is(const at::Tensor& t, at::ScalarType type) {
 const at::Tensor& tensor(const char* name, PyObject* o) {
     if (THPVariable_Check(o)) return THPVariable_Unpack(o);
     PyErr_Format(PyExc_TypeError, "%s: a tensor, an address or None expected", name);
-    throw Failure{};
-}
-
-void* place(const char* name, const at::Tensor& t) {
-    if (t.is_cuda()) return t.data_ptr();
-    PyErr_Format(PyExc_ValueError, "%s: not on a GPU", name);
     throw Failure{};
 }
 
@@ -126,7 +136,7 @@ T* array(Args& a, const char* name, PyObject* o, at::ScalarType type, long long 
                : type == at::kInt    ? "contiguous int32 elements"
                : type == at::kChar   ? "contiguous int8 elements"
                                      : "contiguous uint8 elements");
-    return static_cast<T*>(place(name, t));
+    return static_cast<T*>(a.place(name, t));
 }
 
 // T rows of H heads of D bf16 values: [T, H, D] or [T, H * D], a row's values packed, rows any
@@ -153,7 +163,7 @@ uint16_t* rows(Args& a, const char* name, PyObject* o, int T, int H, int D, PyOb
             refuse(name, o, "expected at least ", T,
                    "rows of packed bf16 heads, the row distance apart");
         step = t.size(0) > 1 || t.stride(0) > width ? t.stride(0) : width;
-        p = static_cast<uint16_t*>(place(name, t));
+        p = static_cast<uint16_t*>(a.place(name, t));
     }
     if (step != (int)step) {
         PyErr_Format(PyExc_OverflowError, "%s: rows %lld elements apart", name, step);
@@ -196,10 +206,10 @@ int call(F f) {
 
 long long product(long long a, long long b) { return a > 0 && b > 0 ? a * b : 0; }
 
-// (W, K, N, group, Wq, g_scale, stream)
+// (device, W, K, N, group, Wq, g_scale, stream)
 PyObject* quantize_weights_grouped(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&] {
-        Args a("rudder_quantize_weights_grouped", args, n, 7);
+        Args a("rudder_quantize_weights_grouped", args, n, 8);
         PyObject* W = a.next();
         const int K = a.integer(), N = a.integer(), group = a.integer();
         const auto* w = array<uint16_t>(a, "W", W, at::kBFloat16, product(K, N));
@@ -212,10 +222,10 @@ PyObject* quantize_weights_grouped(PyObject*, PyObject* const* args, Py_ssize_t 
     });
 }
 
-// (X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y, stream)
+// (device, X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y, stream)
 PyObject* matvec_w4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&] {
-        Args a("rudder_matvec_w4", args, n, 13);
+        Args a("rudder_matvec_w4", args, n, 14);
         PyObject *X = a.next(), *sid = a.next(), *Wq = a.next(), *gs = a.next(), *ca = a.next(),
                  *cb = a.next();
         const int M = a.integer(), N = a.integer(), K = a.integer(), group = a.integer(),
@@ -249,11 +259,11 @@ struct Cache {
     }
 };
 
-// (K, V, row_start, pos, page_table, B, T, max_rows, max_pages, num_pages, Hkv, D, codes, scales,
-//  stream, ldk, ldv)
+// (device, K, V, row_start, pos, page_table, B, T, max_rows, max_pages, num_pages, Hkv, D, codes,
+//  scales, stream, ldk, ldv)
 PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&] {
-        Args a("rudder_cache_append", args, n, 17);
+        Args a("rudder_cache_append", args, n, 18);
         PyObject *K = a.next(), *V = a.next(), *start = a.next(), *pos = a.next(),
                  *table = a.next();
         const int B = a.integer(), T = a.integer(), max_rows = a.integer(),
@@ -275,10 +285,10 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// (codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out, stream)
+// (device, codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out, stream)
 PyObject* cache_dequant(PyObject*, PyObject* const* args, Py_ssize_t count) {
     return guarded([&] {
-        Args a("rudder_cache_dequant", args, count, 10);
+        Args a("rudder_cache_dequant", args, count, 11);
         Cache cache{a.next(), a.next()};
         PyObject* pages = a.next();
         const int n = a.integer(), num_pages = a.integer(), Hkv = a.integer(), D = a.integer();
@@ -294,11 +304,11 @@ PyObject* cache_dequant(PyObject*, PyObject* const* args, Py_ssize_t count) {
     });
 }
 
-// (Q, row_start, kv_len, page_table, codes, scales, B, T, max_rows, max_kv, max_pages, num_pages,
-//  Hq, Hkv, D, sm, causal, workspace, O, stream, ldq, ldo)
+// (device, Q, row_start, kv_len, page_table, codes, scales, B, T, max_rows, max_kv, max_pages,
+//  num_pages, Hq, Hkv, D, sm, causal, workspace, O, stream, ldq, ldo)
 PyObject* cache_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&] {
-        Args a("rudder_cache_attention", args, n, 22);
+        Args a("rudder_cache_attention", args, n, 23);
         PyObject *Q = a.next(), *start = a.next(), *len = a.next(), *table = a.next();
         Cache cache{a.next(), a.next()};
         const int B = a.integer(), T = a.integer(), max_rows = a.integer(), max_kv = a.integer(),
@@ -325,11 +335,11 @@ PyObject* cache_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// (Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, sm, workspace, O,
-//  stream, ldq, ldk, ldv, ldo)
+// (device, Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows, max_kv, Hq, Hkv, D, sm,
+//  workspace, O, stream, ldq, ldk, ldv, ldo)
 PyObject* cross_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&] {
-        Args a("rudder_cross_attention", args, n, 22);
+        Args a("rudder_cross_attention", args, n, 23);
         PyObject *Q = a.next(), *K = a.next(), *V = a.next(), *start = a.next(),
                  *kv_start = a.next(), *len = a.next();
         const int B = a.integer(), T = a.integer(), Tkv = a.integer(), max_rows = a.integer(),

@@ -194,16 +194,26 @@ def _stream_getters() -> None:
                           lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream_for(stream, t) -> Optional[int]:
-    """As _stream; the current stream only for a tensor of the current device."""
-    if stream is not None:
-        return _stream(stream)
-    if _raw_stream is None:
-        _stream_getters()
-    device = _get_device()
-    if t is not None and t.__class__ is not int and t.get_device() != device:
-        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{device}")
-    return _raw_stream(device)
+def _device_and_stream(stream) -> Tuple[int, int]:
+    """The current device (-1: none in use yet), where the operators between the linears want all
+    of their tensors, and the handle of `stream` (None: the current one)."""
+    if stream is None:
+        if _raw_stream is None:
+            _stream_getters()
+        device = _get_device()
+        return device, _raw_stream(device)
+    import torch
+    device = -1
+    if torch.cuda.is_initialized():
+        if _get_device is None:
+            _stream_getters()
+        device = _get_device()
+    if isinstance(stream, int):
+        return device, stream
+    if stream.device_index != device:
+        raise ValueError(f"a stream of cuda:{stream.device_index}, but the current device is "
+                         f"cuda:{device}")
+    return device, stream.cuda_stream
 
 
 def _stream(stream) -> Optional[int]:
@@ -297,9 +307,9 @@ def rudder_stream_sq_error(Y, Yref, stream_id, M: int, N: int, S: int, workspace
 
 # ---------------------------------------------------------------------------
 # Few-row products, cache and attention (include/rudder_attention.h).  Tensors
-# are checked for their type, layout and size against the sizes passed, in
-# csrc/bind.cpp: in Python that took as long as the smallest calls.  Device
-# addresses (ints) pass through unchecked.
+# are checked for their type, layout and size against the sizes passed and for
+# the current device, in csrc/bind.cpp: in Python that took as long as the
+# smallest calls.  Device addresses (ints) pass through unchecked.
 # ---------------------------------------------------------------------------
 
 def grouped_weight_bytes(K: int, N: int) -> int:
@@ -313,14 +323,16 @@ def grouped_scale_count(K: int, N: int, group: int) -> int:
 def rudder_quantize_weights_grouped(W, K: int, N: int, group: int, Wq, g_scale,
                                     stream=None) -> None:
     bind = _bind or _load_bind()
-    _check(bind.quantize_weights_grouped(W, K, N, group, Wq, g_scale, _stream_for(stream, W)))
+    device, handle = _device_and_stream(stream)
+    _check(bind.quantize_weights_grouped(device, W, K, N, group, Wq, g_scale, handle))
 
 
 def rudder_matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M: int, N: int, K: int,
                      group: int, S: int, Y, stream=None) -> None:
     bind = _bind or _load_bind()
-    _check(bind.matvec_w4(X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y,
-                          _stream_for(stream, X)))
+    device, handle = _device_and_stream(stream)
+    _check(bind.matvec_w4(device, X, stream_id, Wq, g_scale, comp_a, comp_b, M, N, K, group, S, Y,
+                          handle))
 
 
 def cache_page_bytes(Hkv: int, D: int) -> int:
@@ -332,16 +344,17 @@ def rudder_cache_append(K, V, row_start, pos, page_table, B: int, T: int, max_ro
                         stream=None, ldk=None, ldv=None) -> None:
     """K, V: [T, Hkv, D] or [T, Hkv * D], rows any distance apart."""
     bind = _bind or _load_bind()
-    _check(bind.cache_append(K, V, row_start, pos, page_table, B, T, max_rows, max_pages,
-                             num_pages, Hkv, D, codes, scales, _stream_for(stream, codes), ldk,
-                             ldv))
+    device, handle = _device_and_stream(stream)
+    _check(bind.cache_append(device, K, V, row_start, pos, page_table, B, T, max_rows, max_pages,
+                             num_pages, Hkv, D, codes, scales, handle, ldk, ldv))
 
 
 def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int, D: int, K_out,
                          V_out, stream=None) -> None:
     bind = _bind or _load_bind()
-    _check(bind.cache_dequant(codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out,
-                              _stream_for(stream, codes)))
+    device, handle = _device_and_stream(stream)
+    _check(bind.cache_dequant(device, codes, scales, pages, n, num_pages, Hkv, D, K_out, V_out,
+                              handle))
 
 
 def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
@@ -356,9 +369,10 @@ def rudder_cache_attention(Q, row_start, kv_len, page_table, codes, scales, B: i
                            ldq=None, ldo=None) -> None:
     """Q, O: [T, Hq, D] or [T, Hq * D], rows any distance apart."""
     bind = _bind or _load_bind()
-    _check(bind.cache_attention(Q, row_start, kv_len, page_table, codes, scales, B, T, max_rows,
-                                max_kv, max_pages, num_pages, Hq, Hkv, D, sm, causal, workspace,
-                                O, _stream_for(stream, Q), ldq, ldo))
+    device, handle = _device_and_stream(stream)
+    _check(bind.cache_attention(device, Q, row_start, kv_len, page_table, codes, scales, B, T,
+                                max_rows, max_kv, max_pages, num_pages, Hq, Hkv, D, sm, causal,
+                                workspace, O, handle, ldq, ldo))
 
 
 def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int, Tkv: int,
@@ -366,9 +380,9 @@ def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int,
                            workspace, O, stream=None, ldq=None, ldk=None, ldv=None,
                            ldo=None) -> None:
     bind = _bind or _load_bind()
-    _check(bind.cross_attention(Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows, max_kv,
-                                Hq, Hkv, D, sm, workspace, O, _stream_for(stream, Q), ldq, ldk,
-                                ldv, ldo))
+    device, handle = _device_and_stream(stream)
+    _check(bind.cross_attention(device, Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows,
+                                max_kv, Hq, Hkv, D, sm, workspace, O, handle, ldq, ldk, ldv, ldo))
 
 
 # ---------------------------------------------------------------------------
