@@ -250,3 +250,34 @@ def test_binding_refuses_tensors_of_another_device(r, monkeypatch):
     for call, args, _ in _calls(r):
         with pytest.raises(ValueError, match="stream of cuda:1.*cuda:0"):
             call(**args, stream=Stream())
+
+
+def test_conveniences_check_shapes(r):
+    """What the allocating forms take their sizes from has to agree: the rows' heads and channels
+    with the cache's, also where there is nothing to do, and the weights and scales with the
+    product's sizes and group."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    q, k = torch.zeros(5, 4, 64, dtype=bf16), torch.zeros(5, 2, 64, dtype=bf16)
+    rows, two = torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32)
+    table = torch.zeros(2, 3, dtype=i32)
+    for heads, D in ((4, 64), (2, 128), (4, 128), (1, 64)):
+        cache = r.new_cache(3, heads, D, device="cpu")
+        for n in (5, 0):
+            with pytest.raises(ValueError, match="codes.*2 heads of 64 channels"):
+                r.cache_append(k[:n], k[:n], rows, two, table, 5, *cache)
+    for n in (5, 0):
+        cache = r.new_cache(3, 2, 128, device="cpu")
+        with pytest.raises(ValueError, match="codes.*2 heads of 64 channels"):
+            r.cache_attention(q[:n], rows, two, table, *cache, 5, 100, 0.1)
+        flat = (cache[0].view(3, 2, -1), cache[1])
+        with pytest.raises(ValueError, match="codes.*2 heads of 64 channels"):
+            r.cache_attention(q[:n], rows, two, table, *flat, 5, 100, 0.1)
+    x = torch.zeros(3, 256, dtype=bf16)
+    for K, N, group in ((256, 48, 32), (256, 48, 128), (256, 64, 64), (128, 48, 64),
+                        (512, 48, 64)):
+        Wq = torch.zeros(r.grouped_weight_bytes(K, N), dtype=torch.uint8)
+        gs = torch.zeros(r.grouped_scale_count(K, N, group), dtype=bf16)
+        with pytest.raises(ValueError, match="K=256, N=48, group=64"):
+            r.matvec_w4(x, Wq, gs, 48, 64)
+        with pytest.raises(ValueError, match="K=256, N=48, group=64"):
+            r.matvec_w4(x[:0], Wq, gs, 48, 64)

@@ -24,6 +24,7 @@ Scaling in World-Action Models", paperlayer.ai digest.)
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -479,6 +480,11 @@ def quantize_weights_grouped(W, group: int, stream=None):
     return Wq, g_scale
 
 
+@functools.lru_cache(maxsize=None)
+def _grouped_sizes(K: int, N: int, group: int) -> Tuple[int, int]:
+    return grouped_weight_bytes(K, N), grouped_scale_count(K, N, group)
+
+
 def matvec_w4(X, Wq, g_scale, N: int, group: int, stream_id=None, comp_a=None, comp_b=None,
               stream=None):
     """X: bf16 [M, K], weights from quantize_weights_grouped, optionally the
@@ -486,6 +492,9 @@ def matvec_w4(X, Wq, g_scale, N: int, group: int, stream_id=None, comp_a=None, c
     [S, N]).  Returns Y bf16 [M, N]."""
     import torch
     M, K = X.shape
+    if (Wq.numel(), g_scale.numel()) != _grouped_sizes(K, N, group):
+        raise ValueError(f"Wq of {Wq.numel()} bytes and {g_scale.numel()} scales are not those of "
+                         f"K={K}, N={N}, group={group}")
     S = 1 if comp_a is None else comp_a.shape[0]
     with _on(stream, X.device):
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
@@ -502,12 +511,18 @@ def new_cache(num_pages: int, Hkv: int, D: int, device="cuda"):
             torch.zeros(num_pages, Hkv, 2, dtype=torch.float32, device=device))
 
 
+def _check_cache(codes, Hkv: int, D: int) -> None:
+    if tuple(codes.shape[1:]) != (Hkv, 2, CACHE_PAGE * D):
+        raise ValueError(f"codes {tuple(codes.shape)} are not pages of {Hkv} heads of {D} channels")
+
+
 def cache_append(K, V, row_start, pos, page_table, max_rows: int, codes, scales,
                  stream=None) -> None:
     """Quantizes K, V [T, Hkv, D] into the cache at pos [B] (see
     include/rudder_attention.h)."""
     B, max_pages = page_table.shape
     T, Hkv, D = K.shape
+    _check_cache(codes, Hkv, D)
     if T == 0 or B == 0:
         return
     with _on(stream, codes.device):
@@ -543,6 +558,7 @@ def cache_attention(Q, row_start, kv_len, page_table, codes, scales, max_rows: i
     B, max_pages = page_table.shape
     T, Hq, D = Q.shape
     num_pages, Hkv = codes.shape[:2]
+    _check_cache(codes, Hkv, D)
     with _on(stream, Q.device):
         ws, O = _attention_buffers(Q, B, max_rows, max_kv, Hkv)
         if T and B:
