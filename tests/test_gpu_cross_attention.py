@@ -111,3 +111,25 @@ def test_queries_that_are_not_finite(rudder, rows, max_kv, D, sm):
         assert torch.isnan(got[r, h]).all(), (r, h)
         got[r, h], want[r, h], bound[r, h] = 0.0, 0.0, 0.0
     ref.assert_within("O", got, want, bound)
+
+
+def test_single_rows_with_any_stride(rudder):
+    """One row has no distance to a next one: what its tensor's stride says does not matter."""
+    log("case single row strides")
+    g = torch.Generator().manual_seed(84)
+    H, D, n = 2, 64, 70
+    buf = torch.randn(1, 5 * H * D + 3, generator=g).to(torch.bfloat16).cuda()
+    q = buf.as_strided((1, H, D), (5 * H * D + 3, D, 1))
+    assert q.stride(0) % 8
+    k = torch.randn(n, H, D, generator=g).to(torch.bfloat16)
+    starts, zero = _i32([0, 1]).cuda(), _i32([0]).cuda()
+    args = (k.cuda(), k.cuda(), starts, zero, _i32([n]).cuda(), 1, n, 0.1)
+    want = rudder.cross_attention(q.contiguous().clone(), *args)
+    assert torch.equal(rudder.cross_attention(q, *args), want)
+    codes, scales = rudder.new_cache(2, H, D)
+    one, other = (codes.clone(), scales.clone()), (codes, scales)
+    table = _i32([[1, 0]]).cuda()
+    rudder.cache_append(q, q, starts, zero, table, 1, *one)
+    rudder.cache_append(q.contiguous().clone(), q.contiguous().clone(), starts, zero, table, 1,
+                        *other)
+    assert torch.equal(one[0], other[0]) and torch.equal(one[1], other[1])

@@ -140,7 +140,8 @@ T* array(Args& a, const char* name, PyObject* o, at::ScalarType type, long long 
 }
 
 // T rows of H heads of D bf16 values: [T, H, D] or [T, H * D], a row's values packed, rows any
-// distance apart.  `ld` (None: the tensor's own) is that distance.
+// distance apart.  `ld` (None: the tensor's own) is that distance; a single row has none, whatever
+// its tensor's stride says.
 uint16_t* rows(Args& a, const char* name, PyObject* o, int T, int H, int D, PyObject* distance,
                int& ld) {
     const bool given = distance != Py_None;
@@ -159,10 +160,10 @@ uint16_t* rows(Args& a, const char* name, PyObject* o, int T, int H, int D, PyOb
                    (t.stride(1) == D || H == 1);
         else if (good)
             good = t.size(1) == width && t.stride(1) == 1;
-        if (!good || t.size(0) < T || (given && want != t.stride(0)))
+        if (!good || t.size(0) < T || (given && T > 1 && want != t.stride(0)))
             refuse(name, o, "expected at least ", T,
                    "rows of packed bf16 heads, the row distance apart");
-        step = t.size(0) > 1 || t.stride(0) > width ? t.stride(0) : width;
+        if (T > 1) step = t.stride(0);
         p = static_cast<uint16_t*>(a.place(name, t));
     }
     if (step != (int)step) {
