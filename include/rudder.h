@@ -267,8 +267,9 @@ rudder_status_t rudder_linear(const void* Xq, const float* row_scale, const uint
  *   t[m][n]   = sum_g s[g][n] * sum_{k in g} q[k][n] * X[m][k]  (fp32 sums)
  *   Y[m][n]   = bf16_rne(fmaf(a[st][n], t, b[st][n])), st = stream_id[m]
  * (Y = bf16_rne(t) without compensation).  A zero scale gives codes 0.  The
- * sums pass through 136 times those of X over a group, so |X| stays below
- * 2^110; a row that is not finite gives NaN in that row only.
+ * sums pass through 31 times those of |X| over a group, so that each group of
+ * t is off by a few 2^-19 * s * sum |X| and |X| stays below 2^110; a row that is
+ * not finite gives NaN in that row only.
  *
  * rudder_quantize_weights_grouped prepares a layer once:
  *   W        bf16 bits [K][N], row-major

@@ -57,8 +57,8 @@ def pack_grouped(q, s):
 def matvec(x, q, s, group, sid=None, a=None, b=None):
     """Y in 64 bits, and the bound on a kernel's distance from it.
 
-    Sums of one group: (136 + q) * x and x, each at most 143 * sum |x| large and of `group`
-    fp32 additions, their difference one more rounding; then K / group fused additions; the
+    Sums of one group: (24 + q) * x and x, each at most 31 * sum |x| large, counted here as 143 (a
+    wider offset's), and of `group` fp32 additions, their difference one more rounding; then K / group fused additions; the
     compensation's fma; the rounding to bf16."""
     x, q, s = x.double(), q.double(), s.double()
     K, N = q.shape

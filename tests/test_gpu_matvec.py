@@ -112,3 +112,22 @@ def test_codes_far_apart(rudder):
     y = rudder.matvec_w4(x.cuda(), Wq, gs, N, group)
     ref.assert_within("Y", y[:, -last:], want, bound)
     assert not y[:, :-last].any()
+
+
+@pytest.mark.parametrize("M,K,N,group", [(1, 2048, 40, 128), (9, 512, 64, 32), (4, 1024, 48, 64)])
+def test_activations_of_one_sign(rudder, M, K, N, group):
+    """Activations of one sign (after a GELU) and in each group one of 2^18 under a code of 0: what
+    the codes' offset adds to the sums and takes away again is far larger than the result.  A code
+    with its offset is at most 31, so that every sum stays below 31 * (2^18 + 2 * 127) < 2^24 and
+    is exact in 32 bits, whatever the order."""
+    log(f"case one sign M={M} K={K} N={N} group={group}")
+    g = torch.Generator().manual_seed(5)
+    x = torch.randint(1, 3, (M, K), generator=g).to(torch.bfloat16)
+    x[:, 7::group] = 2.0 ** 18
+    W = torch.randint(-7, 8, (K, N), generator=g).float() / 8
+    W[::group] = 7 / 8
+    W[7::group] = 0.0
+    W = W.to(torch.bfloat16)
+    Wq, gs = rudder.quantize_weights_grouped(W.cuda(), group)
+    y = rudder.matvec_w4(x.cuda(), Wq, gs, N, group)
+    assert torch.equal(y.cpu(), (x.double() @ W.double()).to(torch.bfloat16))

@@ -8,14 +8,16 @@
 // The product is bound by the bytes of the weight codes (K * N / 2): at 16
 // rows a code is used 16 times, far below what the matrix cores could do.
 // What has to stay small is therefore the work per code.  A code q in
-// [-7, 7] is stored as the nibble q + 8, and (nibble | 0x4300) is the bf16
-// value 128 + nibble = 136 + q: two codes become two matrix operands with one
-// shift and one and-or.  The matrix core then sums (136 + q) * x, and a
+// [-7, 7] is stored as the nibble q + 8, and (nibble << 3 | 0x4180) is the bf16
+// value 16 + nibble = 24 + q: two codes become two matrix operands with one
+// shift and one and-or.  The matrix core then sums (24 + q) * x, and a
 // second product with ones gives sum x, so that
-//   sum q * x = sum (136 + q) * x - 136 * sum x
+//   sum q * x = sum (24 + q) * x - 24 * sum x
 // in fp32, once per group.  The difference cancels: each of the two sums is
-// rounded in fp32 at a magnitude up to about 40 times that of the result, an
-// error of a few 2^-19 relative, 2^-10 of the rounding of the bf16 output.
+// formed at magnitudes up to 31 * sum |x| over the group, so that a group's
+// result is off by a few 2^-19 * sum |x|, whatever its own size.  A code is
+// off by up to a half, which makes that a few 2^-18 of what the weights'
+// rounding may cost; results far below sum |x| have it relative to that.
 #include "rudder_operators.h"
 
 namespace rudder {
@@ -77,7 +79,8 @@ __device__ __forceinline__ void wave_sync() {
 __device__ __forceinline__ bf16x8_t widen_codes(uint32_t w, uint32_t magic) {
     union { uint32_t u[4]; bf16x8_t v; } r;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) r.u[p] = ((w >> (4 * p)) & 0x000F000Fu) | magic;
+    for (int p = 0; p < 4; ++p)
+        r.u[p] = ((p ? w >> (4 * p - 3) : w << 3) & 0x00780078u) | magic;
     return r.v;
 }
 
@@ -124,7 +127,7 @@ matvec_w4_kernel(const uint16_t* __restrict__ X, const uint8_t* __restrict__ sid
     const int x_row = col & (4 * MQ - 1);
     uint8_t* xs = lds.x[wave];
     // one of the two constants in a vector register: and-or takes one scalar operand
-    uint32_t magic = 0x43004300u;
+    uint32_t magic = 0x41804180u;
     asm("" : "+v"(magic));
     bf16x8_t ones;
 #pragma unroll
@@ -171,6 +174,11 @@ matvec_w4_kernel(const uint16_t* __restrict__ X, const uint8_t* __restrict__ sid
             xv[s].u = *reinterpret_cast<const uint4*>(xs + x_row * 256 +
                                                       ((4 * s + quarter) ^ x_row) * 16);
         wave_sync();
+        // Codes are widened behind this line.  Left to itself the compiler began with their shifts,
+        // between a tile's loads, and waited for the first before it had asked for the last (K =
+        // 16384, N = 4096, M = 13, groups of 32: 13.1 us, 10.5 so; K = 8192, N = 12288, M = 16:
+        // 21.3, 16.2).
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
             f32x4_t d[NT], sx = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -195,7 +203,7 @@ matvec_w4_kernel(const uint16_t* __restrict__ X, const uint8_t* __restrict__ sid
                                     __uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[t][i] = fmaf(f[i], fmaf(-136.0f, sx[i], d[t][i]), acc[t][i]);
+                    acc[t][i] = fmaf(f[i], fmaf(-24.0f, sx[i], d[t][i]), acc[t][i]);
             }
         }
     }
