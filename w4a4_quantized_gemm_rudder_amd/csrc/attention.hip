@@ -1084,6 +1084,7 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
 }
 
 constexpr int kFewRows = 16;
+constexpr int kFewWaves = 4;                       // of a workgroup where the keys are split, else 8
 
 template <int D, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2)
@@ -1131,7 +1132,9 @@ attention_few_kernel(const Problem p) {
         for (;;) {
             tile = tile0 + wave + ++index * WAVES;
             if (tile >= tile1) return -1;
-            if (index > 0 && (index & 63) == 0) numbers = page_numbers(index);
+            // the numbers of the next 64.  Not with eight waves, which walk whole stretches: plan()
+            // leaves at most 42 tiles whole
+            if (WAVES == kFewWaves && index > 0 && (index & 63) == 0) numbers = page_numbers(index);
             const int page = __builtin_amdgcn_readlane(numbers, index & 63);
             if (page >= 0 && page < p.num_pages) return page;
         }
@@ -1396,8 +1399,6 @@ struct Plan {
         return pieces > 1 ? (size_t)pieces * (units - whole) * unit_rows : 0;
     }
 };
-
-constexpr int kFewWaves = 4;
 
 // Pieces of at least `least` tiles, `wanted` of them where the tiles suffice.
 void split(Plan& p, int64_t wanted, int tiles, int least) {
