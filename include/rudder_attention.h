@@ -91,8 +91,15 @@ rudder_status_t rudder_cache_dequant(const int8_t* codes, const float* scales,
  * sizes they refuse, and for sizes that need none).  Calls that may run at the
  * same time -- on two streams, or in two graphs replayed side by side -- need
  * a workspace each.
+ * Smaller sizes may need more: fewer rows give fewer workgroups, and then the
+ * keys are split (B = 2, 16 heads of 128 channels, 16384 keys: none for 4096
+ * rows, 34 MB for one).  A buffer for calls of several sizes is as large as
+ * rudder_attention_workspace_bound says for the largest of each: no call of the
+ * same heads and channels with B, T, max_rows and max_kv up to these needs more.
  */
 size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
+                                        int D);
+size_t rudder_attention_workspace_bound(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
                                         int D);
 
 /*

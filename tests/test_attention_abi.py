@@ -281,3 +281,32 @@ def test_conveniences_check_shapes(r):
             r.matvec_w4(x, Wq, gs, 48, 64)
         with pytest.raises(ValueError, match="K=256, N=48, group=64"):
             r.matvec_w4(x[:0], Wq, gs, 48, 64)
+
+
+def test_workspace_bound_holds_for_smaller_sizes(r):
+    """A buffer for the largest sizes serves every smaller call, though single calls' needs do not
+    grow with their sizes."""
+    import random
+    assert (r.attention_workspace_bytes(2, 8192, 4096, 16384, 16, 16, 128) <
+            r.attention_workspace_bytes(2, 2, 1, 16384, 16, 16, 128))
+    rng = random.Random(7)
+    grow = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    for _ in range(400):
+        D, Hkv = rng.choice([64, 128]), rng.choice([1, 2, 5, 8, 16, 48, 128])
+        Hq = Hkv * rng.choice([1, 2, 3, 8, 16, 17])
+        B, rows, kv = grow(1, 300), grow(1, 5000), grow(1, 200000)
+        T = grow(1, B * rows)
+        if min(rows, T) * Hq > 1 << 26:
+            continue
+        bound = r.attention_workspace_bound(B, T, rows, kv, Hq, Hkv, D)
+        # a round of partial rows, or three pieces of 16 rows a sequence and head
+        assert bound <= max(98304, 16 * max(1364, 3 * B * Hkv)) * (D + 2) * 4
+        for _ in range(60):
+            b, m, n = rng.randint(1, B), min(rows, grow(1, rows)), min(kv, grow(1, kv))
+            t = rng.choice([T, rng.randint(1, T)])
+            need = r.attention_workspace_bytes(b, t, m, n, Hq, Hkv, D)
+            assert need <= bound, (b, t, m, n, Hq, Hkv, D)
+            assert r.attention_workspace_bound(b, t, m, n, Hq, Hkv, D) <= bound
+    for bad in ((1, 1, 1, 100, 15, 2, 64), (1, 1, 1, 100, 4, 2, 96), (-1, 1, 1, 100, 4, 2, 64),
+                (1, 1, 1, -1, 4, 2, 64)):
+        assert r.attention_workspace_bound(*bad) == 0

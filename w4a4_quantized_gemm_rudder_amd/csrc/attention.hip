@@ -1523,6 +1523,26 @@ bool attention_workspace(bool cache, bool causal, int B, int T, int max_rows, in
     return true;
 }
 
+// From plan(): few rows, where a group has at most 16 of them, take at most 512 workgroups and one a
+// pair below 256 pairs, 1024 and one a pair up to 341 and three a pair above; else pieces and split
+// units make at most one round.  Pieces have two tiles at least.
+size_t attention_workspace_bound(int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D) {
+    const int64_t tiles = ((int64_t)max_kv + kPage - 1) / kPage, most = (tiles + 1) / 2;
+    if (most <= 1) return 0;
+    const int64_t pairs = (int64_t)B * Hkv, group = Hq / Hkv;
+    const int64_t few = pairs < 256 ? 511 + pairs : 3 * pairs > 1364 ? 3 * pairs : 1364;
+    int64_t rows = 0;
+    if (group <= kFewRows) rows = kFewRows * (few < most * pairs ? few : most * pairs);
+    const int64_t all = (max_rows < T ? max_rows : T) * group;
+    for (const int waves : {4, 8}) {
+        const int64_t unit = kWaveRows * waves, round = waves == 8 ? 256 : D == 64 ? 768 : 512;
+        const int64_t units = most * ((all + unit - 1) / unit) * pairs;
+        const int64_t parts = unit * (units < round ? units : round);
+        rows = rows > parts ? rows : parts;
+    }
+    return (size_t)rows * (size_t)(D + 2) * sizeof(float);
+}
+
 hipError_t launch_cache_attention(const uint16_t* Q, const int32_t* row_start,
                                   const int32_t* kv_len, const int32_t* page_table,
                                   const int8_t* codes, const float* scales, int B, int T,

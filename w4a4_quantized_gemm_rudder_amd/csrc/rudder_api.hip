@@ -500,12 +500,25 @@ rudder_status_t rudder_cache_dequant(const int8_t* codes, const float* scales,
                     f);
 }
 
+namespace {
+
+bool attention_sizes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D) {
+    return B > 0 && T > 0 && max_rows > 0 && max_kv >= 0 && Hkv > 0 && Hkv <= kMaxCacheHeads &&
+           Hq > 0 && Hq % Hkv == 0 && (D == 64 || D == 128) && (int64_t)B * Hkv <= kMaxSequences &&
+           (int64_t)(max_rows < T ? max_rows : T) * Hq <= (1 << 26) && max_kv <= kMaxKeys;
+}
+
+}  // namespace
+
+size_t rudder_attention_workspace_bound(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
+                                        int D) {
+    if (!attention_sizes(B, T, max_rows, max_kv, Hq, Hkv, D)) return 0;
+    return rudder::attention_workspace_bound(B, T, max_rows, max_kv, Hq, Hkv, D);
+}
+
 size_t rudder_attention_workspace_bytes(int B, int T, int max_rows, int max_kv, int Hq, int Hkv,
                                         int D) {
-    if (B <= 0 || T <= 0 || max_rows <= 0 || max_kv < 0 || Hkv <= 0 || Hkv > kMaxCacheHeads ||
-        Hq <= 0 || Hq % Hkv || (D != 64 && D != 128) || (int64_t)B * Hkv > kMaxSequences ||
-        (int64_t)(max_rows < T ? max_rows : T) * Hq > (1 << 26) || max_kv > kMaxKeys)
-        return 0;
+    if (!attention_sizes(B, T, max_rows, max_kv, Hq, Hkv, D)) return 0;
     // one size for both calls, causal or not
     size_t bytes = 0, most = 0;
     for (const int kind : {0, 1, 2})

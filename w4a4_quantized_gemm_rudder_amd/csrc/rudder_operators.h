@@ -25,6 +25,8 @@ hipError_t launch_cache_dequant(const int8_t* codes, const float* scales, const 
 // Workspace of a call over the cache or to bf16 states; false for more work than a launch takes.
 bool attention_workspace(bool cache, bool causal, int B, int T, int max_rows, int max_kv, int Hq,
                          int Hkv, int D, size_t& bytes);
+// At least the workspace of every call of these sizes or smaller ones.
+size_t attention_workspace_bound(int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D);
 hipError_t launch_cache_attention(const uint16_t* Q, const int32_t* row_start,
                                   const int32_t* kv_len, const int32_t* page_table,
                                   const int8_t* codes, const float* scales, int B, int T,

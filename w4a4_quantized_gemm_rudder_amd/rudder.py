@@ -53,7 +53,8 @@ EXPORTED = (
     "rudder_grouped_weight_bytes", "rudder_grouped_scale_count",
     "rudder_quantize_weights_grouped", "rudder_matvec_w4",
     "rudder_cache_page_bytes", "rudder_cache_append", "rudder_cache_dequant",
-    "rudder_attention_workspace_bytes", "rudder_cache_attention", "rudder_cross_attention",
+    "rudder_attention_workspace_bytes", "rudder_attention_workspace_bound",
+    "rudder_cache_attention", "rudder_cross_attention",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -127,6 +128,8 @@ def load_library() -> ctypes.CDLL:
     lib.rudder_cache_dequant.restype = i
     lib.rudder_attention_workspace_bytes.argtypes = [i] * 7
     lib.rudder_attention_workspace_bytes.restype = sz
+    lib.rudder_attention_workspace_bound.argtypes = [i] * 7
+    lib.rudder_attention_workspace_bound.restype = sz
     lib.rudder_cache_attention.argtypes = [vp] * 6 + [i] * 11 + [f, i, vp, sz, vp, vp]
     lib.rudder_cache_attention.restype = i
     lib.rudder_cross_attention.argtypes = [vp] * 6 + [i] * 12 + [f, vp, sz, vp, vp]
@@ -361,6 +364,14 @@ def rudder_cache_dequant(codes, scales, pages, n: int, num_pages: int, Hkv: int,
 def attention_workspace_bytes(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
                               D: int) -> int:
     return int(load_library().rudder_attention_workspace_bytes(B, T, max_rows, max_kv, Hq, Hkv,
+                                                               D))
+
+
+def attention_workspace_bound(B: int, T: int, max_rows: int, max_kv: int, Hq: int, Hkv: int,
+                              D: int) -> int:
+    """Bytes that suffice for every call of these heads with B, T, max_rows and max_kv up to
+    these; attention_workspace_bytes of a smaller call may be larger than a larger one's."""
+    return int(load_library().rudder_attention_workspace_bound(B, T, max_rows, max_kv, Hq, Hkv,
                                                                D))
 
 
