@@ -5,7 +5,8 @@ contraction off (the epilogue's single fma is explicit) and packed-fp32
 instruction selection disabled, then linked into one shared library next to
 this file (_lib/librudder.so).  csrc/bind.cpp, host code, becomes the Python
 module that checks and passes on the arguments of small calls
-(_lib/rudder_bind.so).
+(_lib/rudder_bind.so); it needs Python's and torch's headers, and where they are
+not there the library is built without it.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -83,7 +85,9 @@ def build_bind() -> str:
     return BIND_PATH
 
 
-def build(verbose: bool = False) -> str:
+def build(verbose: bool = False, require_bind: bool = False) -> str:
+    """The library, and the module beside it.  Where that cannot be built its
+    operators raise from Python; the linears and the C ABI do not need it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     generate_tables()
@@ -91,13 +95,18 @@ def build(verbose: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         bind = ex.submit(build_bind)
         objs = list(ex.map(_compile, srcs))
-        bind.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if bind.exception() is not None:
+        if os.path.exists(BIND_PATH):              # an earlier build's, which may not fit
+            os.remove(BIND_PATH)
+        if require_bind:
+            raise bind.exception()
+        warnings.warn(f"built without {os.path.basename(BIND_PATH)}: {bind.exception()}")
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH
