@@ -214,3 +214,54 @@ def test_conveniences_on_a_given_stream(rudder):
         got = rudder.cache_attention(*args, stream=stream)
         st.synchronize()
         assert torch.equal(got, want)
+
+
+def test_block_with_cross_attention(rudder):
+    """A block's way between the linears: QKV linear, append, attention over the cache, the cross
+    attention's query linear, cross attention to an instruction's states, O linear.  Each stage
+    against its 64-bit form on the previous stage's GPU output."""
+    H, D, counts, before, lens = 2, 64, [40, 1], [100, 63], [77, 5]
+    log("case block with cross attention")
+    M = sum(counts)
+    X, qkv, out, sid, comp, K, N, W, Wo = _block(rudder, M, H, D, 55)
+    g = torch.Generator().manual_seed(56)
+    codes = torch.randint(-127, 128, (8, H, 2, PAGE * D), generator=g).to(torch.int8)
+    scales = torch.rand(8, H, 2, generator=g) * 0.01
+    table = torch.tensor([[5, 2, 7], [1, 0, -1]], dtype=torch.int32)
+    starts, pos, kv_start = _i32([0, 40, 41]), _i32(before), _i32([0, 77])
+    kv_len = _i32([b + c for b, c in zip(before, counts)])
+    enc = torch.randn(sum(lens), 2 * H, D, generator=g).to(torch.bfloat16)
+    Wc = (torch.randn(H * D, H * D, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    cross = rudder.quantize_weights(Wc, torch.ones(H * D, device="cuda"))
+    comp_c = torch.ones(1, H * D, device="cuda"), torch.zeros(1, H * D, device="cuda")
+    sm = 1 / math.sqrt(D)
+
+    xq, rs = rudder.quant_act(X, sid, qkv[2], None, 1, 8)
+    Y = rudder.linear(xq, rs, sid, qkv[0], qkv[1], *comp[N], M, N, K, 1, 8)
+    rows = Y.view(M, 3 * H, D)
+    dc, ds, denc = codes.cuda(), scales.cuda(), enc.cuda()
+    rudder.cache_append(rows[:, H:2 * H], rows[:, 2 * H:], starts.cuda(), pos.cuda(),
+                        table.cuda(), max(counts), dc, ds)
+    S = rudder.cache_attention(rows[:, :H], starts.cuda(), kv_len.cuda(), table.cuda(), dc, ds,
+                               max(counts), int(kv_len.max()), sm, True)
+    sq, srs = rudder.quant_act(S.view(M, H * D), sid, cross[2], None, 1, 8)
+    Q = rudder.linear(sq, srs, sid, cross[0], cross[1], *comp_c, M, H * D, H * D, 1, 8)
+    C = rudder.cross_attention(Q.view(M, H, D), denc[:, :H], denc[:, H:], starts.cuda(),
+                               kv_start.cuda(), _i32(lens).cuda(), max(counts), max(lens), sm)
+    cq, crs = rudder.quant_act(C.view(M, H * D), sid, out[2], None, 1, 8)
+    Z = rudder.linear(cq, crs, sid, out[0], out[1], *comp[K], M, K, H * D, 1, 8)
+
+    host = rows.cpu()
+    ref.append(host[:, H:2 * H], host[:, 2 * H:], starts, pos, table, codes, scales)
+    assert torch.equal(dc.cpu(), codes) and torch.equal(ds.cpu(), scales)
+    want, bound = ref.cache_attention(host[:, :H], starts, kv_len, table, codes, scales, sm, True)
+    ref.assert_within("S", S, want, bound)
+    want, bound = ref.cross_attention(Q.view(M, H, D).cpu(), enc[:, :H], enc[:, H:], starts,
+                                      kv_start, lens, sm)
+    ref.assert_within("C", C, want, bound)
+    # the linears against the unquantized products: int4 weights of N(0, s) within half a step of
+    # absmax / 7 (rms about 0.16 s), 8-bit rows within 1 / 254
+    for got, x, w in ((Q, S, Wc), (Z, C, Wo)):
+        full = x.view(M, -1).double() @ w.double()
+        err = (got.double() - full).norm() / full.norm()
+        assert err < 0.25, float(err)
