@@ -1416,7 +1416,11 @@ void split(Plan& p, int64_t wanted, int tiles, int least) {
 // unit draws about 50 GB/s, a join costs about 2 us:
 //   - short stretches, and what is short for many pairs, stay whole: 16 pairs, 512 tokens 9.2 [1],
 //     9.1 [8]; up to 777 tokens of 192 pairs 12.9 [1], 15.2 [2], up to 2048 of 256 23.8 [1], 30.0
-//     [4], up to 1500 of 384 29.6 [1], 31.2 [2];
+//     [4], up to 1500 of 384 29.6 [1], 31.2 [2].  At the limits: 128 pairs, 20 tiles 15.0 [1],
+//     15.3 [2], 24 tiles 16.6 [1], 15.6 [2]; 256 pairs, 42 tiles 28.4 [1], 33.3 [4], 48 tiles 31.6
+//     [1], 34.9 [4]; 264 pairs, which no longer fit one round of workgroups, 24 tiles 22.3 [1],
+//     24.6 [4], 32 tiles 31.5 [1], 29.6 [4]; 384 pairs, 24 tiles 30.1 [1], 30.2 [3], 28 tiles 33.1
+//     [1], 32.8 [3];
 //   - else one workgroup a unit up to 4096 tiles, above two, but pieces of two tiles and more, and
 //     of four where that makes more than eight: 16 pairs, 777 tokens 10.2 [4], 9.5 [8]; 2048 tokens
 //     9.9 [8], 12.0 [16]; 65536 tokens 56 [32], 65 [64];
@@ -1451,21 +1455,28 @@ bool plan(bool cache, bool causal, int B, int max_rows, int max_kv, int Hq, int 
     p.tile_rows = (int)tile_rows;
     p.units = (int)units;
     // A round is what runs at once.  What is left over after whole rounds, or all where it is less
-    // than one, is split over its keys where that repays the join (us, whole | split):
-    //   - less than a round, the sooner the fewer: with 16 heads of 128 channels two pieces from 32
-    //     tiles (1500 rows over 1024 keys 38.8 | 42, over 2048 keys 71 | 52), four from 16 (900
-    //     rows, 1024 keys 38 | 29), more from 4 (one row, 300 keys 13.6 | 11.6, 900 keys 29.6 |
-    //     12.0); 64 channels, whose rounds are larger, from twice as many (2400 rows, 2048 keys
-    //     56 | 63, 4096 keys 100 | 84);
-    //   - behind whole rounds, little of it: from 8 tiles (2 x 4192 rows over 512 keys 66 | 60,
-    //     over 12576 keys, 32 of 544 units, 1188 | 976); much: from 64 (288 of 1056 units of 64
-    //     channels, 2048 keys 85 | 95, 6000 keys 288 | 277); never causal ones, whose last units
-    //     are the shortest (3 x 2000 rows of 24 heads 88 | 98).
+    // than one, is split over its keys where that repays the join (us, whole | split; 16 heads):
+    //   - less than a round, the sooner the fewer: where pieces times tiles of keys reach `enough`.
+    //     256 rows a workgroup, two pieces from 16 tiles (1500 rows over 1024 tokens 42.3 | 39.8,
+    //     states 46.0 | 40.5; 128 rows a workgroup over 960 states 41.0 | 42.6).  128 channels, two
+    //     from 20 (1500 causal rows over 1500 tokens 51.8 | 44.0; 1900 rows over 768 states 36.8 |
+    //     42.4), four from 10 (900 rows over 768 tokens 30.2 | 27.4, states 33.6 | 29.2, over 512
+    //     24.7 | 26.1), more from 4 (40 rows over 300 tokens 15.1 | 13.0, one over 300 states
+    //     15.9 | 12.6).  64 channels, whose rounds are larger, two from 32 (2400 rows over 2048
+    //     tokens 66.6 | 59.0, over 1024 states 38.3 | 39.3), more from 12 (1200 causal rows over
+    //     1200 tokens 30.3 | 24.4, over 768 states 22.4 | 24.1; 600 rows over 768 states 22.1 |
+    //     18.7), below only very many (600 rows over 512 states 16.6 | 18.4);
+    //   - behind whole rounds, little of it: from 8 tiles (2 x 4192 rows over 512 tokens 71.8 |
+    //     65.1, states 73.6 | 69.0, over 12576 tokens, 32 of 544 units, 1224 | 960); much: from 64
+    //     (288 of 1056 units of 64 channels, 2048 states 105 | 114, 6000 390 | 366); never causal
+    //     ones, whose last units are the shortest (3 x 2000 rows of 24 heads of 64 channels 77.8 |
+    //     86.6).
     const int round = p.waves == 8 ? 256 : D == 64 ? 768 : 512, rest = p.units % round;
     const bool alone = p.units < round;
+    const int enough = p.waves == 8 ? 32 : D == 128 ? 40 : tiles >= 12 ? 64 : 128;
     const bool worth =
         rest > 0 && rest <= round / 2 &&
-        (alone ? tiles >= 4 && round / rest * tiles >= (D == 64 ? 128 : 64)
+        (alone ? tiles >= 4 && round / rest * tiles >= enough
                : !causal && tiles >= (rest * 8 > round ? 64 : 8));
     split(p, worth ? round / rest : 1, tiles, 2);
     p.whole = p.pieces > 1 ? p.units - rest : p.units;
