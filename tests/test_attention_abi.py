@@ -272,6 +272,7 @@ def test_conveniences_check_shapes(r):
         flat = (cache[0].view(3, 2, -1), cache[1])
         with pytest.raises(ValueError, match="codes.*2 heads of 64 channels"):
             r.cache_attention(q[:n], rows, two, table, *flat, 5, 100, 0.1)
+    r._check_cache(r.new_cache(3, 2, 64, device="cpu")[0].view(3, -1), 2, 64)    # pages in a row
     x = torch.zeros(3, 256, dtype=bf16)
     for K, N, group in ((256, 48, 32), (256, 48, 128), (256, 64, 64), (128, 48, 64),
                         (512, 48, 64)):

@@ -214,9 +214,9 @@ def _device_and_stream(stream) -> Tuple[int, int]:
         device = _get_device()
     if isinstance(stream, int):
         return device, stream
-    if stream.device_index != device:
-        raise ValueError(f"a stream of cuda:{stream.device_index}, but the current device is "
-                         f"cuda:{device}")
+    of = getattr(stream, "device_index", device)
+    if of != device:
+        raise ValueError(f"a stream of cuda:{of}, but the current device is cuda:{device}")
     return device, stream.cuda_stream
 
 
@@ -523,7 +523,10 @@ def new_cache(num_pages: int, Hkv: int, D: int, device="cuda"):
 
 
 def _check_cache(codes, Hkv: int, D: int) -> None:
-    if tuple(codes.shape[1:]) != (Hkv, 2, CACHE_PAGE * D):
+    page = (Hkv, 2, CACHE_PAGE * D)
+    good = (tuple(codes.shape[1:]) == page if codes.dim() == 4 else
+            codes.numel() == codes.shape[0] * Hkv * page[1] * page[2])
+    if not good:
         raise ValueError(f"codes {tuple(codes.shape)} are not pages of {Hkv} heads of {D} channels")
 
 
