@@ -30,8 +30,8 @@
  * A value is fl32(code * scale).  Pages belong to the caller: sequences may
  * share pages that no append writes to.
  * Undefined results (not checked; no access leaves the buffers): non-finite
- * keys, values or scales, sequences of one append call that write to the same
- * page, or one that lists it twice, overlapping buffers.
+ * keys, values (an encoder's too) or scales, sequences of one append call that
+ * write to the same page, or one that lists it twice, overlapping buffers.
  */
 #ifndef RUDDER_ATTENTION_H
 #define RUDDER_ATTENTION_H
@@ -112,9 +112,10 @@ size_t rudder_attention_workspace_bound(int B, int T, int max_rows, int max_kv, 
  * gives zeros whatever its query, any other query row that is not finite NaN.
  * q enters q . k with an absolute error of at most 2^-15 of its row's largest
  * power of two (2^-14 for an element of magnitude 255/128 times that power);
- * the products with the codes are exact.  The softmax is in fp32, its weights
- * rounded to fp16 for the product with the codes of V, fp32 sums, one rounding
- * to bf16.  V scales below 2^-80 count as 2^-80.
+ * the products with the codes are exact, their sums rounded to fp32 (2^-24).
+ * The softmax is in fp32, its weights rounded to fp16 for the product with the
+ * codes of V, fp32 sums, one rounding to bf16.  V scales below 2^-80 count as
+ * 2^-80.
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)

@@ -423,7 +423,7 @@ __device__ __forceinline__ void wave_sync() {
 
 // The 32 query rows of a wave pass through LDS, so that global memory sees whole rows: a lane's
 // share of its row is 16 bytes in 32 (loads) or 8 in 16 (stores).  2 x 4192 rows of 16 heads over
-// 128 keys 33.9 us without, of which 6.5 were the loads' and 10 the stores'.
+// 128 keys (with weights of one operand) 28.8 us, 33.9 without.
 template <int D>
 struct RowSlab {
     static constexpr int kStride = D * 2 + 16, kBytes = kWaveRows * kStride;
@@ -494,7 +494,8 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
         return;
     }
     // through LDS as well, a wave's partial rows lie behind each other (1500 rows of 16 heads of
-    // 128 channels over 2048 keys, in two pieces: 51.6 us, 54.2 without)
+    // 128 channels over 2048 keys, in two pieces and with weights of one operand: 51.6 us, 54.2
+    // without)
     constexpr int kStride = D * 4 + 16, kPieces = D / 4, kRowsAtOnce = 64 / kPieces;
     const int lane = threadIdx.x & 63;
     const size_t first = ((size_t)split * rest + (unit - p.whole)) * unit_rows + unit_row;
@@ -522,13 +523,16 @@ __device__ __forceinline__ void write_rows(const Problem& p, const Sequence& s, 
 // ---------------------------------------------------------------------------
 // Many rows: 128 of them a workgroup, four waves of 32 that share the tiles through LDS.
 // ---------------------------------------------------------------------------
-// A wave's 32 rows meet 32 keys in 2 D / 16 products of 32 cycles; beside them stand, a lane, 16
-// exponentials of 16 cycles and about 80 vector instructions of 4 (scaling, maximum, sum, rounding,
-// the codes' share of widening).  The pipeline over halves of tiles lets the two overlap within a
-// wave, the second workgroup of the compute unit fills the barriers.  2 x 4192 rows of 16 heads of
-// 128 channels over 512 bf16 keys 67 us (435 TFLOP/s: eight tiles against one load and one store of
-// the rows, 69 MB, and half as many products again as are counted here); 2 x 96 rows over 33536 cached tokens 102 us (520, and 690 counting the quarter
-// of the rows that is empty).
+// A wave's 32 rows meet 32 keys in 2 D / 16 products of 32 cycles (states 3 D / 16); beside them
+// stand, a lane, 16 exponentials of 16 cycles and about 80 vector instructions of 4 (scaling,
+// maximum, sum, rounding, the codes' share of widening; states 120).  The pipeline over halves of
+// tiles lets the two overlap within a wave, the second workgroup of the compute unit fills the
+// barriers.  2 x 4192 rows of 16 heads of 128 channels over 512 states 68 us (430 TFLOP/s: eight
+// tiles against one load and one store of the rows, 69 MB, and half as many products again as are
+// counted here); 2 x 96 rows over 33536 cached tokens 103 us (515, and 685 counting the quarter of
+// the rows that is empty).  Neither unit is half busy there (matrix cores 22 to 29%, vector units
+// 44%): a wave's score products are two chains of D / 16 one behind the other, its tiles one
+// ahead of its loads.
 // 64 channels leave room for three workgroups a compute unit: the exponentials weigh twice as much
 // there as with 128, and a third wave fills what two leave of the vector units, for four registers
 // spilled outside of the loop (2 x 4096 causal rows of 24 heads over 4096 tokens 168 us, with two
@@ -793,11 +797,12 @@ attention_tile_kernel(const Problem p) {
 // A's phases of tile i are 2 i (products: K of i + 1, V of i) and 2 i + 1 (stores i + 3), B's one
 // later, so that slot (i + 3) % 4 = (i - 1) % 4 was last read in phase 2 i - 1 and is first read in
 // 2 i + 4.
-// 2 x 4192 rows of 16 heads over 12576 cached tokens 920 to 940 us, 930 TFLOP/s (a library product
-// of as many operations 715 to 750): the matrix cores are busy 39% of the time, the vector units
-// half of it, LDS 28%; the longer of the two phases sets the pace.  Raised wave priorities, hints
-// to the scheduler and other pairs of waves measured the same or slower (1019, 1040 and 1112
-// against 1019 on one card).
+// 2 x 4192 rows of 16 heads over 12576 cached tokens 920 to 980 us, card by card, 880 to 930 TFLOP/s
+// (a library product of as many operations 715 to 750): the matrix cores are busy 39% of the time,
+// the vector units half of it, LDS 28%; the longer of the two phases sets the pace.  States: 2 x
+// 4700 rows over 8000 and 6280 834 us, 660 TFLOP/s, 990 with the products of the weights' second
+// operand.  Raised wave priorities, hints to the scheduler and other pairs of waves measured the
+// same or slower (1019, 1040 and 1112 against 1019 on one card).
 template <int D, bool CACHE>
 __global__ void __launch_bounds__(512, 2)
 attention_wide_kernel(const Problem p) {
@@ -879,8 +884,8 @@ attention_wide_kernel(const Problem p) {
         }
         ++stored;
     };
-    // the query rows in front of the first tile: bf16 keys 2 x 4700 rows over 8000, 627 us, 642 the
-    // other way round; the tile kernel prefers that one (105 against 108 on 2 x 96 rows)
+    // the query rows in front of the first tile or behind it: the same within 1%; the tile kernel
+    // prefers the latter (105 against 108 on 2 x 96 rows)
     RowSlab<D> rows_in;
     rows_in.fetch(p, s, t, head);
     load();
@@ -1084,7 +1089,7 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
 }
 
 constexpr int kFewRows = 16;
-constexpr int kFewWaves = 4;                       // of a workgroup where the keys are split, else 8
+constexpr int kFewWaves = 4;           // of a workgroup where the keys are split, else eight
 
 template <int D, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2)
@@ -1534,9 +1539,9 @@ bool attention_workspace(bool cache, bool causal, int B, int T, int max_rows, in
     return true;
 }
 
-// From plan(): few rows, where a group has at most 16 of them, take at most 512 workgroups and one a
-// pair below 256 pairs, 1024 and one a pair up to 341 and three a pair above; else pieces and split
-// units make at most one round.  Pieces have two tiles at least.
+// From plan(): few rows, where a group has at most 16 of them, take at most 512 workgroups and one
+// a pair below 256 pairs, 1024 and one a pair up to 341 and three a pair above; else pieces and
+// split units make at most one round.  Pieces have two tiles at least.
 size_t attention_workspace_bound(int B, int T, int max_rows, int max_kv, int Hq, int Hkv, int D) {
     const int64_t tiles = ((int64_t)max_kv + kPage - 1) / kPage, most = (tiles + 1) / 2;
     if (most <= 1) return 0;
