@@ -1,4 +1,4 @@
-// Argument checks and calls of the operators between the linears, for the Python
+// Argument checks and calls of the operators around and between the linears, for the Python
 // binding: a Python module of its own (_lib/rudder_bind.so).
 //
 // Their smallest calls take the GPU 3 to 6 us, and checking seven to nine
@@ -15,6 +15,7 @@
 
 #include "rudder.h"
 #include "rudder_attention.h"
+#include "rudder_block.h"
 
 namespace {
 
@@ -28,6 +29,12 @@ struct Library {
     decltype(&rudder_cache_dequant) cache_dequant;
     decltype(&rudder_cache_attention) cache_attention;
     decltype(&rudder_cross_attention) cross_attention;
+    decltype(&rudder_packed_act_bytes) packed_act_bytes;
+    decltype(&rudder_norm) norm;
+    decltype(&rudder_norm_quant) norm_quant;
+    decltype(&rudder_dequant_act) dequant_act;
+    decltype(&rudder_rotary) rotary;
+    decltype(&rudder_prompt_attention) prompt_attention;
 } lib = {};
 
 struct Failure {};                                 // a Python error is set
@@ -133,6 +140,7 @@ T* array(Args& a, const char* name, PyObject* o, at::ScalarType type, long long 
         refuse(name, o, "expected at least ", least,
                type == at::kBFloat16 ? "contiguous bf16 elements"
                : type == at::kFloat  ? "contiguous fp32 elements"
+               : type == at::kDouble ? "contiguous fp64 elements"
                : type == at::kInt    ? "contiguous int32 elements"
                : type == at::kChar   ? "contiguous int8 elements"
                                      : "contiguous uint8 elements");
@@ -365,6 +373,125 @@ PyObject* cross_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// (device, X, R, gamma, eps, M, K, H, Y, stream, ldx, ldr, ldh, ldy)
+PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&] {
+        Args a("rudder_norm", args, n, 14);
+        PyObject *X = a.next(), *R = a.next(), *gamma = a.next();
+        const float eps = a.real();
+        const int M = a.integer(), K = a.integer();
+        PyObject *H = a.next(), *Y = a.next();
+        void* stream = a.stream();
+        int ldx = 0, ldr = 0, ldh = 0, ldy = 0;
+        const auto* x = rows(a, "X", X, M, 1, K, a.next(), ldx);
+        const auto* r = rows(a, "R", R, M, 1, K, a.next(), ldr);
+        auto* h = rows(a, "H", H, M, 1, K, a.next(), ldh);
+        auto* y = rows(a, "Y", Y, M, 1, K, a.next(), ldy);
+        const auto* g = array<float>(a, "gamma", gamma, at::kFloat, K);
+        return call([&] {
+            return lib.norm(x, r, g, eps, M, K, ldx, ldr, ldh, ldy, h, y, stream);
+        });
+    });
+}
+
+// (device, X, R, stream_id, gamma, inv_smooth, act_scale, eps, M, K, S, abits, codes, H, Xq,
+//  row_scale, stream, ldx, ldr, ldh)
+PyObject* norm_quant(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&] {
+        Args a("rudder_norm_quant", args, n, 20);
+        PyObject *X = a.next(), *R = a.next(), *sid = a.next(), *gamma = a.next(),
+                 *smooth = a.next(), *table = a.next();
+        const float eps = a.real();
+        const int M = a.integer(), K = a.integer(), S = a.integer(), abits = a.integer(),
+                  codes = a.integer();
+        PyObject *H = a.next(), *Xq = a.next(), *scale = a.next();
+        void* stream = a.stream();
+        int ldx = 0, ldr = 0, ldh = 0;
+        const auto* x = rows(a, "X", X, M, 1, K, a.next(), ldx);
+        const auto* r = rows(a, "R", R, M, 1, K, a.next(), ldr);
+        auto* h = rows(a, "H", H, M, 1, K, a.next(), ldh);
+        const auto* st = array<uint8_t>(a, "stream_id", sid, at::kByte, M);
+        const auto* g = array<float>(a, "gamma", gamma, at::kFloat, K);
+        const auto* is = array<float>(a, "inv_smooth", smooth, at::kFloat, K);
+        const auto* d = array<float>(a, "act_scale", table, at::kFloat, S);
+        auto* q = array<void>(a, "Xq", Xq, at::kByte,
+                              (long long)lib.packed_act_bytes(M, K, abits, codes));
+        auto* s = array<float>(a, "row_scale", scale, at::kFloat, M);
+        return call([&] {
+            return lib.norm_quant(x, r, st, g, is, d, eps, M, K, S, abits, codes, ldx, ldr, ldh, h,
+                                  q, s, stream);
+        });
+    });
+}
+
+// (device, Xq, row_scale, M, K, abits, codes, out, stream)
+PyObject* dequant_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&] {
+        Args a("rudder_dequant_act", args, n, 9);
+        PyObject *Xq = a.next(), *scale = a.next();
+        const int M = a.integer(), K = a.integer(), abits = a.integer(), codes = a.integer();
+        const auto* q = array<void>(a, "Xq", Xq, at::kByte,
+                                    (long long)lib.packed_act_bytes(M, K, abits, codes));
+        const auto* s = array<float>(a, "row_scale", scale, at::kFloat, M);
+        auto* out = array<float>(a, "out", a.next(), at::kFloat, product(M, K));
+        void* stream = a.stream();
+        return call([&] { return lib.dequant_act(q, s, M, K, abits, codes, out, stream); });
+    });
+}
+
+// (device, Q, K, row_start, pos, freq, magnitude, B, T, max_rows, Hq, Hkv, D, rotary_dim, layout,
+//  Qo, Ko, stream, ldq, ldk, ldqo, ldko)
+PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&] {
+        Args a("rudder_rotary", args, n, 22);
+        PyObject *Q = a.next(), *K = a.next(), *start = a.next(), *pos = a.next(),
+                 *freq = a.next();
+        const float magnitude = a.real();
+        const int B = a.integer(), T = a.integer(), max_rows = a.integer(), Hq = a.integer(),
+                  Hkv = a.integer(), D = a.integer(), part = a.integer(), layout = a.integer();
+        PyObject *Qo = a.next(), *Ko = a.next();
+        void* stream = a.stream();
+        int ldq = 0, ldk = 0, ldqo = 0, ldko = 0;
+        const auto* q = rows(a, "Q", Q, T, Hq, D, a.next(), ldq);
+        const auto* k = rows(a, "K", K, T, Hkv, D, a.next(), ldk);
+        auto* qo = rows(a, "Qo", Qo, T, Hq, D, a.next(), ldqo);
+        auto* ko = rows(a, "Ko", Ko, T, Hkv, D, a.next(), ldko);
+        const auto* rs = array<int32_t>(a, "row_start", start, at::kInt, (long long)B + 1);
+        const auto* ps = array<int32_t>(a, "pos", pos, at::kInt, B);
+        const auto* fr = array<double>(a, "freq", freq, at::kDouble, part / 2);
+        return call([&] {
+            return lib.rotary(q, k, rs, ps, fr, magnitude, B, T, max_rows, Hq, Hkv, D, part,
+                              layout, ldq, ldk, ldqo, ldko, qo, ko, stream);
+        });
+    });
+}
+
+// (device, Q, K, V, row_start, B, T, max_rows, Hq, Hkv, D, sm, workspace, O, stream, ldq, ldk, ldv,
+//  ldo)
+PyObject* prompt_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&] {
+        Args a("rudder_prompt_attention", args, n, 19);
+        PyObject *Q = a.next(), *K = a.next(), *V = a.next(), *start = a.next();
+        const int B = a.integer(), T = a.integer(), max_rows = a.integer(), Hq = a.integer(),
+                  Hkv = a.integer(), D = a.integer();
+        const float sm = a.real();
+        size_t bytes = 0;
+        void* ws = workspace(a, bytes);
+        PyObject* O = a.next();
+        void* stream = a.stream();
+        int ldq = 0, ldk = 0, ldv = 0, ldo = 0;
+        const auto* q = rows(a, "Q", Q, T, Hq, D, a.next(), ldq);
+        const auto* k = rows(a, "K", K, T, Hkv, D, a.next(), ldk);
+        const auto* v = rows(a, "V", V, T, Hkv, D, a.next(), ldv);
+        auto* o = rows(a, "O", O, T, Hq, D, a.next(), ldo);
+        const auto* rs = array<int32_t>(a, "row_start", start, at::kInt, (long long)B + 1);
+        return call([&] {
+            return lib.prompt_attention(q, k, v, rs, B, T, max_rows, Hq, Hkv, D, ldq, ldk, ldv,
+                                        ldo, sm, ws, bytes, o, stream);
+        });
+    });
+}
+
 // use(path): takes the entry points from the library loaded from there.
 PyObject* use(PyObject*, PyObject* path) {
     const char* name = PyUnicode_AsUTF8(path);
@@ -384,6 +511,12 @@ PyObject* use(PyObject*, PyObject* path) {
     find(l.cache_dequant, "rudder_cache_dequant");
     find(l.cache_attention, "rudder_cache_attention");
     find(l.cross_attention, "rudder_cross_attention");
+    find(l.packed_act_bytes, "rudder_packed_act_bytes");
+    find(l.norm, "rudder_norm");
+    find(l.norm_quant, "rudder_norm_quant");
+    find(l.dequant_act, "rudder_dequant_act");
+    find(l.rotary, "rudder_rotary");
+    find(l.prompt_attention, "rudder_prompt_attention");
     if (!all) return PyErr_Format(PyExc_ImportError, "%s: %s", name, dlerror());
     lib = l;
     Py_RETURN_NONE;
@@ -399,10 +532,15 @@ PyMethodDef methods[] = {
     RUDDER_METHOD(cache_dequant),
     RUDDER_METHOD(cache_attention),
     RUDDER_METHOD(cross_attention),
+    RUDDER_METHOD(norm),
+    RUDDER_METHOD(norm_quant),
+    RUDDER_METHOD(dequant_act),
+    RUDDER_METHOD(rotary),
+    RUDDER_METHOD(prompt_attention),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rudder_bind",
-                      "Argument checks and calls of the operators between the linears.", -1,
+                      "Argument checks and calls of the operators around and between the linears.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,11 +1,13 @@
 // C ABI of librudder: argument validation, error reporting and dispatch to
 // the kernel launchers.  Nothing is launched unless every check passes.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
 #include <string>
 
+#include "rudder_block_launch.h"
 #include "rudder_internal.h"
 #include "rudder_operators.h"
 
@@ -577,6 +579,250 @@ rudder_status_t rudder_cross_attention(const uint16_t* Q, const uint16_t* K, con
                                                    Tkv, max_rows, max_kv, Hq, Hkv, D, ldq, ldk,
                                                    ldv, ldo, sm, workspace, O,
                                                    static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+// ---------------------------------------------------------------------------
+// Norms, rotary positions and prompt attention (include/rudder_block.h).
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxBlockRows = 1 << 25;             // a launch's threads stay below 2^32
+constexpr int64_t kMaxElements = (int64_t)1 << 35;
+
+rudder_status_t check_rows(const char* f, int M, int K) {
+    if (K > RUDDER_MAX_K)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: K=%d exceeds %d", f, K, RUDDER_MAX_K);
+    if (M > kMaxBlockRows || (int64_t)M * K > kMaxElements)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: M=%d rows of K=%d exceed 2^25 rows or 2^35 "
+                    "elements", f, M, K);
+    return RUDDER_OK;
+}
+
+rudder_status_t check_codes(const char* f, int K, int abits, int codes) {
+    if (K % 32) return fail(RUDDER_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 32", f, K);
+    if (abits != 4 && abits != 8)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: abits=%d must be 4 or 8", f, abits);
+    if (codes != RUDDER_CODES_INT && codes != RUDDER_CODES_E2M3)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: unknown code container %d", f, codes);
+    if (codes == RUDDER_CODES_E2M3 && K % 64)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 64 for E2M3 codes", f,
+                    K);
+    return RUDDER_OK;
+}
+
+rudder_status_t check_norm(const char* f, const void* X, const void* R, const void* gamma,
+                           float eps, int M, int K, int ldx, int ldr, int ldh, const void* H) {
+    if (!X || !gamma) return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (!R != !H) return fail(RUDDER_ERR_INVALID_ARG, "%s: R and H come together", f);
+    if (M < 0 || K <= 0 || K % 8)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: M=%d must be >= 0 and K=%d a positive multiple "
+                    "of 8", f, M, K);
+    rudder_status_t st = check_ld(f, "ldx", ldx, 1, K);
+    if (st == RUDDER_OK && R) st = check_ld(f, "ldr", ldr, 1, K);
+    if (st == RUDDER_OK && R) st = check_ld(f, "ldh", ldh, 1, K);
+    if (st != RUDDER_OK) return st;
+    if (!(eps >= 0.0f && eps <= 3.4028234663852886e38f))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", f);
+    if (misaligned(X) || misaligned(R) || misaligned(H) || misaligned(gamma))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: X, R, H and gamma must be 16-byte aligned", f);
+    return RUDDER_OK;
+}
+
+}  // namespace
+
+rudder_status_t rudder_norm(const uint16_t* X, const uint16_t* R, const float* gamma, float eps,
+                            int M, int K, int ldx, int ldr, int ldh, int ldy, uint16_t* H,
+                            uint16_t* Y, void* stream) {
+    const char* f = "rudder_norm";
+    if (!Y) return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    rudder_status_t st = check_norm(f, X, R, gamma, eps, M, K, ldx, ldr, ldh, H);
+    if (st == RUDDER_OK) st = check_ld(f, "ldy", ldy, 1, K);
+    if (st != RUDDER_OK) return st;
+    if (misaligned(Y)) return fail(RUDDER_ERR_INVALID_ARG, "%s: Y must be 16-byte aligned", f);
+    if (Y == H) return fail(RUDDER_ERR_INVALID_ARG, "%s: Y and H are one buffer", f);
+    if ((st = check_rows(f, M, K)) != RUDDER_OK) return st;
+    if (M == 0) return ok();
+    return from_hip(rudder::launch_norm(X, R, nullptr, gamma, nullptr, nullptr, eps, M, K, ldx,
+                                        ldr, ldh, ldy, 0, 0, H, Y, nullptr, nullptr,
+                                        static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_norm_quant(const uint16_t* X, const uint16_t* R, const uint8_t* stream_id,
+                                  const float* gamma, const float* inv_smooth,
+                                  const float* act_scale, float eps, int M, int K, int S,
+                                  int abits, int codes, int ldx, int ldr, int ldh, uint16_t* H,
+                                  void* Xq, float* row_scale, void* stream) {
+    const char* f = "rudder_norm_quant";
+    if (!inv_smooth || !Xq || !row_scale)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (act_scale && !stream_id)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: act_scale needs stream_id", f);
+    rudder_status_t st = check_norm(f, X, R, gamma, eps, M, K, ldx, ldr, ldh, H);
+    if (st == RUDDER_OK) st = check_codes(f, K, abits, codes);
+    if (st != RUDDER_OK) return st;
+    if (act_scale && (S < 1 || S > RUDDER_MAX_STREAMS))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: S=%d must be in 1..%d", f, S, RUDDER_MAX_STREAMS);
+    if (misaligned(inv_smooth) || misaligned(Xq))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: inv_smooth and Xq must be 16-byte aligned", f);
+    if (codes == RUDDER_CODES_E2M3 && abits == 8)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: 8-bit E2M3 codes are not built for this path", f);
+    if ((st = check_rows(f, M, K)) != RUDDER_OK) return st;
+    if (M == 0) return ok();
+    return from_hip(rudder::launch_norm(X, R, stream_id, gamma, inv_smooth, act_scale, eps, M, K,
+                                        ldx, ldr, ldh, 0, abits, codes, H, nullptr, Xq, row_scale,
+                                        static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_dequant_act(const void* Xq, const float* row_scale, int M, int K, int abits,
+                                   int codes, float* out, void* stream) {
+    const char* f = "rudder_dequant_act";
+    if (!Xq || !row_scale || !out)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (M < 0 || K <= 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: M=%d must be >= 0 and K=%d > 0", f, M, K);
+    rudder_status_t st = check_codes(f, K, abits, codes);
+    if (st != RUDDER_OK) return st;
+    if (misaligned(Xq) || misaligned(out))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Xq and out must be 16-byte aligned", f);
+    if ((st = check_rows(f, M, K)) != RUDDER_OK) return st;
+    if (M == 0) return ok();
+    return from_hip(rudder::launch_dequant_act(static_cast<const uint8_t*>(Xq), row_scale, M, K,
+                                               abits, codes, out,
+                                               static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+rudder_status_t rudder_rotary_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                          double trained, double low, double high, double* freq) {
+    const char* f = "rudder_rotary_frequencies";
+    if (!freq) return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (rotary_dim <= 0 || rotary_dim % 2)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: rotary_dim=%d must be positive and even", f,
+                    rotary_dim);
+    const double most = 1.7976931348623157e308;
+    if (!(base > 0 && base <= most))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: base must be positive and finite", f);
+    if (scaling < RUDDER_ROTARY_PLAIN || scaling > RUDDER_ROTARY_PARTS)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: unknown scaling %d", f, scaling);
+    if (scaling != RUDDER_ROTARY_PLAIN && !(factor >= 1 && factor <= most))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: factor must be finite and at least 1", f);
+    const bool parts = scaling == RUDDER_ROTARY_PARTS;
+    if (parts && !(trained > 0 && trained <= most && low >= 0 && high > low && high <= most))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: by parts, trained must be positive, low >= 0, "
+                    "high above low, all finite", f);
+    if (rotary_dim > (1 << 16))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: rotary_dim=%d exceeds %d", f, rotary_dim, 1 << 16);
+    const int n = rotary_dim / 2;
+    if (scaling == RUDDER_ROTARY_BASE && n > 1) base *= pow(factor, (double)n / (n - 1));
+    for (int i = 0; i < n; ++i) {
+        double x = pow(base, -(double)i / n);
+        if (scaling == RUDDER_ROTARY_LINEAR) x /= factor;
+        if (parts) {
+            const double turns = trained * x / 6.283185307179586;
+            const double keep = fmin(fmax((turns - low) / (high - low), 0.0), 1.0);
+            x = x / factor * (1 - keep) + x * keep;
+        }
+        freq[i] = x;
+    }
+    return ok();
+}
+
+rudder_status_t rudder_rotary(const uint16_t* Q, const uint16_t* K, const int32_t* row_start,
+                              const int32_t* pos, const double* freq, float magnitude, int B,
+                              int T, int max_rows, int Hq, int Hkv, int D, int rotary_dim,
+                              int layout, int ldq, int ldk, int ldqo, int ldko, uint16_t* Qo,
+                              uint16_t* Ko, void* stream) {
+    const char* f = "rudder_rotary";
+    if (!Q || !row_start || !freq || !Qo || (Hkv != 0 && (!K || !Ko)))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (B < 0 || T < 0 || max_rows < 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: B=%d, T=%d and max_rows=%d must be >= 0", f, B, T,
+                    max_rows);
+    if (Hq <= 0 || Hkv < 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Hq=%d must be positive and Hkv=%d >= 0", f, Hq,
+                    Hkv);
+    if (layout != RUDDER_ROTARY_HALF && layout != RUDDER_ROTARY_PAIRS)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: unknown layout %d", f, layout);
+    rudder_status_t st = check_heads(f, Hq, D);
+    if (st == RUDDER_OK && Hkv) st = check_heads(f, Hkv, D);
+    if (st != RUDDER_OK) return st;
+    if (rotary_dim <= 0 || rotary_dim > D || rotary_dim % 16)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: rotary_dim=%d must be a positive multiple of 16 "
+                    "up to D=%d", f, rotary_dim, D);
+    if ((st = check_ld(f, "ldq", ldq, Hq, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldqo", ldqo, Hq, D)) != RUDDER_OK) return st;
+    if (Hkv && (st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
+    if (Hkv && (st = check_ld(f, "ldko", ldko, Hkv, D)) != RUDDER_OK) return st;
+    if (!(fabsf(magnitude) <= 3.4028234663852886e38f))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: magnitude must be finite", f);
+    if (misaligned(Q) || misaligned(Qo) || (Hkv && (misaligned(K) || misaligned(Ko))))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Q, K, Qo and Ko must be 16-byte aligned", f);
+    if (B > kMaxSequences)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d exceeds %d", f, B, kMaxSequences);
+    if ((max_rows < T ? max_rows : T) > kMaxBlockRows)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d exceeds %d", f, max_rows,
+                    kMaxBlockRows);
+    if (B == 0 || T == 0 || max_rows == 0) return ok();
+    return from_hip(rudder::launch_rotary(Q, K, row_start, pos, freq, magnitude, B, T, max_rows,
+                                          Hq, Hkv, D, rotary_dim, layout, ldq, ldk, ldqo, ldko, Qo,
+                                          Ko, static_cast<hipStream_t>(stream)),
+                    f);
+}
+
+size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int Hq, int Hkv,
+                                               int D) {
+    size_t bytes = 0;
+    if (!attention_sizes(B, T, max_rows, 0, Hq, Hkv, D) ||
+        !rudder::prompt_attention_workspace(B, T, max_rows, Hq, Hkv, D, bytes))
+        return 0;
+    return bytes;
+}
+
+rudder_status_t rudder_prompt_attention(const uint16_t* Q, const uint16_t* K, const uint16_t* V,
+                                        const int32_t* row_start, int B, int T, int max_rows,
+                                        int Hq, int Hkv, int D, int ldq, int ldk, int ldv, int ldo,
+                                        float sm, void* workspace, size_t workspace_bytes,
+                                        uint16_t* O, void* stream) {
+    const char* f = "rudder_prompt_attention";
+    if (!Q || !K || !V || !row_start || !O)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
+    if (B < 0 || T < 0 || max_rows < 0)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: B=%d, T=%d and max_rows=%d must be >= 0", f, B, T,
+                    max_rows);
+    rudder_status_t st = check_heads(f, Hkv, D);
+    if (st != RUDDER_OK) return st;
+    if (Hq <= 0 || Hq % Hkv)
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Hq=%d must be a positive multiple of Hkv=%d", f,
+                    Hq, Hkv);
+    if ((st = check_ld(f, "ldq", ldq, Hq, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldk", ldk, Hkv, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldv", ldv, Hkv, D)) != RUDDER_OK) return st;
+    if ((st = check_ld(f, "ldo", ldo, Hq, D)) != RUDDER_OK) return st;
+    if (!(sm >= -kMaxSoftmaxScale && sm <= kMaxSoftmaxScale))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: sm must be finite and at most 2^127", f);
+    if (misaligned(Q) || misaligned(K) || misaligned(V) || misaligned(O) || misaligned(workspace))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: Q, K, V, O and workspace must be 16-byte aligned",
+                    f);
+    if ((int64_t)B * Hkv > kMaxSequences)
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d with Hkv=%d exceeds %d", f, B, Hkv,
+                    kMaxSequences);
+    if ((int64_t)(max_rows < T ? max_rows : T) * Hq > (1 << 26))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d with Hq=%d exceeds 2^26 rows", f,
+                    max_rows, Hq);
+    if (B == 0 || T == 0 || max_rows == 0) return ok();
+    size_t need = 0;
+    if (!rudder::prompt_attention_workspace(B, T, max_rows, Hq, Hkv, D, need))
+        return fail(RUDDER_ERR_UNSUPPORTED, "%s: B=%d sequences of max_rows=%d rows exceed a launch",
+                    f, B, max_rows);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: these sizes need a workspace of %zu bytes, not "
+                    "%zu", f, need, workspace ? workspace_bytes : (size_t)0);
+    return from_hip(rudder::launch_prompt_attention(Q, K, V, row_start, B, T, max_rows, Hq, Hkv, D,
+                                                    ldq, ldk, ldv, ldo, sm, workspace, O,
+                                                    static_cast<hipStream_t>(stream)),
                     f);
 }
 

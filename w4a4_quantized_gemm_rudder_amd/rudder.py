@@ -18,6 +18,12 @@ The calls keep their C names and meanings:
                            -- the paged 8-bit cache of keys and values
   rudder_cache_attention, rudder_cross_attention
                            -- attention over that cache, and to bf16 states
+  rudder_norm, rudder_norm_quant, rudder_dequant_act
+                           -- the RMS norm with the residual's addition, its rows or
+                              the next linear's codes, and codes back as values
+  rudder_rotary, rudder_rotary_frequencies
+                           -- rotary positions on queries and keys
+  rudder_prompt_attention  -- causal attention of whole prompts
 (SteerQuant = "SteerQuant: Steering Quantization Error with Action-Guided
 Scaling in World-Action Models", paperlayer.ai digest.)
 """
@@ -41,6 +47,9 @@ RUDDER_ERR_UNSUPPORTED = 2
 RUDDER_ERR_HIP = 3
 MAX_STREAMS = 8
 CACHE_PAGE = 64     # tokens of a cache page
+ROTARY_HALF = 0     # rotary pairs: channels i and i + n of the rotated part
+ROTARY_PAIRS = 1    # channels 2 i and 2 i + 1
+ROTARY_SCALING = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 
 EXPORTED = (
     "rudder_packed_weight_bytes", "rudder_packed_act_bytes", "rudder_quant_act_workspace_bytes",
@@ -55,6 +64,8 @@ EXPORTED = (
     "rudder_cache_page_bytes", "rudder_cache_append", "rudder_cache_dequant",
     "rudder_attention_workspace_bytes", "rudder_attention_workspace_bound",
     "rudder_cache_attention", "rudder_cross_attention",
+    "rudder_norm", "rudder_norm_quant", "rudder_dequant_act", "rudder_rotary_frequencies",
+    "rudder_rotary", "rudder_prompt_attention_workspace_bytes", "rudder_prompt_attention",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -134,6 +145,21 @@ def load_library() -> ctypes.CDLL:
     lib.rudder_cache_attention.restype = i
     lib.rudder_cross_attention.argtypes = [vp] * 6 + [i] * 12 + [f, vp, sz, vp, vp]
     lib.rudder_cross_attention.restype = i
+    d = ctypes.c_double
+    lib.rudder_norm.argtypes = [vp, vp, vp, f] + [i] * 6 + [vp, vp, vp]
+    lib.rudder_norm.restype = i
+    lib.rudder_norm_quant.argtypes = [vp] * 6 + [f] + [i] * 8 + [vp, vp, vp, vp]
+    lib.rudder_norm_quant.restype = i
+    lib.rudder_dequant_act.argtypes = [vp, vp, i, i, i, i, vp, vp]
+    lib.rudder_dequant_act.restype = i
+    lib.rudder_rotary_frequencies.argtypes = [i, d, i, d, d, d, d, vp]
+    lib.rudder_rotary_frequencies.restype = i
+    lib.rudder_rotary.argtypes = [vp] * 5 + [f] + [i] * 12 + [vp, vp, vp]
+    lib.rudder_rotary.restype = i
+    lib.rudder_prompt_attention_workspace_bytes.argtypes = [i] * 6
+    lib.rudder_prompt_attention_workspace_bytes.restype = sz
+    lib.rudder_prompt_attention.argtypes = [vp] * 4 + [i] * 10 + [f, vp, sz, vp, vp]
+    lib.rudder_prompt_attention.restype = i
     lib.rudder_status_string.argtypes = [i]
     lib.rudder_status_string.restype = ctypes.c_char_p
     lib.rudder_last_error.argtypes = []
@@ -398,6 +424,71 @@ def rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B: int, T: int,
 
 
 # ---------------------------------------------------------------------------
+# Norms, rotary positions and prompt attention (include/rudder_block.h), checked
+# in the same place
+# ---------------------------------------------------------------------------
+
+def rudder_norm(X, R, gamma, eps: float, M: int, K: int, H, Y, stream=None, ldx=None, ldr=None,
+                ldh=None, ldy=None) -> None:
+    """X, R, H, Y: [M, K], rows any distance apart; R and H both or neither."""
+    bind = _bind or _load_bind()
+    device, handle = _device_and_stream(stream)
+    _check(bind.norm(device, X, R, gamma, eps, M, K, H, Y, handle, ldx, ldr, ldh, ldy))
+
+
+def rudder_norm_quant(X, R, stream_id, gamma, inv_smooth, act_scale, eps: float, M: int, K: int,
+                      S: int, abits: int, codes: int, H, Xq, row_scale, stream=None, ldx=None,
+                      ldr=None, ldh=None) -> None:
+    """X, R, H: [M, K], rows any distance apart; act_scale None: a step size a row."""
+    bind = _bind or _load_bind()
+    device, handle = _device_and_stream(stream)
+    _check(bind.norm_quant(device, X, R, stream_id, gamma, inv_smooth, act_scale, eps, M, K, S,
+                           abits, codes, H, Xq, row_scale, handle, ldx, ldr, ldh))
+
+
+def rudder_dequant_act(Xq, row_scale, M: int, K: int, abits: int, codes: int, out,
+                       stream=None) -> None:
+    bind = _bind or _load_bind()
+    device, handle = _device_and_stream(stream)
+    _check(bind.dequant_act(device, Xq, row_scale, M, K, abits, codes, out, handle))
+
+
+def rudder_rotary_frequencies(rotary_dim: int, base: float, scaling: int, factor: float,
+                              trained: float, low: float, high: float, freq) -> None:
+    """freq: a contiguous fp64 tensor of rotary_dim / 2 elements in host memory."""
+    import torch
+    if freq.dtype != torch.float64 or freq.device.type != "cpu" or freq.numel() < rotary_dim // 2:
+        raise ValueError("freq: at least rotary_dim / 2 fp64 elements in host memory expected")
+    _check(load_library().rudder_rotary_frequencies(rotary_dim, base, scaling, factor, trained,
+                                                    low, high, _ptr(freq)))
+
+
+def rudder_rotary(Q, K, row_start, pos, freq, magnitude: float, B: int, T: int, max_rows: int,
+                  Hq: int, Hkv: int, D: int, rotary_dim: int, layout: int, Qo, Ko, stream=None,
+                  ldq=None, ldk=None, ldqo=None, ldko=None) -> None:
+    """Q, K, Qo, Ko: [T, H, D] or [T, H * D], rows any distance apart; Qo and Ko may be Q and K."""
+    bind = _bind or _load_bind()
+    device, handle = _device_and_stream(stream)
+    _check(bind.rotary(device, Q, K, row_start, pos, freq, magnitude, B, T, max_rows, Hq, Hkv, D,
+                       rotary_dim, layout, Qo, Ko, handle, ldq, ldk, ldqo, ldko))
+
+
+def prompt_attention_workspace_bytes(B: int, T: int, max_rows: int, Hq: int, Hkv: int,
+                                     D: int) -> int:
+    return int(load_library().rudder_prompt_attention_workspace_bytes(B, T, max_rows, Hq, Hkv, D))
+
+
+def rudder_prompt_attention(Q, K, V, row_start, B: int, T: int, max_rows: int, Hq: int, Hkv: int,
+                            D: int, sm: float, workspace, O, stream=None, ldq=None, ldk=None,
+                            ldv=None, ldo=None) -> None:
+    """Q, K, V, O: [T, H, D] or [T, H * D], rows any distance apart."""
+    bind = _bind or _load_bind()
+    device, handle = _device_and_stream(stream)
+    _check(bind.prompt_attention(device, Q, K, V, row_start, B, T, max_rows, Hq, Hkv, D, sm,
+                                 workspace, O, handle, ldq, ldk, ldv, ldo))
+
+
+# ---------------------------------------------------------------------------
 # Allocating conveniences (torch allocates; the library computes)
 # ---------------------------------------------------------------------------
 
@@ -594,6 +685,95 @@ def cross_attention(Q, K, V, row_start, kv_start, kv_len, max_rows: int, max_kv:
         if T and B and Tkv:
             rudder_cross_attention(Q, K, V, row_start, kv_start, kv_len, B, T, Tkv, max_rows,
                                    max_kv, Hq, Hkv, D, sm, ws, O)
+    return O
+
+
+def norm(X, gamma, eps: float, residual=None, stream=None):
+    """RMS norm of X bf16 [M, K], gamma fp32 [K].  Returns Y bf16 [M, K]; with `residual` [M, K]
+    (Y, H) of the sum H = bf16(residual + X)."""
+    import torch
+    M, K = X.shape
+    with _on(stream, X.device):
+        Y = torch.empty(M, K, dtype=torch.bfloat16, device=X.device)
+        H = None if residual is None else torch.empty_like(Y)
+        if M:
+            rudder_norm(X, residual, gamma, eps, M, K, H, Y)
+    return Y if H is None else (Y, H)
+
+
+def norm_quant(X, gamma, inv_smooth, eps: float, abits: int, codes: int = CODES_INT,
+               stream_id=None, act_scale=None, residual=None, stream=None):
+    """The same norm as the next linear's packed codes: with stream_id uint8 [M] and act_scale
+    fp32 [S] the table's step sizes, without them one a row.  Returns (Xq uint8, row_scale fp32
+    [M]), with `residual` (Xq, row_scale, H)."""
+    import torch
+    M, K = X.shape
+    S = 1 if act_scale is None else act_scale.numel()
+    with _on(stream, X.device):
+        Xq = torch.empty(max(packed_act_bytes(M, K, abits, codes), 1), dtype=torch.uint8,
+                         device=X.device)
+        row_scale = torch.empty(max(M, 1), dtype=torch.float32, device=X.device)
+        H = None
+        if residual is not None:
+            H = torch.empty(M, K, dtype=torch.bfloat16, device=X.device)
+        if M:
+            rudder_norm_quant(X, residual, stream_id, gamma, inv_smooth, act_scale, eps, M, K, S,
+                              abits, codes, H, Xq, row_scale)
+    return (Xq, row_scale) if H is None else (Xq, row_scale, H)
+
+
+def dequant_act(Xq, row_scale, M: int, K: int, abits: int, codes: int = CODES_INT, stream=None):
+    """The values of packed activation codes, fp32 [M, K]."""
+    import torch
+    with _on(stream, Xq.device):
+        out = torch.empty(M, K, dtype=torch.float32, device=Xq.device)
+        if M:
+            rudder_dequant_act(Xq, row_scale, M, K, abits, codes, out)
+    return out
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain",
+                       factor: float = 1.0, trained: float = 0.0, low: float = 1.0,
+                       high: float = 32.0, device="cuda"):
+    """The fp64 frequencies [rotary_dim / 2] that `rotary` takes; scaling "plain", "linear",
+    "base" or "parts" (see include/rudder_block.h)."""
+    import torch
+    freq = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float64)
+    rudder_rotary_frequencies(rotary_dim, base, ROTARY_SCALING[scaling], factor, trained, low,
+                              high, freq)
+    return freq.to(device)
+
+
+def rotary(Q, K, row_start, freq, max_rows: int, pos=None, magnitude: float = 1.0,
+           layout: int = ROTARY_HALF, in_place: bool = False, stream=None):
+    """Rotary positions on Q bf16 [T, Hq, D] and K [T, Hkv, D] (None: Q alone), row i of sequence
+    b at pos[b] + i (None: at i).  Returns (Q', K'): Q and K themselves where in_place, else new
+    tensors (copies in rows of no sequence)."""
+    import torch
+    T, Hq, D = Q.shape
+    Hkv = 0 if K is None else K.shape[1]
+    B = row_start.numel() - 1
+    with _on(stream, Q.device):
+        Qo = Q if in_place else Q.clone(memory_format=torch.contiguous_format)
+        Ko = K if in_place or K is None else K.clone(memory_format=torch.contiguous_format)
+        if T and B:
+            rudder_rotary(Q, K, row_start, pos, freq, magnitude, B, T, max_rows, Hq, Hkv, D,
+                          2 * freq.numel(), layout, Qo, Ko)
+    return Qo, Ko
+
+
+def prompt_attention(Q, K, V, row_start, max_rows: int, sm: float, stream=None):
+    """Causal attention of the prompts row_start [B + 1] of Q bf16 [T, Hq, D] to their own K, V
+    bf16 [T, Hkv, D].  Returns O bf16 [T, Hq, D] (zeros in rows of no sequence)."""
+    import torch
+    T, Hq, D = Q.shape
+    Hkv, B = K.shape[1], row_start.numel() - 1
+    with _on(stream, Q.device):
+        O = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=Q.device)
+        n = prompt_attention_workspace_bytes(B, T, max_rows, Hq, Hkv, D)
+        ws = torch.empty(n, dtype=torch.uint8, device=Q.device) if n else None
+        if T and B:
+            rudder_prompt_attention(Q, K, V, row_start, B, T, max_rows, Hq, Hkv, D, sm, ws, O)
     return O
 
 
