@@ -225,20 +225,27 @@ def test_strides_and_rows_left_alone(rudder):
         used = sum(counts)
         assert torch.equal(out[:used, :Hq * D].cpu().view(used, Hq, D), want[:used])
         assert (out[used:] == 7.0).all() and (out[:, Hq * D:] == 7.0).all()
-        # a bound below the longest prompt leaves its last rows, a loose one changes nothing
+        # a bound below the longest prompt leaves its last rows; a loose one may choose another
+        # kernel, whose sums are rounded in another order: held to the formula as well
         short = max(counts) - 25
         cut = rudder.prompt_attention(*parts, starts, short, 0.1).cpu()
         assert torch.equal(cut[:short], want[:short]) and not cut[short:counts[0]].any()
         assert torch.equal(cut[counts[0]:], want[counts[0]:])
         loose = rudder.prompt_attention(*parts, starts, 10 * T, 0.1).cpu()
-        assert torch.equal(loose, want)
+        rows = torch.cat([torch.arange(40), torch.arange(40, max(counts), 17)])
+        formula, bound = ref.prompt(q, k, v, _starts(counts).tolist(), 0.1, rows=rows)
+        at = torch.cat([r0 + rows[rows < n] for r0, n in zip([0, counts[0]], counts)])
+        aref.assert_within("loose", loose[at], formula[at], bound[at])
+        assert not loose[used:].any()
         # the first and the last sequence are clamped to the buffer, the second is empty
         odd = torch.tensor([-9, counts[0], counts[0] - 50, 10**9], dtype=torch.int32).cuda()
         got = rudder.prompt_attention(*parts, odd, T, 0.1).cpu()
-        assert torch.equal(got[:counts[0] - 50], want[:counts[0] - 50])
+        at = rows[rows < counts[0] - 50]
+        aref.assert_within("clamped", got[at], formula[at], bound[at])
         tail = _run(rudder, q[counts[0] - 50:], k[counts[0] - 50:], v[counts[0] - 50:],
                     [T - counts[0] + 50], 0.1)
-        assert torch.equal(got[counts[0]:], tail[50:])
+        assert torch.allclose(got[counts[0]:].float(), tail[50:].float(), rtol=4 * aref.BF16,
+                              atol=4 * aref.BF16)
 
 
 def test_same_bits_again(rudder):

@@ -18,6 +18,7 @@
 // most 2^-32 of it below.  The power is a multiple of 8, so that tiles of like
 // values share one; where one differs, O follows the smallest.
 #include <cmath>
+#include <type_traits>
 
 #include "rudder_block_launch.h"
 
@@ -30,6 +31,9 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_acc __attribute__((ext_vector_type(16)));
 
+// Lambdas that hold registers of the kernel around them: a call would put those into memory.
+#define RUDDER_INLINE __attribute__((always_inline))
+
 constexpr int kTile = 64;                          // keys
 constexpr int kWaveRows = 32;                      // query rows a wave
 constexpr float kLog2e = 1.4426950408889634f;
@@ -40,7 +44,8 @@ constexpr float kLazy = 6.0f;
 struct Prompt {
     const uint16_t *Q, *K, *V;
     const int32_t* row_start;
-    int T, max_rows, G, Hkv, pairs, tile_rows;
+    int T, max_rows, G, Hkv, tile_rows;
+    int dies, die_pairs, group;                    // order of the work units, see place_unit()
     size_t ldq, ldk, ldv, ldo;
     float sm;
     uint16_t* O;
@@ -75,6 +80,39 @@ __device__ __forceinline__ f32x16_acc mma_f16(uint4 a, uint4 b, f32x16_acc c) {
     x.u = a;
     y.u = b;
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(x.v, y.v, c, 0, 0, 0);
+}
+
+// Unit number -> (key head, sequence) pair and row tile.  Workgroups go round robin to the eight
+// dies: where the pairs divide by eight, the units of a pair, which read the same keys, are kept on
+// one (dies = 8, else 1).  A die's pairs are taken `group` at a time, the units of a group longest
+// first over all its pairs, whose order turns by one from length to length: workgroups go round robin
+// to the parts of a die too, and without the turn the longest of four prompts has a quarter of it
+// (twelve prompts up to 4801 tokens 1749 us, in turn 832).
+struct Unit {
+    int b, h, tile;
+};
+__device__ __forceinline__ Unit place_unit(const Prompt& p) {
+    const int slot = quotient(blockIdx.x, p.dies), low = blockIdx.x - slot * p.dies;
+    const int g = quotient(slot, p.group * p.tile_rows), i = slot - g * (p.group * p.tile_rows);
+    const int size = min(p.group, p.die_pairs - g * p.group);      // the last group may be smaller
+    const int up = quotient(i, size);
+    const int of = i - up * size + up, r = of - quotient(of, size) * size;
+    const int pair = low + p.dies * (g * p.group + r);
+    const int b = quotient(pair, p.Hkv);
+    return {b, pair - b * p.Hkv, p.tile_rows - 1 - up};
+}
+
+// Two fp16 numbers a word, times a power of two.
+__device__ __forceinline__ uint4 times(uint4 x, float f) {
+    union { uint32_t u[4]; f16x2_t h[4]; } r;
+    r.u[0] = x.x;
+    r.u[1] = x.y;
+    r.u[2] = x.z;
+    r.u[3] = x.w;
+    const f16x2_t g = {(_Float16)f, (_Float16)f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.h[i] *= g;
+    return make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
 }
 
 // Largest finite magnitude bits of eight bf16 values, and those that are not finite made zero.
@@ -123,10 +161,8 @@ __global__ void __launch_bounds__(256) prompt_tile_kernel(const Prompt p) {
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // longest rows first; the units of a pair, eight apart, on one die where pairs divide by eight
-    const int up = quotient(blockIdx.x, p.pairs), pair = blockIdx.x - up * p.pairs;
-    const int b = quotient(pair, p.Hkv), h = pair - b * p.Hkv;
-    const int first = (p.tile_rows - 1 - up) * kRows;
+    const Unit unit = place_unit(p);
+    const int b = unit.b, h = unit.h, first = unit.tile * kRows;
     const int r0 = min(max(p.row_start[b], 0), p.T);
     const int n = min(min(max(p.row_start[b + 1], r0), p.T) - r0, p.max_rows);
     const int rows = n * p.G;
@@ -384,12 +420,16 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     }
 }
 
-// 16 bytes a lane from `from` straight to LDS, lane after lane from `lds` on.  In assembly, so that
-// the compiler waits for none of them in front of LDS reads: wait_barrier() orders them.
-__device__ __forceinline__ void load_lds(const void* from, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+// 16 bytes a lane from `from` (the same for all lanes) + `offset` straight to LDS, lane after lane
+// from `lds` on.  In assembly, so that the compiler waits for none of them in front of LDS reads:
+// wait_barrier() orders them.
+__device__ __forceinline__ void load_lds(const void* from, uint32_t offset, uint32_t lds) {
+    const uint64_t a = reinterpret_cast<uint64_t>(from);
+    const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
-                 : "v"(from), "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "v"(offset), "s"(at), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory");
 }
 // All but the wave's last N loads have landed, its LDS reads are done; then the workgroup's barrier.
@@ -403,27 +443,38 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 256 of them a workgroup, two groups of four waves in opposite phases.
+// Many rows: waves of 32 rows that share the tiles in LDS.
 // ---------------------------------------------------------------------------
-// A wave alternates between a phase of products (scores of tile i + 1, values of tile i) and one of
-// vector work (weights of tile i + 1).  Waves w and w + 4 share a vector unit and a matrix core and
-// are one phase apart: group A has its products of step i in phase 2 i, B in 2 i + 1.
-// Tiles come straight to LDS, into rings of four for keys and values each: the vector phase behind
-// step i asks for K of i + 4 and V of i + 3, which are first read in phase 2 i + 6; their places
-// were last read in phase 2 i - 1.
-template <int D>
-__global__ void __launch_bounds__(512, 2) prompt_wide_kernel(const Prompt p) {
-    constexpr int kRows = 8 * kWaveRows, kKS = D / 16, kDT = D / 32, kChunks = D / 8;
-    constexpr int kBytes = kTile * D * 2, kLoads = kBytes / 8192;     // a tile's; a wave's of one
+// Order of a step's N products, their N LDS reads and the vector work beside them.
+template <int N>
+__device__ __forceinline__ void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);     // LDS reads
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // a product
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x400, 1, 0); // an exponential
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // vector instructions
+    }
+}
+
+// A software pipeline over halves of tiles: while the weights of 32 keys are formed on the vector
+// units, the matrix cores work on the scores of the next 32 and the values of the last 32.
+// Tiles come straight to LDS, into rings of RING for keys and values each.  The one barrier of
+// tile i stands between its halves: K of i and V of i - 1 have been read then, their places are
+// asked for K of i + RING and V of i + RING - 1; K of i + 1 and V of i have landed.
+template <int D, int WAVES, int RING>
+__global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt p) {
+    constexpr int kRows = WAVES * kWaveRows, kKS = D / 16, kDT = D / 32, kChunks = D / 8;
+    constexpr int kBytes = kTile * D * 2, kLoads = kBytes / 1024 / WAVES;   // a tile's; a wave's of one
     constexpr int kStride = D * 2 + 16;                               // of an output row in LDS
-    __shared__ __align__(16) uint8_t lds[8 * kBytes];                 // four of keys, four of values
-    static_assert(8 * kWaveRows * kStride <= 8 * kBytes, "the outputs pass through the rings");
+    __shared__ __align__(16) uint8_t lds[2 * RING * kBytes];          // keys, values
+    static_assert(WAVES * kWaveRows * kStride <= 2 * RING * kBytes, "outputs pass through the rings");
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int up = quotient(blockIdx.x, p.pairs), pair = blockIdx.x - up * p.pairs;
-    const int b = quotient(pair, p.Hkv), h = pair - b * p.Hkv;
-    const int first = (p.tile_rows - 1 - up) * kRows;
+    const Unit unit = place_unit(p);
+    const int b = unit.b, h = unit.h, first = unit.tile * kRows;
     const int r0 = min(max(p.row_start[b], 0), p.T);
     const int n = min(min(max(p.row_start[b + 1], r0), p.T) - r0, p.max_rows);
     const int rows = n * p.G;
@@ -433,10 +484,43 @@ __global__ void __launch_bounds__(512, 2) prompt_wide_kernel(const Prompt p) {
     const bool live = row < rows;
     const int t = live ? row / p.G : 0, head = h * p.G + (live ? row % p.G : 0);
     const int limit = live ? t + 1 : 0;            // keys this lane's row sees
-    const int least = quotient(row0, p.G) + 1;     // every row of the wave sees these
+    const int least = row0 < rows ? quotient(row0, p.G) + 1 : 0;       // every row of the wave sees these
     const int most = row0 < rows ? quotient(min(rows, row0 + kWaveRows) - 1, p.G) + 1 : 0;
     const int last = quotient(min(rows, first + kRows) - 1, p.G) + 1;
     const int tiles = (last + kTile - 1) / kTile;
+
+    // this wave's pieces of a tile; tiles behind the last are the last one again, never read; rows
+    // behind the prompt are its last one again
+    const int slot0 = first_slot(r0, b);
+    const uint32_t base = lds_offset(lds);
+    const uint8_t* kp = reinterpret_cast<const uint8_t*>(p.K + (size_t)r0 * p.ldk + (size_t)h * D);
+    const uint8_t* vp = p.images + ((size_t)slot0 * p.Hkv + h) * kBytes;
+    const int whole = n / kTile;                   // tiles that lie in the prompt
+    uint32_t k_from[kLoads], k_end[kLoads];        // in a tile, in the one that ends the prompt
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+        const int key = (wave * kLoads + j) * (64 / kChunks) + lane / kChunks;
+        const uint32_t ck = (lane % kChunks ^ (kChunks == 16 ? key & 15 : key >> 1 & 7)) * 16;
+        const uint32_t step = (uint32_t)p.ldk * 2;
+        k_from[j] = key * step + ck;
+        k_end[j] = min(key, max(n - whole * kTile - 1, 0)) * step + ck;
+    }
+    auto load_keys = [&](int i, int slot) RUDDER_INLINE {
+        const int tile = min(i, tiles - 1);
+        const uint8_t* from = kp + (size_t)tile * kTile * (p.ldk * 2);
+        const bool ends = tile == whole;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            load_lds(from, ends ? k_end[j] : k_from[j],
+                     base + slot * kBytes + (wave * kLoads + j) * 1024);
+    };
+    auto load_values = [&](int i, int slot) RUDDER_INLINE {
+        const uint8_t* from = vp + (size_t)min(i, tiles - 1) * p.Hkv * kBytes;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            load_lds(from, (wave * kLoads + j) * 1024 + lane * 16,
+                     base + (RING + slot) * kBytes + (wave * kLoads + j) * 1024);
+    };
 
     uint4 q[kKS];
     float l = 0.0f, c = fabsf(p.sm) * kLog2e;
@@ -460,43 +544,24 @@ __global__ void __launch_bounds__(512, 2) prompt_wide_kernel(const Prompt p) {
             c = 1.0f;
         }
     }
-
     // notes of 64 tiles, one a lane
-    const int slot0 = first_slot(r0, b);
     const int32_t* notes = p.notes + (size_t)h * p.slots + slot0;
     auto notes_from = [&](int i) { return notes[min(i + lane, tiles - 1)]; };
     int note = notes_from(0);
 
-    // this wave's pieces of a tile; tiles behind the last are the last one again, never read
-    const uint32_t base = lds_offset(lds);
-    const uint8_t* kp = reinterpret_cast<const uint8_t*>(p.K + (size_t)r0 * p.ldk + (size_t)h * D);
-    const uint8_t* vp = p.images + ((size_t)slot0 * p.Hkv + h) * kBytes + lane * 16;
-    auto load_keys = [&](int i) {
-        const int tile = min(i, tiles - 1);
+    load_keys(0, 0);
+    load_values(0, RING - 1);                      // in front of the first tile: weights of 0 meet these
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int piece = wave * kLoads + j, key = piece * (64 / kChunks) + lane / kChunks;
-            const int ck = lane % kChunks ^ (kChunks == 16 ? key & 15 : key >> 1 & 7);
-            load_lds(kp + (size_t)min(tile * kTile + key, n - 1) * (p.ldk * 2) + ck * 16,
-                     base + (i & 3) * kBytes + piece * 1024);
-        }
-    };
-    auto load_values = [&](int i) {
-        const int tile = min(i, tiles - 1);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int piece = wave * kLoads + j;
-            load_lds(vp + (size_t)tile * p.Hkv * kBytes + piece * 1024,
-                     base + (4 + (i & 3)) * kBytes + piece * 1024);
-        }
-    };
+    for (int i = 1; i < RING; ++i) {
+        load_keys(i, i);
+        load_values(i - 1, i - 1);
+    }
 
-    f32x16_acc o[kDT], z[2];
+    f32x16_acc o[kDT], z;
 #pragma unroll
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    uint4 pk[4];
     float m = -INFINITY;
     int scale = 1 << 20;                           // O is held times 2^scale
     int first_bad = 1 << 30;
@@ -504,118 +569,136 @@ __global__ void __launch_bounds__(512, 2) prompt_wide_kernel(const Prompt p) {
 #pragma unroll
     for (int i = 0; i < kKS; ++i) k_at[i] = place<kChunks>(lane & 31, 2 * i + half);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v_at[i] = place<8>(lane & 31, 2 * i + half);
+    for (int i = 0; i < 4; ++i) v_at[i] = RING * kBytes + place<8>(lane & 31, 2 * i + half);
 
-    load_keys(0);
-    load_keys(1);
-    load_values(0);
-    load_keys(2);
-    load_values(1);
-    wait_barrier<4 * kLoads>();
-    if (wave >= 4) wait_barrier<63>();             // group B: one phase behind
-    bool now = false;                              // the wave sees the tile whose V is next
-    for (int i = -1;; ++i) {
-        const bool more = i + 1 < tiles;
-        const int at = (i + 1) * kTile;
-        const bool ahead = more && at < most;
-        if (ahead) {
-            const uint8_t* kt = lds + (i + 1 & 3) * kBytes;
+    auto scores = [&](int slot, int hf) RUDDER_INLINE {
+        f32x16_acc x;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+        for (int j = 0; j < 16; ++j) x[j] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) z[kb][j] = 0.0f;
+        for (int i = 0; i < kKS; ++i)
+            x = mma_bf16(*reinterpret_cast<const uint4*>(lds + k_at[i] + slot * kBytes +
+                                                         hf * 32 * D * 2), q[i], x);
+        return x;
+    };
+    uint4 pend0 = make_uint4(0, 0, 0, 0), pend1 = pend0;       // weights of the 32 keys before
+    auto weigh = [&](int slot, int hf) RUDDER_INLINE {
 #pragma unroll
-            for (int k = 0; k < kKS; ++k)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-                    z[kb] = mma_bf16(
-                        *reinterpret_cast<const uint4*>(kt + k_at[k] + kb * 32 * D * 2), q[k],
-                        z[kb]);
+        for (int dt = 0; dt < kDT; ++dt) {
+            const uint8_t* v = lds + slot * kBytes + dt * 32 * kTile * 2;
+            o[dt] = mma_f16(*reinterpret_cast<const uint4*>(v + v_at[2 * hf]), pend0, o[dt]);
+            o[dt] = mma_f16(*reinterpret_cast<const uint4*>(v + v_at[2 * hf + 1]), pend1, o[dt]);
         }
-        if (now) {
-            const uint8_t* vt = lds + (4 + (i & 3)) * kBytes;
+    };
+    int s = 0;                                     // the tile's power of two
+    // z, the scores of half hf of the tile at `at`, become weights, while the matrix cores work on
+    // the scores of half hf2 in place slot2 and the values of half hf1 in place slot1
+    auto step = [&](auto masked, int at, int hf, int slot2, int hf2, int slot1, int hf1) RUDDER_INLINE {
+        if constexpr (decltype(masked)::value) {
+            const int key0 = at + 32 * hf + 4 * half;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                for (int dt = 0; dt < kDT; ++dt)
-                    o[dt] = mma_f16(
-                        *reinterpret_cast<const uint4*>(vt + v_at[ks] + dt * 32 * kTile * 2),
-                        pk[ks], o[dt]);
+            for (int j = 0; j < 16; ++j)
+                z[j] = key0 + 8 * (j >> 2) + (j & 3) < limit ? z[j] : -INFINITY;
         }
-        if (wave < 4)
-            wait_barrier<63>();
-        else
-            wait_barrier<2 * kLoads>();
-        if (!more) break;
-        load_keys(i + 4);
-        load_values(i + 3);
-        now = ahead;
-        if (ahead) {
-            if (i + 1 > 0 && (i + 1 & 63) == 0) note = notes_from(i + 1);
-            const int word = __builtin_amdgcn_readlane(note, i + 1 & 63);
-            const int s = (word & 255) - 128, bad = word >> 8;
+        float best = z[0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) best = fmaxf(best, z[j]);
+        best *= c;
+        if (s < scale) {
+            // larger values than before.  The weights of the 32 keys before go first: their rows may
+            // see nothing of this tile, and in fp16 they would not survive the factor
+            weigh(slot1, hf1);
+            pend0 = pend1 = make_uint4(0, 0, 0, 0);
+            const float down = __builtin_amdgcn_ldexpf(1.0f, max(s - scale, -252));
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) o[dt] *= down;
+            scale = s;
+        }
+        if (__any(best > m + kLazy)) {
+            // to a whole number, so that the factor is a power of two: exact, for the weights of the
+            // 32 keys before as well
+            const float raised = ceilf(fmaxf(m, fmaxf(best, __shfl_xor(best, 32))));
+            const int less = raised == -INFINITY ? 0 : (int)fmaxf(m - raised, -252.0f);
+            m = raised;
+            const float alpha = __builtin_amdgcn_ldexpf(1.0f, less);
+            l *= alpha;
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) o[dt] *= alpha;
+            pend0 = times(pend0, alpha);
+            pend1 = times(pend1, alpha);
+        }
+        // weights for O are held times 2^(scale - s), their sum is brought back; where that is far,
+        // the sum takes exponentials of its own
+        const float base_m = m == -INFINITY ? 0.0f : m;
+        float back = __builtin_amdgcn_ldexpf(1.0f, s - scale);
+        if (s - scale > 64) {
+            back = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                l += __builtin_amdgcn_exp2f(fmaf(c, z[j], kPShift - base_m));
+        }
+        const float shift = kPShift + (float)(scale - s) - base_m;
+        const f32x16_acc zn = scores(slot2, hf2);
+        weigh(slot1, hf1);
+        float sum = 0.0f;
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = __builtin_amdgcn_exp2f(fmaf(c, z[2 * j], shift));
+            const float e = __builtin_amdgcn_exp2f(fmaf(c, z[2 * j + 1], shift));
+            sum += a + e;
+            w[j] = pack_f16(a, e);
+        }
+        interleave<2 * kDT + kKS>();
+        l = fmaf(sum, back, l);
+        pend0 = make_uint4(w[0], w[1], w[2], w[3]);
+        pend1 = make_uint4(w[4], w[5], w[6], w[7]);
+        z = zn;
+    };
+    // Tile i in place SLOT, known when compiled: LDS addresses are then a register and a constant.
+    // A wave that has seen its last key takes one more half, masked, for the values of the half
+    // before.
+    auto turn = [&](auto masked, int i, auto slot_constant) RUDDER_INLINE {
+        constexpr int SLOT = decltype(slot_constant)::value;
+        constexpr int kNext = (SLOT + 1) % RING, kBefore = (SLOT + RING - 1) % RING;
+        const int at = i * kTile;
+        if (!decltype(masked)::value || at < most + kTile) {
+            if (i > 0 && (i & 63) == 0) note = notes_from(i);
+            const int word = __builtin_amdgcn_readlane(note, i & 63);
+            s = (word & 255) - 128;
+            const int bad = word >> 8;
             if (bad < kTile) first_bad = min(first_bad, at + bad);
-            if (at + kTile > least) {
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (at + 32 * kb + 8 * (j >> 2) + 4 * half + (j & 3) >= limit)
-                            z[kb][j] = -INFINITY;
-            }
-            float best = z[0][0];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) best = fmaxf(best, z[kb][j]);
-            best *= c;
-            if (__any(best > m + kLazy) || s < scale) {
-                const float raised = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)));
-                float alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
-                m = raised;
-                l *= alpha;
-                if (s < scale) {
-                    alpha = __builtin_amdgcn_ldexpf(alpha, max(s - scale, -252));
-                    scale = s;
-                }
-#pragma unroll
-                for (int dt = 0; dt < kDT; ++dt)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
-            }
-            const float shift = kPShift - (m == -INFINITY ? 0.0f : m);
-            float sum = 0.0f;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    z[kb][j] = __builtin_amdgcn_exp2f(fmaf(c, z[kb][j], shift));
-                    sum += z[kb][j];
-                }
-            l += sum;
-            if (s > scale) {                       // small values beside large ones
-                const float down = __builtin_amdgcn_ldexpf(1.0f, scale - s);
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) z[kb][j] *= down;
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = pack_f16(z[ks >> 1][(ks & 1) * 8 + 2 * j],
-                                    z[ks >> 1][(ks & 1) * 8 + 2 * j + 1]);
-                pk[ks] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            step(masked, at, 0, SLOT, 1, kBefore, 1);
         }
-        if (wave < 4)
-            wait_barrier<4 * kLoads>();
-        else
-            wait_barrier<63>();
+        wait_barrier<(RING - 2) * 2 * kLoads>();
+        load_keys(i + RING, SLOT);
+        load_values(i + RING - 1, kBefore);
+        if (!decltype(masked)::value || at < most) step(masked, at, 1, kNext, 0, SLOT, 0);
+    };
+
+    wait_barrier<(RING - 1) * 2 * kLoads>();
+    z = scores(0, 0);
+    int i = 0;
+    for (; (i + RING) * kTile <= least; i += RING) {       // all of the wave's rows see these
+        turn(std::false_type(), i, std::integral_constant<int, 0>());
+        turn(std::false_type(), i + 1, std::integral_constant<int, 1>());
+        if constexpr (RING > 2) turn(std::false_type(), i + 2, std::integral_constant<int, 2>());
     }
-    if (wave < 4) wait_barrier<63>();              // group B's last phase of products
+    int slot = 0;                                  // behind the last tile
+    for (; i < tiles; i += RING) {
+        turn(std::true_type(), i, std::integral_constant<int, 0>());
+        slot = 1;
+        if (i + 1 == tiles) break;
+        turn(std::true_type(), i + 1, std::integral_constant<int, 1>());
+        slot = 2;
+        if constexpr (RING > 2) {
+            if (i + 2 == tiles) break;
+            turn(std::true_type(), i + 2, std::integral_constant<int, 2>());
+            slot = 3;
+        }
+    }
+    // the weights of the last 32 keys, or of 0 (slot 0: a wave whose rows all see every tile)
+    weigh(slot == 0 ? RING - 1 : slot - 1, 1);
     wait_barrier<0>();                             // no load is on its way to LDS any more
     l += __shfl_xor(l, 32);
     // every row sees itself: a sum of zero is one of scores of -inf alone
@@ -658,6 +741,8 @@ bool many_rows(int B, int T, int max_rows, int G, int Hkv, int D) {
     return (int64_t)(max_rows < T ? max_rows : T) * G > 256;
 }
 
+constexpr int kMostLdk = 1 << 24;                  // a tile's keys are reached with 32-bit offsets
+
 int slots_of(int B, int T) { return T / kTile + B; }
 
 }  // namespace
@@ -683,16 +768,21 @@ hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const u
     p.max_rows = max_rows < T ? max_rows : T;
     p.G = Hq / Hkv;
     p.Hkv = Hkv;
-    p.pairs = B * Hkv;
     p.ldq = ldq;
     p.ldk = ldk;
     p.ldv = ldv;
     p.ldo = ldo;
     p.sm = sm;
     p.O = O;
-    if (!many_rows(B, T, max_rows, p.G, Hkv, D)) {
-        p.tile_rows = (p.max_rows * p.G + 127) / 128;
-        const unsigned grid = (unsigned)((int64_t)p.pairs * p.tile_rows);
+    const bool many = many_rows(B, T, max_rows, p.G, Hkv, D) && ldk <= kMostLdk;
+    const int unit_rows = many ? 256 : 128, pairs = B * Hkv;
+    p.tile_rows = (p.max_rows * p.G + unit_rows - 1) / unit_rows;
+    p.dies = pairs % 8 == 0 ? 8 : 1;
+    p.die_pairs = pairs / p.dies;
+    const int64_t fit = (2 << 20) / ((int64_t)p.max_rows * (4 * D)), least = fit > 4 ? fit : 4;
+    p.group = (int)(least < p.die_pairs ? least : p.die_pairs);
+    const unsigned grid = (unsigned)((int64_t)pairs * p.tile_rows);
+    if (unit_rows == 128) {
         if (D == 64)
             prompt_tile_kernel<64><<<grid, 256, 0, stream>>>(p);
         else
@@ -703,14 +793,12 @@ hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const u
     p.images = static_cast<uint8_t*>(workspace);
     p.notes = reinterpret_cast<int32_t*>(p.images + (size_t)p.slots * Hkv * (kTile * D * 2));
     const dim3 tiles((p.max_rows + kTile - 1) / kTile, Hkv, B);
-    p.tile_rows = (p.max_rows * p.G + 255) / 256;
-    const unsigned grid = (unsigned)((int64_t)p.pairs * p.tile_rows);
     if (D == 64) {
         prompt_values_kernel<64><<<tiles, 256, 0, stream>>>(p);
-        prompt_wide_kernel<64><<<grid, 512, 0, stream>>>(p);
+        prompt_wide_kernel<64, 8, 3><<<grid, 512, 0, stream>>>(p);
     } else {
         prompt_values_kernel<128><<<tiles, 256, 0, stream>>>(p);
-        prompt_wide_kernel<128><<<grid, 512, 0, stream>>>(p);
+        prompt_wide_kernel<128, 8, 3><<<grid, 512, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
