@@ -59,7 +59,8 @@ def test_prompts(rudder, counts, Hq, Hkv, D):
 
 # prompts of enough tokens and heads for every kernel
 LONG = [([4192, 4192], 16, 16, 128), ([1500, 700, 1111], 24, 8, 64), ([5000, 20, 3000], 8, 2, 128),
-        ([9001], 4, 1, 64), ([6000], 32, 8, 128), ([300] * 24, 16, 4, 128)]
+        ([9001], 4, 1, 64), ([6000], 32, 8, 128), ([300] * 24, 16, 4, 128), ([8300], 16, 16, 128),
+        ([40] * 100, 4, 2, 64)]
 
 
 @pytest.mark.parametrize("counts,Hq,Hkv,D", LONG)
@@ -186,6 +187,39 @@ def test_rows_see_nothing_behind_them(rudder, rows, D, bad):
         assert torch.equal(got[:, :2], clean[:, :2]), at
         if math.isnan(bad):
             assert torch.isnan(got[at:rows, 2:]).all(), at
+
+
+def test_rows_of_a_long_prompt_see_nothing_behind_them(rudder):
+    """The same on the kernel of eight waves, and tiles of larger and smaller values among them."""
+    log("case long prompt behind")
+    n, H = 8300, 16
+    q, k, v = (x.cuda() for x in _inputs([n], H, H, 128, 38))
+    starts = _starts([n]).cuda()
+    run = lambda kk, vv: rudder.prompt_attention(q, kk, vv, starts, n, 0.1)  # noqa: E731
+    clean = run(k, v)
+    for at, bad in ((5000, float("nan")), (8299, float("inf")), (64, -float("inf"))):
+        vv = v.clone()
+        vv[at, 3, 9] = bad
+        got = run(k, vv)
+        assert torch.equal(got[:at], clean[:at]) and torch.isnan(got[at:, 3]).all()
+        got[at:, 3] = clean[at:, 3]
+        assert torch.equal(got, clean)
+        kk = k.clone()
+        kk[at, 3] = bad
+        assert torch.equal(run(kk, v)[:at], clean[:at])
+    for power in (30, -30):                        # 2^30 times as large, or all but these
+        e = torch.where((torch.arange(n, device="cuda") // 64) % 5 == 2, 2.0 ** power, 1.0)
+        vv = (v.float() * e[:, None, None]).to(torch.bfloat16)
+        got = run(k, vv)
+        for h in (0, 7):
+            s = q[:, h].double() @ k[:, h].double().t().contiguous() * 0.1
+            i = torch.arange(n, device="cuda")
+            s.masked_fill_(i[None, :] > i[:, None], -math.inf)
+            p = torch.softmax(s, -1)
+            want, size = p @ vv[:, h].double(), p @ vv[:, h].double().abs()
+            # weights' half step, four times over for the exponents' roundings, and bf16's
+            bound = 4 * aref.FP16 * size + aref.BF16 * want.abs()
+            assert ((got[:, h].double() - want).abs() <= bound + 2.0 ** -134).all(), (power, h)
 
 
 def test_queries_that_are_not_finite(rudder):

@@ -115,32 +115,44 @@ __device__ __forceinline__ uint4 times(uint4 x, float f) {
     return make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
 }
 
-// Largest finite magnitude bits of eight bf16 values, and those that are not finite made zero.
-__device__ __forceinline__ uint32_t finite_top(uint32_t (&w)[4], bool& bad) {
-    uint32_t top = 0;
+// Largest magnitude bits of eight bf16 values.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2_t top_of(const uint32_t (&w)[4]) {
+    union { uint32_t u; u16x2_t v; } a;
+    u16x2_t top = {0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
-        if (a >= 0x7F80u) {
-            bad = true;
-            w[j] &= 0xFFFF0000u;
-            a = 0;
-        }
-        if (b >= 0x7F80u) {
-            bad = true;
-            w[j] &= 0xFFFFu;
-            b = 0;
-        }
-        top = max(top, max(a, b));
+        a.u = w[j] & 0x7FFF7FFFu;
+        top = __builtin_elementwise_max(top, a.v);
     }
     return top;
 }
 
-// The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
-// that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
-__device__ __forceinline__ int scale_of(uint32_t top) {
-    const int e = (int)(top >> 7) - 127;
-    return top ? min((14 - e) & ~7, 120) : 120;
+// Which four keys (of 16 such) and eight channels of a tile's values a thread takes: a wave 64 bytes
+// of every row, so that its transposed writes go to whole lines and to different banks.
+__device__ __forceinline__ int value_keys(int tid) { return tid / 4 % 16; }
+__device__ __forceinline__ int value_channels(int tid) { return tid % 4 + tid / 64 * 4; }
+
+// Four rows of eight bf16 values: those that are not finite made zero; `bad` becomes the first such
+// row where it is below.  Returns the largest magnitude bits of the others.
+__device__ __forceinline__ uint32_t finite_top(uint32_t (&w)[4][4], int& bad) {
+    u16x2_t most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, top_of(w[i]));
+    uint32_t top = max((uint32_t)most[0], (uint32_t)most[1]);
+    if (!__any(top >= 0x7F80u)) return top;
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = w[i][j] & 0x7FFFu, b = w[i][j] >> 16 & 0x7FFFu;
+            const bool low = a >= 0x7F80u, high = b >= 0x7F80u;
+            if (low || high) bad = min(bad, i);
+            w[i][j] &= (low ? 0u : 0xFFFFu) | (high ? 0u : 0xFFFF0000u);
+            top = max(top, max(low ? 0u : a, high ? 0u : b));
+        }
+    return top;
 }
 
 // Chunks of 16 bytes of an LDS row are exchanged so that 16 lanes reading one chunk of 16 rows find
@@ -150,41 +162,110 @@ __device__ __forceinline__ int place(int row, int chunk) {
     return (row * CHUNKS + (chunk ^ (CHUNKS == 16 ? row & 15 : row >> 1 & 7))) * 16;
 }
 
-// 128 rows a workgroup, (token, query head of the group) pairs of one sequence and key head, so that
-// grouped heads read their keys once; four waves share the tiles through LDS.
+// A tile's image: values as the second product's operand, [channel][key].  Four keys (rows of x) x
+// eight channels, times f, to their places.
+__device__ __forceinline__ void store_values(uint8_t* image, const uint4 (&x)[4], float f, int quad,
+                                             int chunk) {
+    // keys 4 quad .. + 3 are the accumulators' order with bits 0 and 1 of quad exchanged
+    const int to = (quad & ~3) | (quad & 1) << 1 | (quad >> 1 & 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a[4], e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = j == 0 ? x[i].x : j == 1 ? x[i].y : j == 2 ? x[i].z : x[i].w;
+            a[i] = __uint_as_float(w << 16) * f;
+            e[i] = __uint_as_float(w & 0xFFFF0000u) * f;
+        }
+        const int ch = chunk * 8 + 2 * j;
+        *reinterpret_cast<uint2*>(image + place<8>(ch, to >> 1) + (to & 1) * 8) =
+            make_uint2(pack_f16(a[0], a[1]), pack_f16(a[2], a[3]));
+        *reinterpret_cast<uint2*>(image + place<8>(ch + 1, to >> 1) + (to & 1) * 8) =
+            make_uint2(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]));
+    }
+}
+
+// Orders a wave's LDS accesses of different lanes (the hardware keeps their order; this keeps the
+// compiler's).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
+// that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
+__device__ __forceinline__ int scale_of(uint32_t top) {
+    const int e = (int)(top >> 7) - 127;
+    return top ? min((14 - e) & ~7, 120) : 120;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: 32 of them a workgroup, a tile of keys a wave.
+// ---------------------------------------------------------------------------
+// Short prompts are a matter of latency: no launch goes in front, keys come from memory straight to
+// registers as the first product's operand, every wave turns the values of its own tiles to fp16 and
+// transposes them through its own part of LDS, and the four waves meet once, at the end.
 template <int D>
-__global__ void __launch_bounds__(256) prompt_tile_kernel(const Prompt p) {
-    constexpr int kRows = 4 * kWaveRows, kKS = D / 16, kDT = D / 32, kChunks = D / 8;
-    __shared__ __align__(16) uint8_t keys[kTile * D * 2], values[kTile * D * 2];
-    __shared__ uint32_t tops[4];
-    __shared__ int first_bad;
+__global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
+    constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;
+    constexpr int kWaves = 4, kStride = D + 4;     // of a row of partial outputs, in floats
+    __shared__ __align__(16) uint8_t lds[kWaves * (kBytes > kWaveRows * kStride * 4
+                                                       ? kBytes : kWaveRows * kStride * 4)];
+    __shared__ float2 stats[kWaves][kWaveRows];    // a row's maximum and sum, ...
+    __shared__ int scales[kWaves][kWaveRows];      // ... and the power of two of its outputs
+    __shared__ int first_bads[kWaves];
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Unit unit = place_unit(p);
-    const int b = unit.b, h = unit.h, first = unit.tile * kRows;
+    const int b = unit.b, h = unit.h, row0 = unit.tile * kWaveRows;
     const int r0 = min(max(p.row_start[b], 0), p.T);
     const int n = min(min(max(p.row_start[b + 1], r0), p.T) - r0, p.max_rows);
     const int rows = n * p.G;
-    if (first >= rows) return;
+    if (row0 >= rows) return;
 
-    const int row0 = first + wave * kWaveRows, row = row0 + (lane & 31);
+    const int row = row0 + (lane & 31);
     const bool live = row < rows;
     const int t = live ? row / p.G : 0, head = h * p.G + (live ? row % p.G : 0);
     const int limit = live ? t + 1 : 0;            // keys this lane's row sees
-    const int least = quotient(row0, p.G) + 1;     // every row of the wave sees these
-    const int most = row0 < rows ? quotient(min(rows, row0 + kWaveRows) - 1, p.G) + 1 : 0;
-    const int last = quotient(min(rows, first + kRows) - 1, p.G) + 1;
+    const int least = quotient(row0, p.G) + 1;     // every row sees these
+    const int most = quotient(min(rows, row0 + kWaveRows) - 1, p.G) + 1;
+    const int tiles = (most + kTile - 1) / kTile;
 
+    uint4 k[2][kKS], x[kIts][4];
+    // rows behind the prompt are its last one again: no row sees the keys, and the values are made
+    // zero below
+    auto load = [&](int tile) RUDDER_INLINE {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const size_t r = (size_t)min(r0 + tile * kTile + kb * 32 + (lane & 31), r0 + n - 1);
+            const uint16_t* from = p.K + r * p.ldk + (size_t)h * D + half * 8;
+#pragma unroll
+            for (int i = 0; i < kKS; ++i)
+                k[kb][i] = *reinterpret_cast<const uint4*>(from + i * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t r = (size_t)min(r0 + tile * kTile + value_keys(lane) * 4 + i, r0 + n - 1);
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+                x[it][i] = *reinterpret_cast<const uint4*>(
+                    p.V + r * p.ldv + (size_t)h * D + value_channels(lane + it * 64) * 8);
+        }
+    };
     uint4 q[kKS];
-    float l = 0.0f, c = fabsf(p.sm) * kLog2e;
     {
         const uint16_t* from = p.Q + (size_t)(r0 + t) * p.ldq + (size_t)head * D + half * 8;
+#pragma unroll
+        for (int i = 0; i < kKS; ++i) q[i] = *reinterpret_cast<const uint4*>(from + i * 16);
+    }
+    if (wave < tiles) load(wave);
+    float l = 0.0f, c = fabsf(p.sm) * kLog2e;
+    {
         const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kKS; ++i) {
-            q[i] = *reinterpret_cast<const uint4*>(from + i * 16);
             uint32_t w[4] = {q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip};
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
@@ -205,79 +286,51 @@ __global__ void __launch_bounds__(256) prompt_tile_kernel(const Prompt p) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -INFINITY;
-    int scale = 1 << 20;                           // O is held times 2^scale
-    if (tid == 0) first_bad = 1 << 30;
-
-    for (int at = 0; at < last; at += kTile) {
-        // keys as they are; values transposed, four keys x eight channels a thread.  Rows behind
-        // the prompt are seen by none of its rows, but they have to lie in the buffer.
-        __syncthreads();                           // the tile before has been read
-        constexpr int kVThreads = 16 * kChunks;
-        uint32_t v[4][4] = {};
-        uint32_t top = 0;
-        const int quad = tid / kChunks % 16, chunk = tid % kChunks;
-#pragma unroll
-        for (int i = 0; i < kTile * kChunks / 256; ++i) {
-            const int u = tid + i * 256, key = u / kChunks, ck = u % kChunks;
-            const size_t r = (size_t)min(r0 + at + key, r0 + n - 1);
-            *reinterpret_cast<uint4*>(keys + place<kChunks>(key, ck)) =
-                *reinterpret_cast<const uint4*>(p.K + r * p.ldk + (size_t)h * D + ck * 8);
-        }
-        if (tid < kVThreads) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = at + quad * 4 + i;
-                if (key >= n) continue;
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D + chunk * 8);
-                v[i][0] = x.x;
-                v[i][1] = x.y;
-                v[i][2] = x.z;
-                v[i][3] = x.w;
-                bool bad = false;
-                top = max(top, finite_top(v[i], bad));
-                if (bad) atomicMin(&first_bad, key);
-            }
-        }
-#pragma unroll
-        for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-        if (lane == 0) tops[wave] = top;
-        __syncthreads();
-        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-        const int s = __builtin_amdgcn_readfirstlane(scale_of(top));
-        if (tid < kVThreads) {
-            const float f = __uint_as_float((uint32_t)(127 + s) << 23);
-            // keys 4 quad .. + 3 are the accumulators' order with bits 0 and 1 of quad exchanged
-            const int to = (quad & ~3) | (quad & 1) << 1 | (quad >> 1 & 1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a[4], e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = __uint_as_float(v[i][j] << 16) * f;
-                    e[i] = __uint_as_float(v[i][j] & 0xFFFF0000u) * f;
-                }
-                const int ch = chunk * 8 + 2 * j;
-                *reinterpret_cast<uint2*>(values + place<8>(ch, to >> 1) + (to & 1) * 8) =
-                    make_uint2(pack_f16(a[0], a[1]), pack_f16(a[2], a[3]));
-                *reinterpret_cast<uint2*>(values + place<8>(ch + 1, to >> 1) + (to & 1) * 8) =
-                    make_uint2(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]));
-            }
-        }
-        __syncthreads();
-        if (at >= most) continue;                  // no row of this wave sees the tile
-
+    int scale = 1 << 20, first_bad = 1 << 30;      // O of the lane's row is held times 2^scale
+    uint8_t* values = lds + wave * kBytes;
+    for (int tile = wave; tile < tiles; tile += kWaves) {
+        const int at = tile * kTile;
         f32x16_acc z[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) z[kb][j] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kKS; ++i)
-                z[kb] = mma_bf16(*reinterpret_cast<const uint4*>(
-                                     keys + place<kChunks>(kb * 32 + (lane & 31), 2 * i + half)),
-                                 q[i], z[kb]);
+            for (int i = 0; i < kKS; ++i) z[kb] = mma_bf16(k[kb][i], q[i], z[kb]);
         }
+        // the values
+        uint32_t top = 0;
+        int bad = 4;
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t there = at + value_keys(lane) * 4 + i < n ? ~0u : 0u;
+                v[i][0] = x[it][i].x & there;
+                v[i][1] = x[it][i].y & there;
+                v[i][2] = x[it][i].z & there;
+                v[i][3] = x[it][i].w & there;
+            }
+            top = max(top, finite_top(v, bad));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[it][i] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        }
+        bad = bad < 4 ? value_keys(lane) * 4 + bad : kTile;
+#pragma unroll
+        for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+        if (__any(bad < kTile)) {
+#pragma unroll
+            for (int off = 32; off; off >>= 1) bad = min(bad, __shfl_xor(bad, off));
+            first_bad = min(first_bad, at + bad);
+        }
+        const int s = __builtin_amdgcn_readfirstlane(scale_of(top));
+        const float f = __uint_as_float((uint32_t)(127 + s) << 23);
+#pragma unroll
+        for (int it = 0; it < kIts; ++it)
+            store_values(values, x[it], f, value_keys(lane), value_channels(lane + it * 64));
+        if (tile + kWaves < tiles) load(tile + kWaves);
+        // the weights
         if (at + kTile > least) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -292,62 +345,103 @@ __global__ void __launch_bounds__(256) prompt_tile_kernel(const Prompt p) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) best = fmaxf(best, z[kb][j]);
         best *= c;
-        float alpha = 1.0f;
-        if (__any(best > m + kLazy)) {
-            const float raised = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)));
-            alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
-            m = raised;
+        const float raised = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)));
+        const bool smaller = s < scale && at < limit;
+        if (tile >= kWaves) {                      // O is more than nothing
+            float alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
             l *= alpha;
-        }
-        float down = 1.0f;                         // of this tile's weights, for the values
-        if (s < scale) {
-            alpha = __builtin_amdgcn_ldexpf(alpha, max(s - scale, -252));
-            scale = s;
-        } else {
-            down = __builtin_amdgcn_ldexpf(1.0f, scale - s);
-        }
-        if (__any(alpha != 1.0f))
+            if (smaller) alpha = __builtin_amdgcn_ldexpf(alpha, max(s - scale, -252));
 #pragma unroll
-            for (int i = 0; i < kDT; ++i)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
+            for (int i = 0; i < kDT; ++i) o[i] *= alpha;
+        }
+        m = raised;
+        scale = smaller ? s : scale;
+        const float down = __builtin_amdgcn_ldexpf(1.0f, at < limit ? scale - s : 0);
         const float shift = kPShift - (m == -INFINITY ? 0.0f : m);
+        uint4 w[4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            uint32_t w[4];
+            uint32_t y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at_z = (ks & 1) * 8 + 2 * j;
                 const float a = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z], shift));
                 const float e = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z + 1], shift));
                 l += a + e;
-                w[j] = pack_f16(a * down, e * down);
+                y[j] = pack_f16(a * down, e * down);
             }
+            w[ks] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        wave_sync();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int i = 0; i < kDT; ++i)
                 o[i] = mma_f16(*reinterpret_cast<const uint4*>(
                                    values + place<8>(i * 32 + (lane & 31), 2 * ks + half)),
-                               make_uint4(w[0], w[1], w[2], w[3]), o[i]);
-        }
+                               w[ks], o[i]);
+        wave_sync();
     }
+    // the waves' results side by side
     l += __shfl_xor(l, 32);
-    __syncthreads();
-    // every row sees itself: a sum of zero is one of scores of -inf alone
-    float f = l > 0.0f ? 1.0f / l : __uint_as_float(0x7FC00000u);
-    if (t >= first_bad) f = __uint_as_float(0x7FC00000u);          // sees a value that is not finite
-    if (!live) return;
-    uint16_t* to = p.O + (size_t)(r0 + t) * p.ldo + (size_t)head * D + half * 4;
+    __syncthreads();                               // the values have been read
+    if (half == 0) {
+        stats[wave][lane] = make_float2(m, l);
+        scales[wave][lane] = scale;
+    }
+    if (lane == 0) first_bads[wave] = first_bad;
+    float* part = reinterpret_cast<float*>(lds) + wave * kWaveRows * kStride;
 #pragma unroll
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float x[4];
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<float4*>(part + (lane & 31) * kStride + i * 32 + g * 8 + half * 4) =
+                make_float4(o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]);
+    __syncthreads();
+    // eight channels a thread
+    constexpr int kChunks = D / 8;
+    for (int i = tid; i < kWaveRows * kChunks; i += 256) {
+        const int r = i / kChunks, d = i % kChunks * 8, rr = row0 + r;
+        if (rr >= rows) continue;
+        const int tt = rr / p.G, hd = h * p.G + rr % p.G;
+        float best = -INFINITY, sum = 0.0f;
+        int low = 1 << 20, first = 1 << 30;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[j] = __builtin_amdgcn_ldexpf(o[i][4 * g + j] * f, -scale);
-            *reinterpret_cast<uint2*>(to + i * 32 + g * 8) =
-                make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        for (int w = 0; w < kWaves; ++w) {
+            best = fmaxf(best, stats[w][r].x);
+            if (stats[w][r].x > -INFINITY) low = min(low, scales[w][r]);
+            first = min(first, first_bads[w]);
         }
+        float y[8] = {};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float2 ml = stats[w][r];
+            // a maximum of -inf: the wave has seen no key of this row (or its sum is NaN)
+            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - best);
+            sum += ml.x == -INFINITY ? ml.y : ml.y * f;
+            const float g = __builtin_amdgcn_ldexpf(f, max(low - scales[w][r], -252));
+            const float4* from = reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(lds) + (w * kWaveRows + r) * kStride + d);
+            const float4 u = from[0], v = from[1];
+            if (ml.x == -INFINITY) continue;
+            y[0] = fmaf(u.x, g, y[0]);
+            y[1] = fmaf(u.y, g, y[1]);
+            y[2] = fmaf(u.z, g, y[2]);
+            y[3] = fmaf(u.w, g, y[3]);
+            y[4] = fmaf(v.x, g, y[4]);
+            y[5] = fmaf(v.y, g, y[5]);
+            y[6] = fmaf(v.z, g, y[6]);
+            y[7] = fmaf(v.w, g, y[7]);
+        }
+        // every row sees itself: a sum of zero is one of scores of -inf alone
+        float f = sum > 0.0f ? 1.0f / sum : __uint_as_float(0x7FC00000u);
+        if (tt >= first) f = __uint_as_float(0x7FC00000u);         // sees a value that is not finite
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __builtin_amdgcn_ldexpf(y[j] * f, -low);
+        *reinterpret_cast<uint4*>(p.O + (size_t)(r0 + tt) * p.ldo + (size_t)hd * D + d) =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                       pack_bf16(y[6], y[7]));
+    }
 }
 
 // A prompt's tiles are kept at slots of their own: floor((r0 + n) / 64) + 1 >= floor(r0 / 64) +
@@ -370,28 +464,23 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     if (at >= n) return;
     if (tid == 0) first_bad = kTile;
     __syncthreads();
-    const int quad = tid / kChunks % 16, chunk = tid % kChunks;
-    uint32_t v[4][4] = {};
-    uint32_t top = 0;
-    if (tid < kVThreads) {
+    const int quad = value_keys(tid), chunk = value_channels(tid);
+    uint32_t v[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = at + quad * 4 + i;
-            if (key >= n) continue;
-            const uint4 x = *reinterpret_cast<const uint4*>(
-                p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D + chunk * 8);
-            v[i][0] = x.x;
-            v[i][1] = x.y;
-            v[i][2] = x.z;
-            v[i][3] = x.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bool bad = false;
-            top = max(top, finite_top(v[i], bad));
-            if (bad) atomicMin(&first_bad, quad * 4 + i);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int key = at + quad * 4 + i;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (tid < kVThreads && key < n)
+            x = *reinterpret_cast<const uint4*>(p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D +
+                                                chunk * 8);
+        v[i][0] = x.x;
+        v[i][1] = x.y;
+        v[i][2] = x.z;
+        v[i][3] = x.w;
     }
+    int bad = 4;
+    uint32_t top = finite_top(v, bad);
+    if (bad < 4) atomicMin(&first_bad, quad * 4 + bad);
 #pragma unroll
     for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
     if (lane == 0) tops[wave] = top;
@@ -402,22 +491,11 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     if (tid == 0) p.notes[(size_t)h * p.slots + slot] = s + 128 + (first_bad << 8);
     if (tid >= kVThreads) return;
     const float f = __uint_as_float((uint32_t)(127 + s) << 23);
-    const int to = (quad & ~3) | (quad & 1) << 1 | (quad >> 1 & 1);
-    uint8_t* image = p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float a[4], e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = __uint_as_float(v[i][j] << 16) * f;
-            e[i] = __uint_as_float(v[i][j] & 0xFFFF0000u) * f;
-        }
-        const int ch = chunk * 8 + 2 * j;
-        *reinterpret_cast<uint2*>(image + place<8>(ch, to >> 1) + (to & 1) * 8) =
-            make_uint2(pack_f16(a[0], a[1]), pack_f16(a[2], a[3]));
-        *reinterpret_cast<uint2*>(image + place<8>(ch + 1, to >> 1) + (to & 1) * 8) =
-            make_uint2(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]));
-    }
+    const uint4 out[4] = {make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]),
+                          make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]),
+                          make_uint4(v[2][0], v[2][1], v[2][2], v[2][3]),
+                          make_uint4(v[3][0], v[3][1], v[3][2], v[3][3])};
+    store_values(p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2), out, f, quad, chunk);
 }
 
 // 16 bytes a lane from `from` (the same for all lanes) + `offset` straight to LDS, lane after lane
@@ -445,26 +523,13 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // ---------------------------------------------------------------------------
 // Many rows: waves of 32 rows that share the tiles in LDS.
 // ---------------------------------------------------------------------------
-// Order of a step's N products, their N LDS reads and the vector work beside them.
-template <int N>
-__device__ __forceinline__ void interleave() {
-    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);     // LDS reads
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // a product
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x400, 1, 0); // an exponential
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // vector instructions
-    }
-}
-
 // A software pipeline over halves of tiles: while the weights of 32 keys are formed on the vector
 // units, the matrix cores work on the scores of the next 32 and the values of the last 32.
 // Tiles come straight to LDS, into rings of RING for keys and values each.  The one barrier of
 // tile i stands between its halves: K of i and V of i - 1 have been read then, their places are
 // asked for K of i + RING and V of i + RING - 1; K of i + 1 and V of i have landed.
 template <int D, int WAVES, int RING>
-__global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt p) {
+__global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kernel(const Prompt p) {
     constexpr int kRows = WAVES * kWaveRows, kKS = D / 16, kDT = D / 32, kChunks = D / 8;
     constexpr int kBytes = kTile * D * 2, kLoads = kBytes / 1024 / WAVES;   // a tile's; a wave's of one
     constexpr int kStride = D * 2 + 16;                               // of an output row in LDS
@@ -563,7 +628,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -INFINITY;
-    int scale = 1 << 20;                           // O is held times 2^scale
+    int scale = 1 << 20;                           // the row's
     int first_bad = 1 << 30;
     int k_at[kKS], v_at[4];                        // where the lane's operands lie in a tile
 #pragma unroll
@@ -584,11 +649,12 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
     uint4 pend0 = make_uint4(0, 0, 0, 0), pend1 = pend0;       // weights of the 32 keys before
     auto weigh = [&](int slot, int hf) RUDDER_INLINE {
 #pragma unroll
-        for (int dt = 0; dt < kDT; ++dt) {
-            const uint8_t* v = lds + slot * kBytes + dt * 32 * kTile * 2;
-            o[dt] = mma_f16(*reinterpret_cast<const uint4*>(v + v_at[2 * hf]), pend0, o[dt]);
-            o[dt] = mma_f16(*reinterpret_cast<const uint4*>(v + v_at[2 * hf + 1]), pend1, o[dt]);
-        }
+        for (int x = 0; x < 2; ++x)                // product after product of another accumulator
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt)
+                o[dt] = mma_f16(*reinterpret_cast<const uint4*>(
+                                    lds + slot * kBytes + dt * 32 * kTile * 2 + v_at[2 * hf + x]),
+                                x ? pend1 : pend0, o[dt]);
     };
     int s = 0;                                     // the tile's power of two
     // z, the scores of half hf of the tile at `at`, become weights, while the matrix cores work on
@@ -604,15 +670,20 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
 #pragma unroll
         for (int j = 1; j < 16; ++j) best = fmaxf(best, z[j]);
         best *= c;
-        if (s < scale) {
-            // larger values than before.  The weights of the 32 keys before go first: their rows may
-            // see nothing of this tile, and in fp16 they would not survive the factor
+        // O of a row is held times 2^scale, the smallest power of the tiles that it has seen; where all
+        // rows see the tile it is one number
+        constexpr bool kMasked = decltype(masked)::value;
+        const int had = kMasked ? scale : __builtin_amdgcn_readfirstlane(scale);
+        const bool smaller = s < had && (!kMasked || at < limit);
+        if (kMasked ? __any(smaller) : smaller) {
+            // larger values than before.  The weights of the 32 keys before go first: in fp16 they
+            // would not survive the factor, and their row may see nothing of this tile
             weigh(slot1, hf1);
             pend0 = pend1 = make_uint4(0, 0, 0, 0);
-            const float down = __builtin_amdgcn_ldexpf(1.0f, max(s - scale, -252));
+            const float down = smaller ? __builtin_amdgcn_ldexpf(1.0f, max(s - had, -252)) : 1.0f;
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) o[dt] *= down;
-            scale = s;
+            scale = smaller ? s : had;
         }
         if (__any(best > m + kLazy)) {
             // to a whole number, so that the factor is a power of two: exact, for the weights of the
@@ -630,14 +701,17 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
         // weights for O are held times 2^(scale - s), their sum is brought back; where that is far,
         // the sum takes exponentials of its own
         const float base_m = m == -INFINITY ? 0.0f : m;
-        float back = __builtin_amdgcn_ldexpf(1.0f, s - scale);
-        if (s - scale > 64) {
-            back = 0.0f;
+        const int above = s - (kMasked ? scale : __builtin_amdgcn_readfirstlane(scale));
+        float back = __builtin_amdgcn_ldexpf(1.0f, above);
+        if (kMasked ? __any(above > 64) : above > 64) {
+            float apart = 0.0f;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                l += __builtin_amdgcn_exp2f(fmaf(c, z[j], kPShift - base_m));
+                apart += __builtin_amdgcn_exp2f(fmaf(c, z[j], kPShift - base_m));
+            l += above > 64 ? apart : 0.0f;
+            back = above > 64 ? 0.0f : back;
         }
-        const float shift = kPShift + (float)(scale - s) - base_m;
+        const float shift = kPShift - (float)above - base_m;
         const f32x16_acc zn = scores(slot2, hf2);
         weigh(slot1, hf1);
         float sum = 0.0f;
@@ -649,7 +723,6 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
             sum += a + e;
             w[j] = pack_f16(a, e);
         }
-        interleave<2 * kDT + kKS>();
         l = fmaf(sum, back, l);
         pend0 = make_uint4(w[0], w[1], w[2], w[3]);
         pend1 = make_uint4(w[4], w[5], w[6], w[7]);
@@ -717,8 +790,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
             *reinterpret_cast<uint2*>(slab + (lane & 31) * kStride + (dt * 32 + g * 8 + half * 4) * 2) =
                 make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
         }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     constexpr int kAtOnce = 64 / kChunks;
 #pragma unroll
     for (int i = 0; i < kWaveRows / kAtOnce; ++i) {
@@ -736,9 +808,33 @@ __global__ void __launch_bounds__(WAVES * 64, 2) prompt_wide_kernel(const Prompt
 
 namespace {
 
-// Whether a call takes the kernel for many rows.
-bool many_rows(int B, int T, int max_rows, int G, int Hkv, int D) {
-    return (int64_t)(max_rows < T ? max_rows : T) * G > 256;
+// Work units of the kernel for few rows.
+int64_t few_units(int B, int T, int max_rows, int G, int Hkv) {
+    const int64_t rows = (int64_t)(max_rows < T ? max_rows : T) * G;
+    return (rows + kWaveRows - 1) / kWaveRows * B * Hkv;
+}
+
+// The kernel for few rows where its workgroups, one a compute unit, make one round, or two and the
+// prompts are long: there a round beside the launch in front costs less.  us, few | many rows, 128
+// channels: 4 x 77 rows of 16 heads (192 units) 9.6 | 12.9, 2 x 256 (256) 11.7 | 17.8, 4 x 130 (320)
+// 17.1 | 15.7, 2 x 400 (416, 7 tiles) 22.8 | 21.3, 1 x 600 (304, 10 tiles) 19.8 | 23.6, 1 x 1000 (512)
+// 34.6 | 36.0, 2 x 600 (608) 36.6 | 26.0; 64 channels, 24 heads of eight key heads: 4 x 77 (256) 7.0 |
+// 11.3, 2 x 256 (384, 4 tiles) 12.5 | 13.5, 1 x 600 (456) 17.3 | 20.1, 2 x 400 (608) 20.3 | 16.4.
+bool few_rows(int64_t units, int max_rows, int D) {
+    const int tiles = (max_rows + kTile - 1) / kTile;
+    return units <= 256 || (units <= 512 && tiles >= (D == 64 ? 4 : 9));
+}
+
+// Waves of the kernel for many rows, eight or four.  Four make rounds of workgroups that end more
+// evenly, two of them a compute unit go through their barriers apart; eight read every tile half as
+// often.  us, eight | four; 128 channels: 2 x 1500 rows of 16 heads 53.9 | 45.6, 1 x 5000 of 8
+// (two key heads) 125.8 | 98.3, 2 x 6000 of 16 320 | 311, 1 x 12000 of 8 (376 units of 256 rows) 335
+// | 301, 1 x 8192 of 16 (512) 303 | 315, 1 x 16576 of 16 1055 | 1072, of 32 (eight key heads) 2032 |
+// 2078.  64 channels, whose registers leave room for a third: 3 x 1500 of 24 43.4 | 39.4, 1 x 16576
+// of 32 1255 | 1177.
+bool eight_waves(int pairs, int max_rows, int G, int D) {
+    const int64_t units = ((int64_t)max_rows * G + 255) / 256 * pairs;
+    return D == 128 && units >= 512 && max_rows >= 128 * kTile;
 }
 
 constexpr int kMostLdk = 1 << 24;                  // a tile's keys are reached with 32-bit offsets
@@ -748,11 +844,11 @@ int slots_of(int B, int T) { return T / kTile + B; }
 }  // namespace
 
 bool prompt_attention_workspace(int B, int T, int max_rows, int Hq, int Hkv, int D, size_t& bytes) {
-    const int64_t rows = (int64_t)(max_rows < T ? max_rows : T) * (Hq / Hkv);
-    bytes = 0;
-    if (many_rows(B, T, max_rows, Hq / Hkv, Hkv, D))
-        bytes = (size_t)slots_of(B, T) * Hkv * (kTile * D * 2 + 4);
-    return (rows + 127) / 128 * B * Hkv <= (1 << 21);
+    const int64_t units = few_units(B, T, max_rows, Hq / Hkv, Hkv);
+    // from more than one round of the few rows' kernel on, whichever is taken then: no smaller call
+    // needs more
+    bytes = units > 256 ? (size_t)slots_of(B, T) * Hkv * (kTile * D * 2 + 4) : 0;
+    return units <= (1 << 23);
 }
 
 hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const uint16_t* V,
@@ -774,19 +870,22 @@ hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const u
     p.ldo = ldo;
     p.sm = sm;
     p.O = O;
-    const bool many = many_rows(B, T, max_rows, p.G, Hkv, D) && ldk <= kMostLdk;
-    const int unit_rows = many ? 256 : 128, pairs = B * Hkv;
+    const bool many = !few_rows(few_units(B, T, max_rows, p.G, Hkv), p.max_rows, D) &&
+                      ldk <= kMostLdk;
+    const int pairs = B * Hkv;
+    const bool eight = many && eight_waves(pairs, p.max_rows, p.G, D);
+    const int unit_rows = kWaveRows * (eight ? 8 : many ? 4 : 1);
     p.tile_rows = (p.max_rows * p.G + unit_rows - 1) / unit_rows;
     p.dies = pairs % 8 == 0 ? 8 : 1;
     p.die_pairs = pairs / p.dies;
     const int64_t fit = (2 << 20) / ((int64_t)p.max_rows * (4 * D)), least = fit > 4 ? fit : 4;
     p.group = (int)(least < p.die_pairs ? least : p.die_pairs);
     const unsigned grid = (unsigned)((int64_t)pairs * p.tile_rows);
-    if (unit_rows == 128) {
+    if (!many) {
         if (D == 64)
-            prompt_tile_kernel<64><<<grid, 256, 0, stream>>>(p);
+            prompt_few_kernel<64><<<grid, 256, 0, stream>>>(p);
         else
-            prompt_tile_kernel<128><<<grid, 256, 0, stream>>>(p);
+            prompt_few_kernel<128><<<grid, 256, 0, stream>>>(p);
         return hipGetLastError();
     }
     p.slots = slots_of(B, T);
@@ -795,10 +894,13 @@ hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const u
     const dim3 tiles((p.max_rows + kTile - 1) / kTile, Hkv, B);
     if (D == 64) {
         prompt_values_kernel<64><<<tiles, 256, 0, stream>>>(p);
-        prompt_wide_kernel<64, 8, 3><<<grid, 512, 0, stream>>>(p);
+        prompt_wide_kernel<64, 4, 2><<<grid, 256, 0, stream>>>(p);
     } else {
         prompt_values_kernel<128><<<tiles, 256, 0, stream>>>(p);
-        prompt_wide_kernel<128, 8, 3><<<grid, 512, 0, stream>>>(p);
+        if (eight)
+            prompt_wide_kernel<128, 8, 3><<<grid, 512, 0, stream>>>(p);
+        else
+            prompt_wide_kernel<128, 4, 2><<<grid, 256, 0, stream>>>(p);
     }
     return hipGetLastError();
 }
