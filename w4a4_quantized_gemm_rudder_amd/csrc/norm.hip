@@ -41,6 +41,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Two bf16 values a word, added in 32 bits and rounded.
+__device__ __forceinline__ uint32_t add_bf16(uint32_t a, uint32_t b) {
+    return pack_bf16(low(a) + low(b), high(a) + high(b));
+}
+__device__ __forceinline__ void load8(const float* from, float (&to)[8]) {
+    const float4 u = reinterpret_cast<const float4*>(from)[0];
+    const float4 v = reinterpret_cast<const float4*>(from)[1];
+    to[0] = u.x;
+    to[1] = u.y;
+    to[2] = u.z;
+    to[3] = u.w;
+    to[4] = v.x;
+    to[5] = v.y;
+    to[6] = v.z;
+    to[7] = v.w;
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off);
@@ -52,75 +69,93 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return v;
 }
 
-// Channels of one piece of a row, a lane's share of a load and a store.
-constexpr int piece_of(int out) { return out == kRows16 ? 8 : out == kE2M3 ? 32 : 16; }
+// Bytes of the codes of eight channels, and of what is stored at once: the codes of 16 channels, of 32
+// in the E2M3 container.
+constexpr int code_bytes(int out) { return out == kInt8 ? 8 : out == kInt4 ? 4 : 6; }
+constexpr int slot_pieces(int out) { return out == kE2M3 ? 4 : 2; }
 
-// ROWS rows a workgroup, WAVES waves a row, N pieces a lane.
+// Rows a workgroup whose codes pass through LDS, and their distance there.
+__host__ __device__ constexpr bool staged(int out, int rows) {
+    return out != kRows16 && (rows > 1 || out == kE2M3);
+}
+__host__ __device__ constexpr int stage_stride(int out, int K) {
+    return K / 8 * code_bytes(out) + (out == kInt8 ? 16 : 8);
+}
+
+// ROWS rows a workgroup, WAVES waves a row, N pieces of eight channels a lane.
 template <int OUT, int WAVES, int ROWS, int N, bool ADD>
 __global__ void __launch_bounds__(64 * WAVES * ROWS) norm_kernel(const Norm a) {
-    constexpr int kPiece = piece_of(OUT), kWords = kPiece / 2, kLoads = kPiece / 8;
+    constexpr bool kEarly = N <= 2;                // gamma and inv_smooth on their way beside the row
+    extern __shared__ __align__(16) uint8_t stage[];
     __shared__ double sums[ROWS][WAVES];
     __shared__ uint32_t tops[ROWS][WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int in_group = wave / WAVES, part = wave % WAVES;
     const int row = blockIdx.x * ROWS + in_group;
     const bool live = row < a.M;
-    const int pieces = a.K / kPiece;
+    const int pieces = a.K / 8;
     auto piece = [&](int i) { return (i * WAVES + part) * 64 + lane; };
+    // pieces behind the row's last read that one again and are left out below
+    auto place = [&](int i) { return (size_t)min(piece(i), pieces - 1) * 8; };
 
-    uint32_t h[N][kWords] = {};
+    uint32_t h[N][4] = {};
+    float early[kEarly ? N : 1][2][8];
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            load8(a.gamma + place(i), early[i][0]);
+            if constexpr (OUT != kRows16) load8(a.inv_smooth + place(i), early[i][1]);
+        }
+    }
+    auto gammas = [&](int i, float (&g)[8]) {
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = early[i][0][j];
+        } else {
+            load8(a.gamma + piece(i) * 8, g);
+        }
+    };
+    auto smooths = [&](int i, float (&g)[8]) {
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = early[i][1][j];
+        } else {
+            load8(a.inv_smooth + piece(i) * 8, g);
+        }
+    };
     double sum = 0.0;
     if (live) {
         const uint16_t* x = a.X + (size_t)row * a.ldx;
-        // pieces behind the row's last read that one again and are left out below
+        uint4 v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint4* from =
-                reinterpret_cast<const uint4*>(x + (size_t)min(piece(i), pieces - 1) * kPiece);
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const uint4 v = from[j];
-                h[i][4 * j] = v.x;
-                h[i][4 * j + 1] = v.y;
-                h[i][4 * j + 2] = v.z;
-                h[i][4 * j + 3] = v.w;
-            }
-        }
+        for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const uint4*>(x + place(i));
         if constexpr (ADD) {
             const uint16_t* r = a.R + (size_t)row * a.ldr;
+            uint4 w[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4*>(r + place(i));
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const size_t at = (size_t)min(piece(i), pieces - 1) * kPiece;
-                const uint4* from = reinterpret_cast<const uint4*>(r + at);
-                uint32_t w[kWords];
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) {
-                    const uint4 v = from[j];
-                    w[4 * j] = v.x;
-                    w[4 * j + 1] = v.y;
-                    w[4 * j + 2] = v.z;
-                    w[4 * j + 3] = v.w;
-                }
-#pragma unroll
-                for (int j = 0; j < kWords; ++j)
-                    h[i][j] = pack_bf16(low(w[j]) + low(h[i][j]), high(w[j]) + high(h[i][j]));
-                if (piece(i) < pieces) {
-                    uint4* to = reinterpret_cast<uint4*>(a.H + (size_t)row * a.ldh + at);
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j)
-                        to[j] = make_uint4(h[i][4 * j], h[i][4 * j + 1], h[i][4 * j + 2],
-                                           h[i][4 * j + 3]);
-                }
+                v[i].x = add_bf16(w[i].x, v[i].x);
+                v[i].y = add_bf16(w[i].y, v[i].y);
+                v[i].z = add_bf16(w[i].z, v[i].z);
+                v[i].w = add_bf16(w[i].w, v[i].w);
+                if (piece(i) < pieces)
+                    *reinterpret_cast<uint4*>(a.H + (size_t)row * a.ldh + place(i)) = v[i];
             }
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            h[i][0] = v[i].x;
+            h[i][1] = v[i].y;
+            h[i][2] = v[i].z;
+            h[i][3] = v[i].w;
             double s = 0.0;
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                const double u = low(h[i][j]), v = high(h[i][j]);
-                s = __builtin_fma(u, u, s);
-                s = __builtin_fma(v, v, s);
+            for (int j = 0; j < 4; ++j) {
+                const double e = low(h[i][j]), f = high(h[i][j]);
+                s = __builtin_fma(e, e, s);
+                s = __builtin_fma(f, f, s);
             }
             sum += piece(i) < pieces ? s : 0.0;
         }
@@ -139,21 +174,21 @@ __global__ void __launch_bounds__(64 * WAVES * ROWS) norm_kernel(const Norm a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (!live || piece(i) >= pieces) continue;
-        const int k0 = piece(i) * kPiece;
+        float g[8];
+        gammas(i, g);
 #pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-            const float2 g = *reinterpret_cast<const float2*>(a.gamma + k0 + 2 * j);
-            h[i][j] = pack_bf16(low(h[i][j]) * r * g.x, high(h[i][j]) * r * g.y);
-        }
+        for (int j = 0; j < 4; ++j)
+            h[i][j] = pack_bf16(low(h[i][j]) * r * g[2 * j], high(h[i][j]) * r * g[2 * j + 1]);
         if constexpr (OUT == kRows16) {
-            *reinterpret_cast<uint4*>(a.Y + (size_t)row * a.ldy + k0) =
+            *reinterpret_cast<uint4*>(a.Y + (size_t)row * a.ldy + piece(i) * 8) =
                 make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]);
         } else if (!a.table) {
+            float s[8];
+            smooths(i, s);
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                const float2 s = *reinterpret_cast<const float2*>(a.inv_smooth + k0 + 2 * j);
-                top = max(top, __float_as_uint(low(h[i][j]) * s.x) & 0x7FFFFFFFu);
-                top = max(top, __float_as_uint(high(h[i][j]) * s.y) & 0x7FFFFFFFu);
+            for (int j = 0; j < 4; ++j) {
+                top = max(top, __float_as_uint(low(h[i][j]) * s[2 * j]) & 0x7FFFFFFFu);
+                top = max(top, __float_as_uint(high(h[i][j]) * s[2 * j + 1]) & 0x7FFFFFFFu);
             }
         }
     }
@@ -175,36 +210,90 @@ __global__ void __launch_bounds__(64 * WAVES * ROWS) norm_kernel(const Norm a) {
         }
         const float inv = step_reciprocal(step);
         if (live && part == 0 && lane == 0) a.row_scale[row] = step;
+        // codes as integer-valued floats; padding rows and pieces behind the last hold zeros
+        auto codes = [&](int i, float (&c)[8]) {
+            float s[8] = {};
+            if (live && piece(i) < pieces) smooths(i, s);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (piece(i) >= pieces) continue;
-            const int k0 = piece(i) * kPiece;
-            float c[kPiece];
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-                const float2 s = *reinterpret_cast<const float2*>(a.inv_smooth + k0 + 2 * j);
-                c[2 * j] = quantize_clamped_f(low(h[i][j]) * s.x * inv, kMost);
-                c[2 * j + 1] = quantize_clamped_f(high(h[i][j]) * s.y * inv, kMost);
-                if (!live) c[2 * j] = c[2 * j + 1] = 0.0f;      // padding rows
+            for (int j = 0; j < 4; ++j) {
+                c[2 * j] = quantize_clamped_f(low(h[i][j]) * s[2 * j] * inv, kMost);
+                c[2 * j + 1] = quantize_clamped_f(high(h[i][j]) * s[2 * j + 1] * inv, kMost);
             }
-            if constexpr (OUT == kE2M3) {
+        };
+        uint8_t* line = stage + in_group * stage_stride(OUT, a.K);
+        if constexpr (OUT == kE2M3) {
+            // the fields of 32 codes are a string of 192 bits: those of four pieces, 48 bits each,
+            // whose place in the row's string is six bytes a piece
+#pragma unroll
+            for (int i0 = 0; i0 < N; i0 += 4) {
+                float c[32] = {};
+#pragma unroll
+                for (int i = 0; i < 4 && i0 + i < N; ++i) {
+                    float part8[8];
+                    codes(i0 + i, part8);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) c[8 * i + j] = part8[j];
+                }
                 uint32_t d[6];
                 pack_e2m3x32(c, d);
-                uint8_t* block = a.Xq + e2m3_block_offset(row, k0, a.K);
-                const int slot = e2m3_slot(row, k0);
-                *reinterpret_cast<uint4*>(block + slot * 16) = make_uint4(d[0], d[1], d[2], d[3]);
-                *reinterpret_cast<uint2*>(block + 1024 + slot * 8) = make_uint2(d[4], d[5]);
-            } else {
-                int q[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) q[j] = (int)c[j];
-                if constexpr (OUT == kInt8)
-                    *reinterpret_cast<uint4*>(a.Xq + tiled_slot_offset<8>(row, k0, a.K)) =
-                        make_uint4(byte_word(q), byte_word(q + 4), byte_word(q + 8),
-                                   byte_word(q + 12));
-                else
-                    *reinterpret_cast<uint2*>(a.Xq + tiled_slot_offset<4>(row, k0, a.K)) =
-                        make_uint2(split_nibble_word(q), split_nibble_word(q + 8));
+                for (int i = 0; i < 4 && i0 + i < N; ++i) {
+                    if (piece(i0 + i) >= pieces) continue;
+                    uint16_t* to = reinterpret_cast<uint16_t*>(line + piece(i0 + i) * 6);
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        to[j] = (uint16_t)(d[(3 * i + j) / 2] >> ((3 * i + j) % 2 * 16));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (piece(i) >= pieces) continue;
+                float c[8];
+                codes(i, c);
+                int q[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[j] = (int)c[j];
+                const int k0 = piece(i) * 8;
+                if constexpr (OUT == kInt8) {
+                    const uint2 w = make_uint2(byte_word(q), byte_word(q + 4));
+                    if constexpr (staged(OUT, ROWS))
+                        *reinterpret_cast<uint2*>(line + k0) = w;
+                    else
+                        *reinterpret_cast<uint2*>(a.Xq + tiled_slot_offset<8>(row, k0, a.K) +
+                                                  (k0 & 8)) = w;
+                } else {
+                    const uint32_t w = split_nibble_word(q);
+                    if constexpr (staged(OUT, ROWS))
+                        *reinterpret_cast<uint32_t*>(line + k0 / 2) = w;
+                    else
+                        *reinterpret_cast<uint32_t*>(a.Xq + tiled_slot_offset<4>(row, k0, a.K) +
+                                                     (k0 & 8) / 2) = w;
+                }
+            }
+        }
+        if constexpr (staged(OUT, ROWS)) {
+            // slot by slot, a workgroup's rows beside each other: 16 ROWS bytes in a row (8 ROWS for
+            // four bits)
+            __syncthreads();
+            constexpr int kSlot = slot_pieces(OUT) * 8;
+            for (int u = threadIdx.x; u < a.K / kSlot * ROWS; u += 64 * WAVES * ROWS) {
+                const int in = u % ROWS, k0 = u / ROWS * kSlot, to = blockIdx.x * ROWS + in;
+                const uint8_t* from = stage + in * stage_stride(OUT, a.K);
+                if constexpr (OUT == kInt8) {
+                    *reinterpret_cast<uint4*>(a.Xq + tiled_slot_offset<8>(to, k0, a.K)) =
+                        *reinterpret_cast<const uint4*>(from + k0);
+                } else if constexpr (OUT == kInt4) {
+                    *reinterpret_cast<uint2*>(a.Xq + tiled_slot_offset<4>(to, k0, a.K)) =
+                        *reinterpret_cast<const uint2*>(from + k0 / 2);
+                } else {
+                    const uint2* w = reinterpret_cast<const uint2*>(from + k0 / 4 * 3);
+                    const uint2 x = w[0], y = w[1], z = w[2];
+                    uint8_t* block = a.Xq + e2m3_block_offset(to, k0, a.K);
+                    const int slot = e2m3_slot(to, k0);
+                    *reinterpret_cast<uint4*>(block + slot * 16) = make_uint4(x.x, x.y, y.x, y.y);
+                    *reinterpret_cast<uint2*>(block + 1024 + slot * 8) = z;
+                }
             }
         }
     }
@@ -215,27 +304,40 @@ hipError_t start(const Norm& a, hipStream_t stream) {
     // codes: padding rows up to a multiple of 32 as well
     const int64_t rows = OUT == kRows16 ? a.M : ((int64_t)a.M + 31) / 32 * 32;
     const unsigned grid = (unsigned)((rows + ROWS - 1) / ROWS);
+    const size_t lds = staged(OUT, ROWS) ? (size_t)ROWS * stage_stride(OUT, a.K) : 0;
     if (a.R)
-        norm_kernel<OUT, WAVES, ROWS, N, true><<<grid, 64 * WAVES * ROWS, 0, stream>>>(a);
+        norm_kernel<OUT, WAVES, ROWS, N, true><<<grid, 64 * WAVES * ROWS, lds, stream>>>(a);
     else
-        norm_kernel<OUT, WAVES, ROWS, N, false><<<grid, 64 * WAVES * ROWS, 0, stream>>>(a);
+        norm_kernel<OUT, WAVES, ROWS, N, false><<<grid, 64 * WAVES * ROWS, lds, stream>>>(a);
     return hipGetLastError();
 }
 
+// Few rows take eight waves each, their gamma and smoothing factors on the way beside them; many rows a
+// wave each, four a workgroup: codes then leave in pieces of 64 bytes, and two to four workgroups share
+// a compute unit.  us, eight waves a row | one, residual added, 8-bit codes with a step size a row: 512
+// rows of 2048 channels 5.4 | 6.1, 1024 7.4 | 6.6; 1024 of 4096 9.7 | 10.6 (bf16 rows 6.6 | 7.8, 1536
+// E2M3 13.6 | 13.5); 1536 of 8192 21.4 | 27.4; 16576 of 4096, E2M3 137 | 103.  Eight rows a workgroup
+// 107, 16576 of 4096 8-bit 114 against 106; two rows 110.
 template <int OUT>
 hipError_t launch(const Norm& a, hipStream_t stream) {
-    constexpr int kPiece = piece_of(OUT);
-    if (a.K > 8192) return start<OUT, 8, 1, 128 / kPiece>(a, stream);
-    if (a.M <= 512) return start<OUT, 8, 1, 32 / kPiece>(a, stream);
-    if (a.K <= 2048) return start<OUT, 1, 8, 32 / kPiece>(a, stream);
-    if (a.K <= 4096) return start<OUT, 1, 8, 64 / kPiece>(a, stream);
-    return start<OUT, 1, 8, 128 / kPiece>(a, stream);
+    if (a.K > 8192) return start<OUT, 8, 1, 16>(a, stream);
+    if (a.M <= (a.K <= 2048 ? 512 : a.K <= 4096 ? 1024 : 1536))
+        return a.K <= 4096 ? start<OUT, 8, 1, 1>(a, stream) : start<OUT, 8, 1, 2>(a, stream);
+    if (a.K <= 2048) return start<OUT, 1, 4, 4>(a, stream);
+    if (a.K <= 4096) return start<OUT, 1, 4, 8>(a, stream);
+    return start<OUT, 1, 4, 16>(a, stream);
 }
 
 // ---------------------------------------------------------------------------
-// Values of packed codes: eight lanes take 32 channels of a row, a wave eight
-// rows at once, so that its stores are whole lines; 32 rows x 32 channels a wave.
+// Values of packed codes: four lanes take 32 channels of a row, a wave 16 rows at once, so that its
+// stores are whole lines; 32 rows x 32 channels a wave.
 // ---------------------------------------------------------------------------
+// The value of a 6-bit E2M3 field: its exponent and mantissa at the places of a 32-bit number's, whose
+// bias is 126 more; numbers below the first binade are subnormal in both.
+__device__ __forceinline__ float e2m3_value(uint32_t field) {
+    return __uint_as_float((field & 31u) << 20 | (field & 32u) << 26) * 0x1p126f;
+}
+
 template <int BITS, int CODES>
 __global__ void __launch_bounds__(256)
 dequant_act_kernel(const uint8_t* __restrict__ Xq, const float* __restrict__ row_scale, int M,
@@ -244,56 +346,52 @@ dequant_act_kernel(const uint8_t* __restrict__ Xq, const float* __restrict__ row
     const int columns = K >> 5;
     const int64_t at = (int64_t)blockIdx.x * 4 + wave;
     if (at >= (int64_t)((M + 31) >> 5) * columns) return;
-    const int rb = (int)(at / columns), k = (int)(at - (int64_t)rb * columns) * 32 + lane % 8 * 4;
+    const int rb = (int)(at / columns), k = (int)(at - (int64_t)rb * columns) * 32 + lane % 4 * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = rb * 32 + i * 8 + lane / 8;
+    for (int i = 0; i < 2; ++i) {
+        const int row = rb * 32 + i * 16 + lane / 4;
         if (row >= M) continue;
-        float c[4];
+        float c[8];
         if constexpr (CODES == RUDDER_CODES_E2M3) {
-            // four fields of six bits are the bytes 3 t .. 3 t + 2 of the slot's string, of which
-            // 16 lie in plane 0
-            const int slot = e2m3_slot(row, k), t = (k & 31) / 4;
+            // eight fields of six bits are six bytes of the slot's string, of which 16 lie in plane 0
             constexpr int kPlanes = BITS == 8 ? 2 : 1;
+            const int slot = e2m3_slot(row, k), first = lane % 4 * 6;
             const uint8_t* block = Xq + kPlanes * e2m3_block_offset(row, k, K);
-            float digit[kPlanes][4];
+            uint32_t w[kPlanes][3];
 #pragma unroll
-            for (int p = 0; p < kPlanes; ++p) {
-                uint32_t w = 0;
+            for (int p = 0; p < kPlanes; ++p)
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
-                    const int b = 3 * t + j;
-                    w |= (uint32_t)block[p * 1536 + (b < 16 ? slot * 16 + b
-                                                           : 1024 + slot * 8 + b - 16)]
-                         << (8 * j);
+                    const int b = first + 2 * j;
+                    w[p][j] = *reinterpret_cast<const uint16_t*>(
+                        block + p * 1536 + (b < 16 ? slot * 16 + b : 1024 - 16 + slot * 8 + b));
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // eighths: m below the first binade, (8 + m) 2^(e - 1) from there on
-                    const int f = w >> (6 * j), e = f >> 3 & 3, m = f & 7;
-                    const int eighths = e ? (8 + m) << (e - 1) : m;
-                    digit[p][j] = 0.125f * (float)(f & 32 ? -eighths : eighths);
+            for (int j = 0; j < 8; ++j) {
+                float digit[kPlanes];
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) {
+                    const uint64_t all = w[p][0] | w[p][1] << 16 | (uint64_t)w[p][2] << 32;
+                    digit[p] = e2m3_value((uint32_t)(all >> (6 * j)));
                 }
+                c[j] = BITS == 8 ? 32.0f * digit[0] + 2.0f * digit[kPlanes - 1] : digit[0];
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = BITS == 8 ? 32.0f * digit[0][j] + 2.0f * digit[kPlanes - 1][j]
-                                 : digit[0][j];
         } else if constexpr (BITS == 8) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                Xq + tiled_slot_offset<8>(row, k, K) + (k & 15));
+            const uint2 w = *reinterpret_cast<const uint2*>(Xq + tiled_slot_offset<8>(row, k, K) +
+                                                            (k & 8));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = (float)(int8_t)(w >> (8 * j));
+            for (int j = 0; j < 8; ++j) c[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (j % 4 * 8));
         } else {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(
                 Xq + tiled_slot_offset<4>(row, k, K) + (k & 8) / 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = (float)((int)(w << (28 - 8 * j - (k & 4))) >> 28);
+            for (int j = 0; j < 8; ++j)
+                c[j] = (float)((int)(w << (28 - j % 4 * 8 - j / 4 * 4)) >> 28);
         }
         const float s = row_scale[row];
-        *reinterpret_cast<float4*>(out + (size_t)row * K + k) =
-            make_float4(c[0] * s, c[1] * s, c[2] * s, c[3] * s);
+        float4* to = reinterpret_cast<float4*>(out + (size_t)row * K + k);
+        to[0] = make_float4(c[0] * s, c[1] * s, c[2] * s, c[3] * s);
+        to[1] = make_float4(c[4] * s, c[5] * s, c[6] * s, c[7] * s);
     }
 }
 
