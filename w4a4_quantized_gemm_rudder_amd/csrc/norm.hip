@@ -58,6 +58,14 @@ __device__ __forceinline__ void load8(const float* from, float (&to)[8]) {
     to[7] = v.w;
 }
 
+// A store past the caches, for what is not read again soon: the residual stream, which the next norm
+// wants, several linears later (16576 x 4096 rows, with their values read back, 150 us, through the
+// caches 152), and values (152, 190).  Rows and codes go to the next call and stay.
+__device__ __forceinline__ void stream16(void* to, uint4 x) {
+    typedef unsigned v4u __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(v4u{x.x, x.y, x.z, x.w}, static_cast<v4u*>(to));
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off);
@@ -140,8 +148,7 @@ __global__ void __launch_bounds__(64 * WAVES * ROWS) norm_kernel(const Norm a) {
                 v[i].y = add_bf16(w[i].y, v[i].y);
                 v[i].z = add_bf16(w[i].z, v[i].z);
                 v[i].w = add_bf16(w[i].w, v[i].w);
-                if (piece(i) < pieces)
-                    *reinterpret_cast<uint4*>(a.H + (size_t)row * a.ldh + place(i)) = v[i];
+                if (piece(i) < pieces) stream16(a.H + (size_t)row * a.ldh + place(i), v[i]);
             }
         }
 #pragma unroll
@@ -329,7 +336,7 @@ hipError_t launch(const Norm& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Values of packed codes: four lanes take 32 channels of a row, a wave 16 rows at once, so that its
+// Values of packed codes: eight lanes take 32 channels of a row, a wave eight rows at once, so that its
 // stores are whole lines; 32 rows x 32 channels a wave.
 // ---------------------------------------------------------------------------
 // The value of a 6-bit E2M3 field: its exponent and mantissa at the places of a 32-bit number's, whose
@@ -346,52 +353,52 @@ dequant_act_kernel(const uint8_t* __restrict__ Xq, const float* __restrict__ row
     const int columns = K >> 5;
     const int64_t at = (int64_t)blockIdx.x * 4 + wave;
     if (at >= (int64_t)((M + 31) >> 5) * columns) return;
-    const int rb = (int)(at / columns), k = (int)(at - (int64_t)rb * columns) * 32 + lane % 4 * 8;
+    const int rb = (int)(at / columns), k = (int)(at - (int64_t)rb * columns) * 32 + lane % 8 * 4;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = rb * 32 + i * 16 + lane / 4;
+    for (int i = 0; i < 4; ++i) {
+        const int row = rb * 32 + i * 8 + lane / 8;
         if (row >= M) continue;
-        float c[8];
+        float c[4];
         if constexpr (CODES == RUDDER_CODES_E2M3) {
-            // eight fields of six bits are six bytes of the slot's string, of which 16 lie in plane 0
+            // four fields of six bits are the bytes 3 t .. 3 t + 2 of the slot's string, of which
+            // 16 lie in plane 0
+            const int slot = e2m3_slot(row, k), t = (k & 31) / 4;
             constexpr int kPlanes = BITS == 8 ? 2 : 1;
-            const int slot = e2m3_slot(row, k), first = lane % 4 * 6;
             const uint8_t* block = Xq + kPlanes * e2m3_block_offset(row, k, K);
-            uint32_t w[kPlanes][3];
+            float digit[kPlanes][4];
 #pragma unroll
-            for (int p = 0; p < kPlanes; ++p)
+            for (int p = 0; p < kPlanes; ++p) {
+                uint32_t w = 0;
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
-                    const int b = first + 2 * j;
-                    w[p][j] = *reinterpret_cast<const uint16_t*>(
-                        block + p * 1536 + (b < 16 ? slot * 16 + b : 1024 - 16 + slot * 8 + b));
+                    const int b = 3 * t + j;
+                    w |= (uint32_t)block[p * 1536 + (b < 16 ? slot * 16 + b
+                                                           : 1024 + slot * 8 + b - 16)]
+                         << (8 * j);
                 }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float digit[kPlanes];
-#pragma unroll
-                for (int p = 0; p < kPlanes; ++p) {
-                    const uint64_t all = w[p][0] | w[p][1] << 16 | (uint64_t)w[p][2] << 32;
-                    digit[p] = e2m3_value((uint32_t)(all >> (6 * j)));
-                }
-                c[j] = BITS == 8 ? 32.0f * digit[0] + 2.0f * digit[kPlanes - 1] : digit[0];
+                for (int j = 0; j < 4; ++j) digit[p][j] = e2m3_value(w >> (6 * j));
             }
-        } else if constexpr (BITS == 8) {
-            const uint2 w = *reinterpret_cast<const uint2*>(Xq + tiled_slot_offset<8>(row, k, K) +
-                                                            (k & 8));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (j % 4 * 8));
+            for (int j = 0; j < 4; ++j)
+                c[j] = BITS == 8 ? 32.0f * digit[0][j] + 2.0f * digit[kPlanes - 1][j]
+                                 : digit[0][j];
+        } else if constexpr (BITS == 8) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                Xq + tiled_slot_offset<8>(row, k, K) + (k & 15));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = (float)(int8_t)(w >> (8 * j));
         } else {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(
                 Xq + tiled_slot_offset<4>(row, k, K) + (k & 8) / 2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                c[j] = (float)((int)(w << (28 - j % 4 * 8 - j / 4 * 4)) >> 28);
+            for (int j = 0; j < 4; ++j)
+                c[j] = (float)((int)(w << (28 - 8 * j - (k & 4))) >> 28);
         }
         const float s = row_scale[row];
-        float4* to = reinterpret_cast<float4*>(out + (size_t)row * K + k);
-        to[0] = make_float4(c[0] * s, c[1] * s, c[2] * s, c[3] * s);
-        to[1] = make_float4(c[4] * s, c[5] * s, c[6] * s, c[7] * s);
+        stream16(out + (size_t)row * K + k,
+                 make_uint4(__float_as_uint(c[0] * s), __float_as_uint(c[1] * s),
+                            __float_as_uint(c[2] * s), __float_as_uint(c[3] * s)));
     }
 }
 
