@@ -262,17 +262,23 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
     if (wave < tiles) load(wave);
     float l = 0.0f, c = fabsf(p.sm) * kLog2e;
     {
-        const uint32_t flip = p.sm < 0.0f ? 0x80008000u : 0u;
-        uint32_t top = 0;
+        u16x2_t most = {0, 0};
 #pragma unroll
         for (int i = 0; i < kKS; ++i) {
-            uint32_t w[4] = {q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
-            q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            most = __builtin_elementwise_max(most, top_of(w));
         }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (top >= 0x7F80u) l = __uint_as_float(0x7FC00000u);      // not finite
+        const uint32_t top = max((uint32_t)most[0], (uint32_t)most[1]);
+        if (__any(top >= 0x7F80u)) {               // not finite
+            if (max(top, (uint32_t)__shfl_xor((int)top, 32)) >= 0x7F80u)
+                l = __uint_as_float(0x7FC00000u);
+        }
+        if (p.sm < 0.0f) {
+#pragma unroll
+            for (int i = 0; i < kKS; ++i)
+                q[i] = make_uint4(q[i].x ^ 0x80008000u, q[i].y ^ 0x80008000u, q[i].z ^ 0x80008000u,
+                                  q[i].w ^ 0x80008000u);
+        }
         if (c == 0.0f) {                           // all keys alike, however large the scores
 #pragma unroll
             for (int i = 0; i < kKS; ++i) q[i] = make_uint4(0, 0, 0, 0);
@@ -306,11 +312,18 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
             uint32_t v[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t there = at + value_keys(lane) * 4 + i < n ? ~0u : 0u;
-                v[i][0] = x[it][i].x & there;
-                v[i][1] = x[it][i].y & there;
-                v[i][2] = x[it][i].z & there;
-                v[i][3] = x[it][i].w & there;
+                v[i][0] = x[it][i].x;
+                v[i][1] = x[it][i].y;
+                v[i][2] = x[it][i].z;
+                v[i][3] = x[it][i].w;
+            }
+            if (at + kTile > n) {                  // the prompt ends in this tile
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t there = at + value_keys(lane) * 4 + i < n ? ~0u : 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] &= there;
+                }
             }
             top = max(top, finite_top(v, bad));
 #pragma unroll
@@ -356,7 +369,8 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
         }
         m = raised;
         scale = smaller ? s : scale;
-        const float down = __builtin_amdgcn_ldexpf(1.0f, at < limit ? scale - s : 0);
+        // weights for smaller values than before; in the wave's first tile there are none
+        const int less = tile >= kWaves && at < limit ? scale - s : 0;
         const float shift = kPShift - (m == -INFINITY ? 0.0f : m);
         uint4 w[4];
 #pragma unroll
@@ -368,9 +382,14 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
                 const float a = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z], shift));
                 const float e = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z + 1], shift));
                 l += a + e;
-                y[j] = pack_f16(a * down, e * down);
+                y[j] = pack_f16(a, e);
             }
             w[ks] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        if (__any(less)) {
+            const float down = __builtin_amdgcn_ldexpf(1.0f, less);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) w[ks] = times(w[ks], down);
         }
         wave_sync();
 #pragma unroll
@@ -415,6 +434,7 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
         float y[8] = {};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
+            if (w >= tiles && w > 0) break;        // the wave had no tile
             const float2 ml = stats[w][r];
             // a maximum of -inf: the wave has seen no key of this row (or its sum is NaN)
             const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - best);
