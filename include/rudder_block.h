@@ -180,11 +180,15 @@ size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int H
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   K, V     bf16 bits [T][Hkv][D], row distances ldk, ldv
- *   sm       the softmax scale, e.g. 1 / sqrt(D)
+ *   sm       the softmax scale, e.g. 1 / sqrt(D); sm * q . k stays below 2^126 in
+ *            magnitude
  *   workspace, workspace_bytes  at least
  *            rudder_prompt_attention_workspace_bytes(...) bytes (NULL if 0)
  *   B, T, max_rows >= 0 (0 is a no-op), Hq a multiple of Hkv, D 64 or 128
- * At most two launches.  Results do not depend on anything but the arguments.
+ * At most two launches.  Results do not depend on anything but the arguments
+ * (max_rows, which chooses the kernel, among them).  Sequences that overlap (a
+ * row_start that does not ascend) have undefined outputs; no access leaves the
+ * buffers.
  * Errors: INVALID_ARG for a null required pointer, negative sizes, Hq or Hkv
  * <= 0, Hq % Hkv != 0, a row distance below its heads' channels or not a
  * multiple of 8, sm not finite or beyond 2^127 in magnitude, a workspace that

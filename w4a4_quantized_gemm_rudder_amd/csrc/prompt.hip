@@ -204,7 +204,11 @@ __device__ __forceinline__ int scale_of(uint32_t top) {
 // ---------------------------------------------------------------------------
 // Short prompts are a matter of latency: no launch goes in front, keys come from memory straight to
 // registers as the first product's operand, every wave turns the values of its own tiles to fp16 and
-// transposes them through its own part of LDS, and the four waves meet once, at the end.
+// transposes them through its own part of LDS, and the four waves meet once, at the end.  One workgroup
+// a compute unit: a wave's keys and values on their way take half of its registers.  16 heads of 128
+// channels, one token 7.5 us, 77 8.9, 200 10.6; with 128 rows a workgroup and a tile after the other
+// 7.1, 10.7 and 15.4.  What is left is the way from lengths to rows (two trips to memory) and about 1300
+// instructions a wave, one wave a vector unit.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
     constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;
@@ -470,7 +474,10 @@ __device__ __forceinline__ int first_slot(int r0, int b) { return r0 / kTile + b
 
 // ---------------------------------------------------------------------------
 // Values for the kernel of many rows: transposed, in fp16, times a tile's power of two, laid out as
-// that kernel keeps them in LDS.  One tile and head a workgroup.
+// that kernel keeps them in LDS.  One tile and head a workgroup.  Bound by memory: 8384 tokens of 16
+// heads of 128 channels 14 us, 68 MB read and written at 4.9 TB/s.  Converting in the kernel itself would
+// repeat it for every 128 rows; weights in bf16, which need no conversion, put as much error into the
+// outputs as their own rounding does.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
@@ -548,6 +555,16 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // Tiles come straight to LDS, into rings of RING for keys and values each.  The one barrier of
 // tile i stands between its halves: K of i and V of i - 1 have been read then, their places are
 // asked for K of i + RING and V of i + RING - 1; K of i + 1 and V of i have landed.
+// 32 rows meet 32 keys in D / 8 products of 32 cycles; beside them stand, a lane, 16 exponentials and
+// about 60 vector instructions.  16576 tokens of 32 heads (eight key heads) of 128 channels 2035 to
+// 2080 us with the launch in front, 1085 to 1107 TFLOP/s, where a library product of 8192^3 reaches 1208
+// to 1379 card by card: matrix cores busy 54% of the time, vector units 47%, LDS 27%, no bank
+// conflicts; the card lowers its clock to 1.96 GHz for it (on zeros 1637 us).  2 x 4192 of 16 heads 170
+// to 178 (matrix cores 46%), twelve prompts up to 4801 of 32 heads 740 (50%), 3 x 1500 of 24 heads of 64
+// channels 34 (18%, vector units 36%: the longest unit's 24 tiles one after the other).  Two phases
+// apart with a barrier each, as in the cache's kernel for very many rows, 2304 us; 64 rows a wave, whose
+// operands from LDS serve two products, 2360 (one wave a vector unit hides nothing); hints to the
+// scheduler 2128 against 2097; a wave's priority raised for its products the same.
 template <int D, int WAVES, int RING>
 __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kernel(const Prompt p) {
     constexpr int kRows = WAVES * kWaveRows, kKS = D / 16, kDT = D / 32, kChunks = D / 8;
