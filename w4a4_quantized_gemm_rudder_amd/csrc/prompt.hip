@@ -117,7 +117,8 @@ __device__ __forceinline__ uint4 times(uint4 x, float f) {
 
 // Largest magnitude bits of eight bf16 values.
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ u16x2_t top_of(const uint32_t (&w)[4]) {
+__device__ __forceinline__ u16x2_t top_of(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     union { uint32_t u; u16x2_t v; } a;
     u16x2_t top = {0, 0};
 #pragma unroll
@@ -133,24 +134,32 @@ __device__ __forceinline__ u16x2_t top_of(const uint32_t (&w)[4]) {
 __device__ __forceinline__ int value_keys(int tid) { return tid / 4 % 16; }
 __device__ __forceinline__ int value_channels(int tid) { return tid % 4 + tid / 64 * 4; }
 
-// Four rows of eight bf16 values: those that are not finite made zero; `bad` becomes the first such
-// row where it is below.  Returns the largest magnitude bits of the others.
-__device__ __forceinline__ uint32_t finite_top(uint32_t (&w)[4][4], int& bad) {
+// N times four rows of eight bf16 values: those that are not finite made zero; `bad` becomes the first
+// such row (of four) where it is below.  Returns the largest magnitude bits of the others.
+template <int N>
+__device__ __forceinline__ uint32_t finite_top(uint4 (&x)[N][4], int& bad) {
     u16x2_t most = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, top_of(w[i]));
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, top_of(x[n][i]));
     uint32_t top = max((uint32_t)most[0], (uint32_t)most[1]);
     if (!__any(top >= 0x7F80u)) return top;
     top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t a = w[i][j] & 0x7FFFu, b = w[i][j] >> 16 & 0x7FFFu;
-            const bool low = a >= 0x7F80u, high = b >= 0x7F80u;
-            if (low || high) bad = min(bad, i);
-            w[i][j] &= (low ? 0u : 0xFFFFu) | (high ? 0u : 0xFFFF0000u);
-            top = max(top, max(low ? 0u : a, high ? 0u : b));
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4] = {x[n][i].x, x[n][i].y, x[n][i].z, x[n][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = w[j] & 0x7FFFu, b = w[j] >> 16 & 0x7FFFu;
+                const bool low = a >= 0x7F80u, high = b >= 0x7F80u;
+                if (low || high) bad = min(bad, i);
+                w[j] &= (low ? 0u : 0xFFFFu) | (high ? 0u : 0xFFFF0000u);
+                top = max(top, max(low ? 0u : a, high ? 0u : b));
+            }
+            x[n][i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     return top;
 }
@@ -206,9 +215,11 @@ __device__ __forceinline__ int scale_of(uint32_t top) {
 // registers as the first product's operand, every wave turns the values of its own tiles to fp16 and
 // transposes them through its own part of LDS, and the four waves meet once, at the end.  One workgroup
 // a compute unit: a wave's keys and values on their way take half of its registers.  16 heads of 128
-// channels, one token 7.5 us, 77 8.9, 200 10.6; with 128 rows a workgroup and a tile after the other
-// 7.1, 10.7 and 15.4.  What is left is the way from lengths to rows (two trips to memory) and about 1300
-// instructions a wave, one wave a vector unit.
+// channels, one token 7.4 us, 77 8.6, 200 10.4; with 128 rows a workgroup and a tile after the other
+// 7.1, 10.7 and 15.4.  The next tile's keys are asked for as soon as the products have read these, its
+// values once the registers are free of the last ones (both at once: 600 tokens 20.0 us against 18.9).
+// What is left is the way from lengths to rows (two trips to memory; waves wait for two thirds of
+// their time at 77 tokens) and a tile's instructions, one wave a vector unit.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
     constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
     uint4 k[2][kKS], x[kIts][4];
     // rows behind the prompt are its last one again: no row sees the keys, and the values are made
     // zero below
-    auto load = [&](int tile) RUDDER_INLINE {
+    auto load_keys = [&](int tile) RUDDER_INLINE {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const size_t r = (size_t)min(r0 + tile * kTile + kb * 32 + (lane & 31), r0 + n - 1);
@@ -248,6 +259,8 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
             for (int i = 0; i < kKS; ++i)
                 k[kb][i] = *reinterpret_cast<const uint4*>(from + i * 16);
         }
+    };
+    auto load_values = [&](int tile) RUDDER_INLINE {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const size_t r = (size_t)min(r0 + tile * kTile + value_keys(lane) * 4 + i, r0 + n - 1);
@@ -263,15 +276,15 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
 #pragma unroll
         for (int i = 0; i < kKS; ++i) q[i] = *reinterpret_cast<const uint4*>(from + i * 16);
     }
-    if (wave < tiles) load(wave);
+    if (wave < tiles) {
+        load_keys(wave);
+        load_values(wave);
+    }
     float l = 0.0f, c = fabsf(p.sm) * kLog2e;
     {
         u16x2_t most = {0, 0};
 #pragma unroll
-        for (int i = 0; i < kKS; ++i) {
-            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-            most = __builtin_elementwise_max(most, top_of(w));
-        }
+        for (int i = 0; i < kKS; ++i) most = __builtin_elementwise_max(most, top_of(q[i]));
         const uint32_t top = max((uint32_t)most[0], (uint32_t)most[1]);
         if (__any(top >= 0x7F80u)) {               // not finite
             if (max(top, (uint32_t)__shfl_xor((int)top, 32)) >= 0x7F80u)
@@ -308,31 +321,20 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
 #pragma unroll
             for (int i = 0; i < kKS; ++i) z[kb] = mma_bf16(k[kb][i], q[i], z[kb]);
         }
+        if (tile + kWaves < tiles) load_keys(tile + kWaves);
         // the values
-        uint32_t top = 0;
-        int bad = 4;
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-            uint32_t v[4][4];
+        if (at + kTile > n) {                      // the prompt ends in this tile
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i][0] = x[it][i].x;
-                v[i][1] = x[it][i].y;
-                v[i][2] = x[it][i].z;
-                v[i][3] = x[it][i].w;
+                const uint32_t there = at + value_keys(lane) * 4 + i < n ? ~0u : 0u;
+#pragma unroll
+                for (int it = 0; it < kIts; ++it)
+                    x[it][i] = make_uint4(x[it][i].x & there, x[it][i].y & there,
+                                          x[it][i].z & there, x[it][i].w & there);
             }
-            if (at + kTile > n) {                  // the prompt ends in this tile
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t there = at + value_keys(lane) * 4 + i < n ? ~0u : 0u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][j] &= there;
-                }
-            }
-            top = max(top, finite_top(v, bad));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[it][i] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
         }
+        int bad = 4;
+        uint32_t top = finite_top(x, bad);
         bad = bad < 4 ? value_keys(lane) * 4 + bad : kTile;
 #pragma unroll
         for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
@@ -346,7 +348,6 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
 #pragma unroll
         for (int it = 0; it < kIts; ++it)
             store_values(values, x[it], f, value_keys(lane), value_channels(lane + it * 64));
-        if (tile + kWaves < tiles) load(tile + kWaves);
         // the weights
         if (at + kTile > least) {
 #pragma unroll
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
                                    values + place<8>(i * 32 + (lane & 31), 2 * ks + half)),
                                w[ks], o[i]);
         wave_sync();
+        if (tile + kWaves < tiles) load_values(tile + kWaves);
     }
     // the waves' results side by side
     l += __shfl_xor(l, 32);
@@ -492,21 +494,17 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     if (tid == 0) first_bad = kTile;
     __syncthreads();
     const int quad = value_keys(tid), chunk = value_channels(tid);
-    uint32_t v[4][4];
+    uint4 x[1][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int key = at + quad * 4 + i;
-        uint4 x = make_uint4(0, 0, 0, 0);
+        x[0][i] = make_uint4(0, 0, 0, 0);
         if (tid < kVThreads && key < n)
-            x = *reinterpret_cast<const uint4*>(p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D +
-                                                chunk * 8);
-        v[i][0] = x.x;
-        v[i][1] = x.y;
-        v[i][2] = x.z;
-        v[i][3] = x.w;
+            x[0][i] = *reinterpret_cast<const uint4*>(p.V + (size_t)(r0 + key) * p.ldv +
+                                                      (size_t)h * D + chunk * 8);
     }
     int bad = 4;
-    uint32_t top = finite_top(v, bad);
+    uint32_t top = finite_top(x, bad);
     if (bad < 4) atomicMin(&first_bad, quad * 4 + bad);
 #pragma unroll
     for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
@@ -518,11 +516,7 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     if (tid == 0) p.notes[(size_t)h * p.slots + slot] = s + 128 + (first_bad << 8);
     if (tid >= kVThreads) return;
     const float f = __uint_as_float((uint32_t)(127 + s) << 23);
-    const uint4 out[4] = {make_uint4(v[0][0], v[0][1], v[0][2], v[0][3]),
-                          make_uint4(v[1][0], v[1][1], v[1][2], v[1][3]),
-                          make_uint4(v[2][0], v[2][1], v[2][2], v[2][3]),
-                          make_uint4(v[3][0], v[3][1], v[3][2], v[3][3])};
-    store_values(p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2), out, f, quad, chunk);
+    store_values(p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2), x[0], f, quad, chunk);
 }
 
 // 16 bytes a lane from `from` (the same for all lanes) + `offset` straight to LDS, lane after lane
