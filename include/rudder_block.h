@@ -68,10 +68,10 @@ rudder_status_t rudder_norm(const uint16_t* X, const uint16_t* R, const float* g
  * A row that is not finite has undefined codes, in that row only; without a
  * table its row scale is NaN or infinite.
  * Errors: those of rudder_norm (Y apart), INVALID_ARG also for a null
- * inv_smooth, Xq or row_scale, act_scale without stream_id, K not a multiple of 32 (of 64 for E2M3), S outside 1..8 with a
- * table, abits not 4 or 8, an unknown container, inv_smooth or Xq not 16-byte
- * aligned; UNSUPPORTED also for E2M3 with abits = 8 (8-bit E2M3 codes are not
- * built for this path).
+ * inv_smooth, Xq or row_scale, act_scale without stream_id, K not a multiple
+ * of 32 (of 64 for E2M3), S outside 1..8 with a table, abits not 4 or 8, an
+ * unknown container, inv_smooth or Xq not 16-byte aligned; UNSUPPORTED also for
+ * E2M3 with abits = 8 (8-bit E2M3 codes are not built for this path).
  */
 rudder_status_t rudder_norm_quant(const uint16_t* X, const uint16_t* R, const uint8_t* stream_id,
                                   const float* gamma, const float* inv_smooth,
@@ -170,9 +170,9 @@ size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int H
  *   o = sum_j softmax_j(sm * q . k_j) v_j,  j <= i
  * Products of q and k in bf16 with fp32 sums; the softmax is in fp32, its
  * weights rounded to fp16 (2^-11; 2^-33 of the largest below 2^-22 of it); v
- * enters with an absolute error of at most 2^-32 of the largest magnitude of its head
- * among the 64 tokens (counted from the prompt's first) around it; fp32 sums,
- * one rounding to bf16.  A row sees nothing of the rows behind it, whatever
+ * enters with an absolute error of at most 2^-32 of the largest magnitude of its
+ * head among the 64 tokens (counted from the prompt's first) around it; fp32
+ * sums, one rounding to bf16.  A row sees nothing of the rows behind it, whatever
  * they hold: infinities and NaN there leave it alone.  A query row that is not
  * finite gives NaN in its row and head, a key or value that is not finite in
  * the rows that see it and the heads that read it (a score of -inf is a weight

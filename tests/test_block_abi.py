@@ -195,6 +195,31 @@ def test_frequencies_binding(r):
         r.rotary_frequencies(16, scaling="other", device="cpu")
 
 
+def test_frequencies_of_one_element_many_times(r):
+    """An expanded or strided tensor has the elements but not the memory behind each other."""
+    one, far = torch.zeros(1, dtype=torch.float64), torch.zeros(16, dtype=torch.float64)
+    for bad in (one.expand(8), far[::2]):
+        with pytest.raises(ValueError, match="contiguous fp64"):
+            r.rudder_rotary_frequencies(16, 1e4, 0, 1.0, 0.0, 1.0, 32.0, bad)
+    assert not one.any() and not far.any()
+
+
+def test_conveniences_check_shapes(r):
+    """Vectors of other widths and codes of other sizes, also where there is nothing to do."""
+    x, g, wide = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(64), torch.zeros(128)
+    for n in (3, 0):
+        with pytest.raises(ValueError, match="gamma of 128 elements.*K=64"):
+            r.norm(x[:n], wide, 1e-6)
+        with pytest.raises(ValueError, match="gamma of 128 elements.*K=64"):
+            r.norm_quant(x[:n], wide, g, 1e-6, 8)
+        with pytest.raises(ValueError, match="inv_smooth of 128 elements.*K=64"):
+            r.norm_quant(x[:n], g, wide, 1e-6, 8)
+    for M, K, abits, codes in ((32, 64, 8, 0), (32, 64, 4, 1), (64, 64, 4, 0), (32, 128, 4, 0)):
+        Xq = torch.zeros(r.packed_act_bytes(M, K, abits, codes), dtype=torch.uint8)
+        with pytest.raises(ValueError, match="codes of M=32, K=64, abits=4, codes=0"):
+            r.dequant_act(Xq, torch.zeros(32), 32, 64, 4)
+
+
 def test_binding_refuses_host_tensors(r):
     """Tensors of the wrong place, type, size or layout never reach the library."""
     bf, i32 = torch.bfloat16, torch.int32

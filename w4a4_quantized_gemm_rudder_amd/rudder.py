@@ -457,8 +457,10 @@ def rudder_rotary_frequencies(rotary_dim: int, base: float, scaling: int, factor
                               trained: float, low: float, high: float, freq) -> None:
     """freq: a contiguous fp64 tensor of rotary_dim / 2 elements in host memory."""
     import torch
-    if freq.dtype != torch.float64 or freq.device.type != "cpu" or freq.numel() < rotary_dim // 2:
-        raise ValueError("freq: at least rotary_dim / 2 fp64 elements in host memory expected")
+    if (freq.dtype != torch.float64 or freq.device.type != "cpu" or not freq.is_contiguous()
+            or freq.numel() < rotary_dim // 2):
+        raise ValueError("freq: at least rotary_dim / 2 contiguous fp64 elements in host memory "
+                         "expected")
     _check(load_library().rudder_rotary_frequencies(rotary_dim, base, scaling, factor, trained,
                                                     low, high, _ptr(freq)))
 
@@ -688,11 +690,18 @@ def cross_attention(Q, K, V, row_start, kv_start, kv_len, max_rows: int, max_kv:
     return O
 
 
+def _check_channels(K: int, **vectors) -> None:
+    for name, v in vectors.items():
+        if v.numel() != K:
+            raise ValueError(f"{name} of {v.numel()} elements does not fit K={K} channels")
+
+
 def norm(X, gamma, eps: float, residual=None, stream=None):
     """RMS norm of X bf16 [M, K], gamma fp32 [K].  Returns Y bf16 [M, K]; with `residual` [M, K]
     (Y, H) of the sum H = bf16(residual + X)."""
     import torch
     M, K = X.shape
+    _check_channels(K, gamma=gamma)
     with _on(stream, X.device):
         Y = torch.empty(M, K, dtype=torch.bfloat16, device=X.device)
         H = None if residual is None else torch.empty_like(Y)
@@ -708,6 +717,7 @@ def norm_quant(X, gamma, inv_smooth, eps: float, abits: int, codes: int = CODES_
     [M]), with `residual` (Xq, row_scale, H)."""
     import torch
     M, K = X.shape
+    _check_channels(K, gamma=gamma, inv_smooth=inv_smooth)
     S = 1 if act_scale is None else act_scale.numel()
     with _on(stream, X.device):
         Xq = torch.empty(max(packed_act_bytes(M, K, abits, codes), 1), dtype=torch.uint8,
@@ -725,6 +735,9 @@ def norm_quant(X, gamma, inv_smooth, eps: float, abits: int, codes: int = CODES_
 def dequant_act(Xq, row_scale, M: int, K: int, abits: int, codes: int = CODES_INT, stream=None):
     """The values of packed activation codes, fp32 [M, K]."""
     import torch
+    if Xq.numel() != max(packed_act_bytes(M, K, abits, codes), 1):
+        raise ValueError(f"Xq of {Xq.numel()} bytes are not the codes of M={M}, K={K}, "
+                         f"abits={abits}, codes={codes}")
     with _on(stream, Xq.device):
         out = torch.empty(M, K, dtype=torch.float32, device=Xq.device)
         if M:
