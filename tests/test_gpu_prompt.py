@@ -316,3 +316,127 @@ def test_offsets_past_32_bits(rudder):
     want, bound = ref.prompt(q, k, v, _starts(counts).tolist(), 0.125, rows=rows)
     at = torch.cat([r0 + rows[rows < n] for r0, n in zip(_starts(counts).tolist(), counts)])
     aref.assert_within("O", got[at], want[at], bound[at])
+
+
+# Prompts of no rows behind the others: enough work units for the kernel for many rows at any size.
+EMPTY = [0] * 600
+
+
+def _run_many(rudder, q, k, v, counts, sm):
+    n = rudder.prompt_attention_workspace_bytes(len(counts + EMPTY), q.shape[0], max(counts),
+                                                q.shape[1], k.shape[1], q.shape[2])
+    assert n > 0
+    return _run(rudder, q, k, v, counts + EMPTY, sm)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (6, 2), (8, 1), (5, 1)])
+@pytest.mark.parametrize("counts", COUNTS)
+def test_prompts_among_many(rudder, counts, Hq, Hkv, D):
+    log(f"case prompt among many {counts} Hq={Hq} Hkv={Hkv} D={D}")
+    q, k, v = _inputs(counts, Hq, Hkv, D, sum(counts) + D + 1, 1.5)
+    sm = 1 / math.sqrt(D)
+    got = _run_many(rudder, q, k, v, counts, sm)
+    heads = sorted({0, Hq // 2, Hq - 1})
+    want, bound = ref.prompt(q, k, v, _starts(counts).tolist(), sm, heads)
+    aref.assert_within("O", got[:, heads], want[:, heads], bound[:, heads])
+
+
+@pytest.mark.parametrize("rows,D", [(70, 64), (330, 128)])
+@pytest.mark.parametrize("scale,sm", [(1.0, 0.0), (1.0, -2.0), (30.0, 0.3), (1e30, 1e-31),
+                                      (1e30, 0.0), (1e-30, 1e29), (0.0, 0.1)])
+def test_scales_among_many(rudder, rows, D, scale, sm):
+    log(f"case prompt among many scale={scale} sm={sm} rows={rows} D={D}")
+    counts = [rows, 1, 40]
+    q, k, v = _inputs(counts, 2, 1, D, 51, scale)
+    got = _run_many(rudder, q, k, v, counts, sm)
+    want, bound = ref.prompt(q, k, v, _starts(counts).tolist(), sm)
+    aref.assert_within("O", got, want, bound)
+
+
+@pytest.mark.parametrize("rows,D", [(200, 64), (400, 128)])
+def test_sizes_of_values_among_many(rudder, rows, D):
+    log(f"case prompt among many value sizes rows={rows} D={D}")
+    q, k, v = _inputs([rows], 3, 1, D, 53)
+    tile = torch.arange(rows) // 64
+    for powers in ([0, 20, -20, 3, 60, -60], [100, 0, -100], [-126, -100, -60, 0],
+                   [8, 7, 6, 7, 8, -1, -2], [115]):
+        e = torch.tensor(powers)[tile % len(powers)].double()
+        vv = (v.double() * (2.0 ** e)[:, None, None]).to(torch.bfloat16)
+        vv[tile == 1] = 0
+        got = _run_many(rudder, q, k, vv, [rows], 0.1)
+        for t in list(range(70)) + list(range(70, rows, 13)):
+            want, bound = ref.prompt(q[:t + 1], k[:t + 1], vv[:t + 1], [0, t + 1], 0.1,
+                                     rows=torch.tensor([t]))
+            aref.assert_within(f"{powers} row {t}", got[t:t + 1], want[t:], bound[t:])
+
+
+@pytest.mark.parametrize("rows,D", [(130, 64), (400, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3.3e38])
+def test_rows_among_many_see_nothing_behind_them(rudder, rows, D, bad):
+    log(f"case prompt among many behind rows={rows} D={D} bad={bad}")
+    counts, Hq, Hkv = [rows, 50], 4, 2
+    q, k, v = _inputs(counts + [30], Hq, Hkv, D, 57)
+    clean = _run_many(rudder, q, k, v, counts, 0.1)
+    for at in (0, 1, 63, 64, 100, rows - 1):
+        kk, vv = k.clone(), v.clone()
+        vv[at, 1, 5] = bad
+        vv[sum(counts):] = bad
+        kk[sum(counts):] = bad
+        got = _run_many(rudder, q, kk, vv, counts, 0.1)
+        assert torch.equal(got[:, :2], clean[:, :2]), at           # heads of the other key head
+        if math.isfinite(bad):
+            # whole tiles in front keep their bits, as in test_rows_see_nothing_behind_them
+            whole = at // 64 * 64
+            assert torch.equal(got[:whole, 2:], clean[:whole, 2:]), at
+        else:
+            assert torch.equal(got[:at, 2:], clean[:at, 2:]), at
+            assert torch.isnan(got[at:rows, 2:]).all(), at
+        assert torch.equal(got[rows:], clean[rows:]), at
+        kk = k.clone()
+        kk[at, 1] = bad
+        got = _run_many(rudder, q, kk, v, counts, 0.1)
+        assert torch.equal(got[:at], clean[:at]) and torch.equal(got[rows:], clean[rows:]), at
+        assert torch.equal(got[:, :2], clean[:, :2]), at
+        if math.isnan(bad):
+            assert torch.isnan(got[at:rows, 2:]).all(), at
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_among_many_that_are_not_finite(rudder, D):
+    log(f"case prompt among many queries not finite D={D}")
+    rows = 150
+    q, k, v = _inputs([rows, 9], 4, 2, D, 59)
+    clean = _run_many(rudder, q, k, v, [rows, 9], 0.1)
+    bad = q.clone()
+    spots = [(0, 1, float("nan")), (33, 0, float("inf")), (64, 3, -float("inf")),
+             (rows - 1, 2, float("inf")), (rows + 3, 1, float("nan"))]
+    for t, h, x in spots:
+        bad[t, h, 7] = x
+    got = _run_many(rudder, bad, k, v, [rows, 9], 0.1)
+    for t, h, _ in spots:
+        assert torch.isnan(got[t, h]).all(), (t, h)
+        got[t, h] = clean[t, h]
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,rows", [(64, 24, 8, 300), (64, 24, 8, 682), (64, 24, 8, 683),
+                                           (128, 16, 16, 512), (128, 16, 16, 513),
+                                           (128, 16, 16, 1024), (128, 16, 16, 1025)])
+def test_sizes_beside_the_limits_of_a_kernel(rudder, D, Hq, Hkv, rows):
+    """The last and the first sizes of each kernel, with the workspace that the library asks for and
+    not a byte more."""
+    log(f"case prompt limits D={D} Hq={Hq} Hkv={Hkv} rows={rows}")
+    q, k, v = _inputs([rows], Hq, Hkv, D, 61)
+    sm = 1 / math.sqrt(D)
+    n = rudder.prompt_attention_workspace_bytes(1, rows, rows, Hq, Hkv, D)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    O = torch.zeros(rows, Hq, D, dtype=torch.bfloat16, device="cuda")
+    rudder.rudder_prompt_attention(q.cuda(), k.cuda(), v.cuda(), _starts([rows]).cuda(), 1, rows,
+                                   rows, Hq, Hkv, D, sm, buf[:n] if n else None, O)
+    some = torch.cat([torch.arange(40), torch.arange(40, rows, 17), torch.tensor([rows - 1])]).unique()
+    heads = [0, Hq - 1]
+    want, bound = ref.prompt(q, k, v, [0, rows], sm, heads, some)
+    got = O.cpu()
+    aref.assert_within("O", got[some][:, heads], want[some][:, heads], bound[some][:, heads])
+    assert (buf[n:] == 0xA5).all()

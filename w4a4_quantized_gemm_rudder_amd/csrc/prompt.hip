@@ -214,14 +214,15 @@ __device__ __forceinline__ int scale_of(uint32_t top) {
 // Short prompts are a matter of latency: no launch goes in front, keys come from memory straight to
 // registers as the first product's operand, every wave turns the values of its own tiles to fp16 and
 // transposes them through its own part of LDS, and the four waves meet once, at the end.  One workgroup
-// a compute unit: a wave's keys and values on their way take half of its registers.  16 heads of 128
+// a compute unit, two of 64 channels (2 x 256 rows of 24 heads 8.9 us, one 12.1; three spill): a wave's
+// keys and values on their way take half of its registers.  16 heads of 128
 // channels, one token 7.4 us, 77 8.6, 200 10.4; with 128 rows a workgroup and a tile after the other
 // 7.1, 10.7 and 15.4.  The next tile's keys are asked for as soon as the products have read these, its
 // values once the registers are free of the last ones (both at once: 600 tokens 20.0 us against 18.9).
 // What is left is the way from lengths to rows (two trips to memory; waves wait for two thirds of
 // their time at 77 tokens) and a tile's instructions, one wave a vector unit.
 template <int D>
-__global__ void __launch_bounds__(256) prompt_few_kernel(const Prompt p) {
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const Prompt p) {
     constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;
     constexpr int kWaves = 4, kStride = D + 4;     // of a row of partial outputs, in floats
     __shared__ __align__(16) uint8_t lds[kWaves * (kBytes > kWaveRows * kStride * 4
@@ -839,21 +840,25 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
 
 namespace {
 
+// Workgroups of the kernel for few rows that run at once.
+int round_of(int D) { return D == 64 ? 512 : 256; }
+
 // Work units of the kernel for few rows.
 int64_t few_units(int B, int T, int max_rows, int G, int Hkv) {
     const int64_t rows = (int64_t)(max_rows < T ? max_rows : T) * G;
     return (rows + kWaveRows - 1) / kWaveRows * B * Hkv;
 }
 
-// The kernel for few rows where its workgroups, one a compute unit, make one round, or two and the
-// prompts are long: there a round beside the launch in front costs less.  us, few | many rows, 128
-// channels: 4 x 77 rows of 16 heads (192 units) 9.6 | 12.9, 2 x 256 (256) 11.7 | 17.8, 4 x 130 (320)
-// 17.1 | 15.7, 2 x 400 (416, 7 tiles) 22.8 | 21.3, 1 x 600 (304, 10 tiles) 19.8 | 23.6, 1 x 1000 (512)
-// 34.6 | 36.0, 2 x 600 (608) 36.6 | 26.0; 64 channels, 24 heads of eight key heads: 4 x 77 (256) 7.0 |
-// 11.3, 2 x 256 (384, 4 tiles) 12.5 | 13.5, 1 x 600 (456) 17.3 | 20.1, 2 x 400 (608) 20.3 | 16.4.
+// The kernel for few rows where its workgroups make one round, or, of 128 channels, two and the prompts
+// are long: there a round beside the launch in front costs less.  us, few | many rows, 128 channels: 4 x
+// 77 rows of 16 heads (192 units) 9.6 | 12.9, 2 x 256 (256) 11.4 | 17.8, 4 x 130 (320) 17.1 | 15.7, 2 x
+// 400 (416, 7 tiles) 22.8 | 21.3, 1 x 600 (304, 10 tiles) 18.9 | 23.6, 1 x 1000 (512) 34.6 | 36.0, 2 x
+// 600 (608) 36.6 | 26.0; 64 channels, 24 heads of eight key heads: 2 x 256 (384) 8.8 | 11.5, 1 x 600
+// (456) 12.9 | 15.9, 8 x 77 (512) 8.0 | 10.1, 2 x 400 (608) 13.4 | 13.1, 12 x 77 (768) 11.2 | 10.5, 1 x
+// 1000 (752) 21.3 | 20.8; 8 heads of two, 1 x 2000 (500) 22.2 | 31.3.
 bool few_rows(int64_t units, int max_rows, int D) {
     const int tiles = (max_rows + kTile - 1) / kTile;
-    return units <= 256 || (units <= 512 && tiles >= (D == 64 ? 4 : 9));
+    return units <= round_of(D) || (D == 128 && units <= 512 && tiles >= 9);
 }
 
 // Waves of the kernel for many rows, eight or four.  Four make rounds of workgroups that end more
@@ -876,9 +881,9 @@ int slots_of(int B, int T) { return T / kTile + B; }
 
 bool prompt_attention_workspace(int B, int T, int max_rows, int Hq, int Hkv, int D, size_t& bytes) {
     const int64_t units = few_units(B, T, max_rows, Hq / Hkv, Hkv);
-    // from more than one round of the few rows' kernel on, whichever is taken then: no smaller call
-    // needs more
-    bytes = units > 256 ? (size_t)slots_of(B, T) * Hkv * (kTile * D * 2 + 4) : 0;
+    // from more than one round of the few rows' kernel on, which is all there is up to there, whichever
+    // is taken then: no smaller call needs more
+    bytes = units > round_of(D) ? (size_t)slots_of(B, T) * Hkv * (kTile * D * 2 + 4) : 0;
     return units <= (1 << 23);
 }
 
@@ -919,6 +924,7 @@ hipError_t launch_prompt_attention(const uint16_t* Q, const uint16_t* K, const u
             prompt_few_kernel<128><<<grid, 256, 0, stream>>>(p);
         return hipGetLastError();
     }
+    if (!workspace) return hipErrorInvalidValue;
     p.slots = slots_of(B, T);
     p.images = static_cast<uint8_t*>(workspace);
     p.notes = reinterpret_cast<int32_t*>(p.images + (size_t)p.slots * Hkv * (kTile * D * 2));
