@@ -520,28 +520,11 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     store_values(p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2), x[0], f, quad, chunk);
 }
 
-// 16 bytes a lane from `from` (the same for all lanes) + `offset` straight to LDS, lane after lane
-// from `lds` on.  In assembly, so that the compiler waits for none of them in front of LDS reads:
-// wait_barrier() orders them.
-__device__ __forceinline__ void load_lds(const void* from, uint32_t offset, uint32_t lds) {
-    const uint64_t a = reinterpret_cast<uint64_t>(from);
-    const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
-                        (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :
-                 : "v"(offset), "s"(at), "s"(__builtin_amdgcn_readfirstlane(lds))
-                 : "memory");
-}
 // All but the wave's last N loads have landed, its LDS reads are done; then the workgroup's barrier.
 template <int N>
 __device__ __forceinline__ void wait_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-    typedef __attribute__((address_space(3))) const void* lds_ptr;
-    return (uint32_t)(uintptr_t)(lds_ptr)p;
-}
-
 // ---------------------------------------------------------------------------
 // Many rows: waves of 32 rows that share the tiles in LDS.
 // ---------------------------------------------------------------------------
@@ -608,15 +591,15 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
         const bool ends = tile == whole;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            load_lds(from, ends ? k_end[j] : k_from[j],
-                     base + slot * kBytes + (wave * kLoads + j) * 1024);
+            load_lds16(from, ends ? k_end[j] : k_from[j],
+                       base + slot * kBytes + (wave * kLoads + j) * 1024);
     };
     auto load_values = [&](int i, int slot) RUDDER_INLINE {
         const uint8_t* from = vp + (size_t)min(i, tiles - 1) * p.Hkv * kBytes;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            load_lds(from, (wave * kLoads + j) * 1024 + lane * 16,
-                     base + (RING + slot) * kBytes + (wave * kLoads + j) * 1024);
+            load_lds16(from, (wave * kLoads + j) * 1024 + lane * 16,
+                       base + (RING + slot) * kBytes + (wave * kLoads + j) * 1024);
     };
 
     uint4 q[kKS];

@@ -92,6 +92,34 @@ __device__ __forceinline__ float step_reciprocal(float d) {
     return d > 0.0f ? (float)(1.0 / (double)d) : 0.0f;
 }
 
+// Direct-to-LDS 16-byte load: lane l reads 16 bytes at base + voff(l)
+// (wave-uniform 64-bit base in SGPRs, 32-bit per-lane offset) and the wave
+// writes them lane-linearly at LDS offset `lds` (M0).  Written as inline asm
+// so the compiler does not add its own conservative vmcnt waits in front of
+// LDS reads; the kernels order these loads themselves, with waits and barriers
+// of their own.  The instruction has no VGPR results.  A load to LDS has to
+// stand one wait state behind the scalar write of M0 that it reads; the
+// compiler keeps that between instructions of its own, not inside an asm block.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t voff, uint32_t lds) {
+    // the base is wave-uniform by construction; make that explicit so it
+    // is always held in SGPRs
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    const void* sbase = reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo);
+    const uint32_t slds = __builtin_amdgcn_readfirstlane(lds);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(voff), "s"(sbase), "s"(slds)
+                 : "memory", "m0");
+}
+
+// LDS offset of a generic pointer into LDS.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    typedef __attribute__((address_space(3))) const void* lds_ptr;
+    return (uint32_t)(uintptr_t)(lds_ptr)p;
+}
+
 // Symmetric quantizer: clamp to [-q, q], round half to even.
 __device__ __forceinline__ int quantize_clamped(float v, float q) {
     v = fminf(fmaxf(v, -q), q);

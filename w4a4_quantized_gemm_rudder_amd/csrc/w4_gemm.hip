@@ -79,7 +79,6 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int BM = 128;          // tokens per block tile
 constexpr int BN = 256;          // output channels per block tile
@@ -249,26 +248,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rne(float a, float b) {
     return r;
 }
 
-// Direct-to-LDS 16-byte load: lane l reads 16 bytes at sbase + voff(l)
-// (wave-uniform 64-bit base in SGPRs, 32-bit per-lane offset) and the wave
-// writes them lane-linearly at LDS offset `lds` (M0).  Written as inline asm
-// so the compiler does not add its own conservative vmcnt waits in front of
-// LDS reads; the kernel orders these loads itself with wait_and_barrier().
-// The instruction has no VGPR results.
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t voff, uint32_t lds) {
-    // the base is wave-uniform by construction; make that explicit so it
-    // is always held in SGPRs
-    const uint64_t b = reinterpret_cast<uint64_t>(base);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
-    const void* sbase = reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo);
-    const uint32_t slds = __builtin_amdgcn_readfirstlane(lds);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :
-                 : "v"(voff), "s"(sbase), "s"(slds)
-                 : "memory");
-}
-
 // Wait until this wave's LDS reads are complete and at most N of its
 // vector-memory loads are in flight, then barrier the workgroup: afterwards
 // every wave's loads up to that point have landed in LDS, and no wave still
@@ -282,10 +261,6 @@ template <int N>
 __device__ __forceinline__ void wait_and_barrier() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-    return (uint32_t)(uintptr_t)(lds_ptr_t)p;
 }
 
 // Map the linear workgroup id to (tile_m, tile_n): XCD-contiguous ranges,
