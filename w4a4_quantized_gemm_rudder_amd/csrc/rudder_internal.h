@@ -100,6 +100,8 @@ __device__ __forceinline__ float step_reciprocal(float d) {
 // of their own.  The instruction has no VGPR results.  A load to LDS has to
 // stand one wait state behind the scalar write of M0 that it reads; the
 // compiler keeps that between instructions of its own, not inside an asm block.
+// M0 is reserved: it cannot be a clobber, and the compiler writes it in front
+// of each use of its own.
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t voff, uint32_t lds) {
     // the base is wave-uniform by construction; make that explicit so it
     // is always held in SGPRs
@@ -111,7 +113,7 @@ __device__ __forceinline__ void load_lds16(const void* base, uint32_t voff, uint
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(voff), "s"(sbase), "s"(slds)
-                 : "memory", "m0");
+                 : "memory");
 }
 
 // LDS offset of a generic pointer into LDS.
