@@ -11,12 +11,13 @@
 // order.  With 32x32x16 products a lane of half h = lane / 32 holds keys
 // 8 * (j / 4) + 4 * h + j % 4, j = 0..15, of a block of 32.
 //
-// Weights P are held in fp16 (2^-11 relative; times 2^8, so that weights down to
+// Weights P are held in fp16 (2^-11 relative; times 2^9, so that weights down to
 // 2^-22 of the largest keep all of their bits), values in fp16 as well: a
 // tile's values, times a power of two that brings their largest magnitude into
 // [2^7, 2^15), are exact in fp16 down to 2^-24 of that magnitude and off by at
 // most 2^-32 of it below.  The power is a multiple of 8, so that tiles of like
-// values share one; where one differs, O follows the smallest.
+// values share one; where one differs, a row's O is brought to it in 32 bits
+// (see follow()), so that no tile's values or weights lose bits to another's.
 #include <cmath>
 #include <type_traits>
 
@@ -37,9 +38,14 @@ typedef float f32x16_acc __attribute__((ext_vector_type(16)));
 constexpr int kTile = 64;                          // keys
 constexpr int kWaveRows = 32;                      // query rows a wave
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 8.0f;                    // P and its sums are held times 2^8
-// The running maximum is raised only where a score passes it by more than 2^6: P stays below 2^14.
+constexpr float kPShift = 9.0f;                    // P and its sums are held times 2^9
+// The running maximum is raised only where a score passes it by more than 2^6: P stays below 2^15.
 constexpr float kLazy = 6.0f;
+// Scores this far below the maximum have weights of at most 2^-26, zeros in fp16 whatever the
+// exponential's last bits.
+constexpr float kNothing = kPShift + 26.0f;
+// O is brought to a larger power of two up to this size: further sums are far from 32 bits' end.
+constexpr int kRoom = 96;
 
 struct Prompt {
     const uint16_t *Q, *K, *V;
@@ -201,6 +207,28 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// A row's O, held times 2^scale by the row's two lanes, for a tile whose values are times 2^s: returns
+// the power of two by which this tile's weights have to be smaller.  That is 0 but for a row whose O would
+// not stay below 2^kRoom times 2^s; there the weights' lost bits are beneath O's own.  A row to which the
+// tile adds nothing (`counts` false) keeps its scale, however large the values.
+template <int DT>
+__device__ __forceinline__ int follow(f32x16_acc (&o)[DT], int& scale, int s, bool counts) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(o[i][j]));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const int room = top > 0.0f ? max(kRoom + 127 - (int)(__float_as_uint(top) >> 23), 0) : 1 << 20;
+    const int by = counts ? min(s - scale, room) : 0;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = __builtin_amdgcn_ldexpf(o[i][j], max(by, -300));
+    scale += by;
+    return counts ? s - scale : 0;
+}
+
 // The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
 // that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
 __device__ __forceinline__ int scale_of(uint32_t top) {
@@ -310,7 +338,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -INFINITY;
-    int scale = 1 << 20, first_bad = 1 << 30;      // O of the lane's row is held times 2^scale
+    int scale = 0, first_bad = 1 << 30;            // O of the lane's row is held times 2^scale
     uint8_t* values = lds + wave * kBytes;
     for (int tile = wave; tile < tiles; tile += kWaves) {
         const int at = tile * kTile;
@@ -364,19 +392,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll
             for (int j = 0; j < 16; ++j) best = fmaxf(best, z[kb][j]);
         best *= c;
-        const float raised = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)));
-        const bool smaller = s < scale && at < limit;
+        best = fmaxf(best, __shfl_xor(best, 32));
+        const float raised = fmaxf(m, best);
+        int above = 0;
         if (tile >= kWaves) {                      // O is more than nothing
-            float alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+            const float alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
             l *= alpha;
-            if (smaller) alpha = __builtin_amdgcn_ldexpf(alpha, max(s - scale, -252));
 #pragma unroll
             for (int i = 0; i < kDT; ++i) o[i] *= alpha;
+            if (__any(scale != s && at < limit)) above = follow(o, scale, s, best > raised - kNothing);
+        } else {
+            scale = s;
         }
         m = raised;
-        scale = smaller ? s : scale;
-        // weights for smaller values than before; in the wave's first tile there are none
-        const int less = tile >= kWaves && at < limit ? scale - s : 0;
         const float shift = kPShift - (m == -INFINITY ? 0.0f : m);
         uint4 w[4];
 #pragma unroll
@@ -392,8 +420,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
             }
             w[ks] = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        if (__any(less)) {
-            const float down = __builtin_amdgcn_ldexpf(1.0f, less);
+        if (__any(above)) {
+            const float down = __builtin_amdgcn_ldexpf(1.0f, -above);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) w[ks] = times(w[ks], down);
         }
@@ -430,41 +458,36 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
         const int r = i / kChunks, d = i % kChunks * 8, rr = row0 + r;
         if (rr >= rows) continue;
         const int tt = rr / p.G, hd = h * p.G + rr % p.G;
-        float best = -INFINITY, sum = 0.0f;
-        int low = 1 << 20, first = 1 << 30;
+        float best = -INFINITY, sum = 0.0f, f[kWaves];
+        int first = 1 << 30;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             best = fmaxf(best, stats[w][r].x);
-            if (stats[w][r].x > -INFINITY) low = min(low, scales[w][r]);
             first = min(first, first_bads[w]);
         }
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float2 ml = stats[w][r];
+            // a maximum of -inf: the wave has seen no key of this row (or its sum is NaN)
+            f[w] = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - best);
+            sum += ml.x == -INFINITY ? ml.y : ml.y * f[w];
+        }
+        // every row sees itself: a sum of zero is one of scores of -inf alone
+        float share = sum > 0.0f ? 1.0f / sum : __uint_as_float(0x7FC00000u);
+        if (tt >= first) share = __uint_as_float(0x7FC00000u);     // sees a value that is not finite
         float y[8] = {};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             if (w >= tiles && w > 0) break;        // the wave had no tile
-            const float2 ml = stats[w][r];
-            // a maximum of -inf: the wave has seen no key of this row (or its sum is NaN)
-            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - best);
-            sum += ml.x == -INFINITY ? ml.y : ml.y * f;
-            const float g = __builtin_amdgcn_ldexpf(f, max(low - scales[w][r], -252));
             const float4* from = reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(lds) + (w * kWaveRows + r) * kStride + d);
             const float4 u = from[0], v = from[1];
-            if (ml.x == -INFINITY) continue;
-            y[0] = fmaf(u.x, g, y[0]);
-            y[1] = fmaf(u.y, g, y[1]);
-            y[2] = fmaf(u.z, g, y[2]);
-            y[3] = fmaf(u.w, g, y[3]);
-            y[4] = fmaf(v.x, g, y[4]);
-            y[5] = fmaf(v.y, g, y[5]);
-            y[6] = fmaf(v.z, g, y[6]);
-            y[7] = fmaf(v.w, g, y[7]);
-        }
-        // every row sees itself: a sum of zero is one of scores of -inf alone
-        float f = sum > 0.0f ? 1.0f / sum : __uint_as_float(0x7FC00000u);
-        if (tt >= first) f = __uint_as_float(0x7FC00000u);         // sees a value that is not finite
+            const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            const float g = f[w] * share;
+            const int e = -scales[w][r];           // a part of its own power of two each
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __builtin_amdgcn_ldexpf(y[j] * f, -low);
+            for (int j = 0; j < 8; ++j) y[j] += __builtin_amdgcn_ldexpf(x[j] * g, e);
+        }
         *reinterpret_cast<uint4*>(p.O + (size_t)(r0 + tt) * p.ldo + (size_t)hd * D + d) =
             make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
                        pack_bf16(y[6], y[7]));
@@ -643,7 +666,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -INFINITY;
-    int scale = 1 << 20;                           // the row's
+    int scale = 1 << 20;                           // the row's, of no tile yet
     int first_bad = 1 << 30;
     int k_at[kKS], v_at[4];                        // where the lane's operands lie in a tile
 #pragma unroll
@@ -685,21 +708,6 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
 #pragma unroll
         for (int j = 1; j < 16; ++j) best = fmaxf(best, z[j]);
         best *= c;
-        // O of a row is held times 2^scale, the smallest power of the tiles that it has seen; where all
-        // rows see the tile it is one number
-        constexpr bool kMasked = decltype(masked)::value;
-        const int had = kMasked ? scale : __builtin_amdgcn_readfirstlane(scale);
-        const bool smaller = s < had && (!kMasked || at < limit);
-        if (kMasked ? __any(smaller) : smaller) {
-            // larger values than before.  The weights of the 32 keys before go first: in fp16 they
-            // would not survive the factor, and their row may see nothing of this tile
-            weigh(slot1, hf1);
-            pend0 = pend1 = make_uint4(0, 0, 0, 0);
-            const float down = smaller ? __builtin_amdgcn_ldexpf(1.0f, max(s - had, -252)) : 1.0f;
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt) o[dt] *= down;
-            scale = smaller ? s : had;
-        }
         if (__any(best > m + kLazy)) {
             // to a whole number, so that the factor is a power of two: exact, for the weights of the
             // 32 keys before as well
@@ -713,20 +721,23 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
             pend0 = times(pend0, alpha);
             pend1 = times(pend1, alpha);
         }
-        // weights for O are held times 2^(scale - s), their sum is brought back; where that is far,
-        // the sum takes exponentials of its own
-        const float base_m = m == -INFINITY ? 0.0f : m;
-        const int above = s - (kMasked ? scale : __builtin_amdgcn_readfirstlane(scale));
-        float back = __builtin_amdgcn_ldexpf(1.0f, above);
-        if (kMasked ? __any(above > 64) : above > 64) {
-            float apart = 0.0f;
+        // O of a row is held times 2^scale, the power of the tile that it saw last
+        float shift = kPShift - (m == -INFINITY ? 0.0f : m), share = 1.0f;
+        if (__any(scale != s && (!decltype(masked)::value || at < limit))) {
+            // the weights of the 32 keys before go first: they are of the power of two before
+            weigh(slot1, hf1);
+            pend0 = pend1 = make_uint4(0, 0, 0, 0);
+            const int above = follow(o, scale, s,
+                                     fmaxf(best, __shfl_xor(best, 32)) > m - kNothing);
+            if (__any(above)) {                    // the sum takes exponentials of its own
+                float apart = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                apart += __builtin_amdgcn_exp2f(fmaf(c, z[j], kPShift - base_m));
-            l += above > 64 ? apart : 0.0f;
-            back = above > 64 ? 0.0f : back;
+                for (int j = 0; j < 16; ++j) apart += __builtin_amdgcn_exp2f(fmaf(c, z[j], shift));
+                l += above ? apart : 0.0f;
+                share = above ? 0.0f : 1.0f;
+                shift -= (float)above;
+            }
         }
-        const float shift = kPShift - (float)above - base_m;
         const f32x16_acc zn = scores(slot2, hf2);
         weigh(slot1, hf1);
         float sum = 0.0f;
@@ -738,7 +749,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
             sum += a + e;
             w[j] = pack_f16(a, e);
         }
-        l = fmaf(sum, back, l);
+        l = fmaf(sum, share, l);
         pend0 = make_uint4(w[0], w[1], w[2], w[3]);
         pend1 = make_uint4(w[4], w[5], w[6], w[7]);
         z = zn;
