@@ -168,8 +168,9 @@ size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int H
  * keys and values.  For row i of sequence b, head h of Hq and its key head
  * h / (Hq / Hkv):
  *   o = sum_j softmax_j(sm * q . k_j) v_j,  j <= i
- * Products of q and k in bf16 with fp32 sums; the softmax is in fp32, its
- * weights rounded to fp16 (2^-11; 2^-33 of the largest below 2^-22 of it); v
+ * Products of q and k in bf16 with fp32 sums; the softmax is in fp32 and goes by
+ * the differences of these sums, however far from zero they are, its weights
+ * rounded to fp16 (2^-11; 2^-33 of the largest below 2^-22 of it); v
  * enters with an absolute error of at most 2^-32 of the largest magnitude of its
  * head among the 64 tokens (counted from the prompt's first) around it; fp32
  * sums, one rounding to bf16.  A row sees nothing of the rows behind it, whatever
@@ -180,8 +181,8 @@ size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int H
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   K, V     bf16 bits [T][Hkv][D], row distances ldk, ldv
- *   sm       the softmax scale, e.g. 1 / sqrt(D); sm * q . k stays below 2^126 in
- *            magnitude
+ *   sm       the softmax scale, e.g. 1 / sqrt(D); q . k and sm * q . k stay below
+ *            2^126 in magnitude
  *   workspace, workspace_bytes  at least
  *            rudder_prompt_attention_workspace_bytes(...) bytes (NULL if 0)
  *   B, T, max_rows >= 0 (0 is a no-op), Hq a multiple of Hkv, D 64 or 128

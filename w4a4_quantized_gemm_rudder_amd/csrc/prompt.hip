@@ -3,8 +3,8 @@
 //
 //   o[t][h] = sum_{j <= t} softmax_j(sm * q[t][h] . k[j][h']) * v[j][h'],  h' = h / (Hq / Hkv)
 //
-// One pass over the keys with the running maximum m and sum l of the softmax, in
-// base 2: z_j = c * (q . k_j), c = sm * log2(e).  Both products are formed
+// One pass over the keys with the running maximum and sum l of the softmax, in
+// base 2: weights are exp2(c * z_j - maximum), z_j = q . k_j, c = sm * log2(e).  Both products are formed
 // transposed, so that a query is a column of every matrix and a lane keeps one
 // query's numbers: the accumulators of Z^T = K Q^T, packed in pairs, are the
 // operand of O^T = V^T P^T, provided that the keys of V^T are stored in their
@@ -40,10 +40,14 @@ constexpr int kWaveRows = 32;                      // query rows a wave
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 9.0f;                    // P and its sums are held times 2^9
 // The running maximum is raised only where a score passes it by more than 2^6: P stays below 2^15.
-constexpr float kLazy = 6.0f;
-// Scores this far below the maximum have weights of at most 2^-26, zeros in fp16 whatever the
-// exponential's last bits.
-constexpr float kNothing = kPShift + 26.0f;
+constexpr float kMostP = kPShift + 6.0f;
+// Weights of at most 2^-26 are zeros in fp16, whatever the exponential's last bits.
+constexpr float kNothing = -26.0f;
+// Of a row that has seen no score above -inf: any one is above its maximum.
+constexpr float kUnset = 3e38f;
+// Maxima below this magnitude are kept as whole numbers in base 2, exact in 32 bits, others as the score
+// itself.
+constexpr float kFar = 4194304.0f;
 // O is brought to a larger power of two up to this size: further sums are far from 32 bits' end.
 constexpr int kRoom = 96;
 
@@ -229,6 +233,24 @@ __device__ __forceinline__ int follow(f32x16_acc (&o)[DT], int& scale, int s, bo
     return counts ? s - scale : 0;
 }
 
+// What a row's weights are relative to: P = exp2(c (z - a) + b).  Near zero a is 0 and b a whole number,
+// so that a new maximum is a power of two on all that was summed; far from it, where c z and a number
+// beside it have no bits left for b, a is the largest score and the difference is taken first.
+struct Reference {
+    float a, b;
+    // log2 of P for a score
+    __device__ __forceinline__ float exponent(float c, float z) const { return fmaf(c, z - a, b); }
+    // log2 of what turns weights relative to this into weights relative to another
+    __device__ __forceinline__ float to(float c, const Reference& other) const {
+        return fmaf(c, a - other.a, other.b - b);
+    }
+};
+// The reference for a largest score of z.
+__device__ __forceinline__ Reference reference(float c, float z) {
+    const float t = c * z;
+    return fabsf(t) < kFar ? Reference{0.0f, kPShift - ceilf(t)} : Reference{z, kPShift};
+}
+
 // The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
 // that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
 __device__ __forceinline__ int scale_of(uint32_t top) {
@@ -255,7 +277,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
     constexpr int kWaves = 4, kStride = D + 4;     // of a row of partial outputs, in floats
     __shared__ __align__(16) uint8_t lds[kWaves * (kBytes > kWaveRows * kStride * 4
                                                        ? kBytes : kWaveRows * kStride * 4)];
-    __shared__ float2 stats[kWaves][kWaveRows];    // a row's maximum and sum, ...
+    __shared__ Reference refs[kWaves][kWaveRows];  // what a row's weights are relative to, ...
+    __shared__ float sums[kWaves][kWaveRows];      // ... their sum ...
     __shared__ int scales[kWaves][kWaveRows];      // ... and the power of two of its outputs
     __shared__ int first_bads[kWaves];
 
@@ -337,7 +360,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -INFINITY;
+    Reference ref = {0.0f, kUnset};
+    bool far = false;                              // of a row of the wave
     int scale = 0, first_bad = 1 << 30;            // O of the lane's row is held times 2^scale
     uint8_t* values = lds + wave * kBytes;
     for (int tile = wave; tile < tiles; tile += kWaves) {
@@ -391,21 +415,30 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int j = 0; j < 16; ++j) best = fmaxf(best, z[kb][j]);
-        best *= c;
         best = fmaxf(best, __shfl_xor(best, 32));
-        const float raised = fmaxf(m, best);
-        int above = 0;
-        if (tile >= kWaves) {                      // O is more than nothing
-            const float alpha = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
-            l *= alpha;
+        const bool raised = ref.exponent(c, best) > kPShift;
+        if (__any(raised)) {
+            const Reference now = raised ? reference(c, best) : ref;
+            if (tile >= kWaves) {                  // O is more than nothing
+                const float alpha = __builtin_amdgcn_exp2f(ref.to(c, now));
+                l *= alpha;
 #pragma unroll
-            for (int i = 0; i < kDT; ++i) o[i] *= alpha;
-            if (__any(scale != s && at < limit)) above = follow(o, scale, s, best > raised - kNothing);
-        } else {
-            scale = s;
+                for (int i = 0; i < kDT; ++i) o[i] *= alpha;
+            }
+            ref = now;
+            far = __any(ref.a != 0.0f);
         }
-        m = raised;
-        const float shift = kPShift - (m == -INFINITY ? 0.0f : m);
+        int above = 0;
+        if (tile < kWaves)
+            scale = s;
+        else if (__any(scale != s && at < limit))
+            above = follow(o, scale, s, ref.exponent(c, best) > kNothing);
+        if (far) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[kb][j] -= ref.a;
+        }
         uint4 w[4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
@@ -413,8 +446,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at_z = (ks & 1) * 8 + 2 * j;
-                const float a = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z], shift));
-                const float e = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z + 1], shift));
+                const float a = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z], ref.b));
+                const float e = __builtin_amdgcn_exp2f(fmaf(c, z[ks >> 1][at_z + 1], ref.b));
                 l += a + e;
                 y[j] = pack_f16(a, e);
             }
@@ -440,7 +473,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
     l += __shfl_xor(l, 32);
     __syncthreads();                               // the values have been read
     if (half == 0) {
-        stats[wave][lane] = make_float2(m, l);
+        refs[wave][lane] = ref;
+        sums[wave][lane] = l;
         scales[wave][lane] = scale;
     }
     if (lane == 0) first_bads[wave] = first_bad;
@@ -458,19 +492,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
         const int r = i / kChunks, d = i % kChunks * 8, rr = row0 + r;
         if (rr >= rows) continue;
         const int tt = rr / p.G, hd = h * p.G + rr % p.G;
-        float best = -INFINITY, sum = 0.0f, f[kWaves];
-        int first = 1 << 30;
+        Reference best = refs[0][r];               // of the largest score
+        float sum = 0.0f, f[kWaves];
+        int first = first_bads[0];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            best = fmaxf(best, stats[w][r].x);
+        for (int w = 1; w < kWaves; ++w) {
+            if (refs[w][r].to(c, best) > 0.0f) best = refs[w][r];
             first = min(first, first_bads[w]);
         }
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float2 ml = stats[w][r];
-            // a maximum of -inf: the wave has seen no key of this row (or its sum is NaN)
-            f[w] = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - best);
-            sum += ml.x == -INFINITY ? ml.y : ml.y * f[w];
+            // 0 for a wave that has seen no key of this row, whose sum is 0 (or NaN)
+            f[w] = __builtin_amdgcn_exp2f(refs[w][r].to(c, best));
+            sum += sums[w][r] * f[w];
         }
         // every row sees itself: a sum of zero is one of scores of -inf alone
         float share = sum > 0.0f ? 1.0f / sum : __uint_as_float(0x7FC00000u);
@@ -665,7 +699,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -INFINITY;
+    Reference ref = {0.0f, kUnset};
+    bool far = false;                              // of a row of the wave
     int scale = 1 << 20;                           // the row's, of no tile yet
     int first_bad = 1 << 30;
     int k_at[kKS], v_at[4];                        // where the lane's operands lie in a tile
@@ -707,36 +742,48 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
         float best = z[0];
 #pragma unroll
         for (int j = 1; j < 16; ++j) best = fmaxf(best, z[j]);
-        best *= c;
-        if (__any(best > m + kLazy)) {
-            // to a whole number, so that the factor is a power of two: exact, for the weights of the
-            // 32 keys before as well
-            const float raised = ceilf(fmaxf(m, fmaxf(best, __shfl_xor(best, 32))));
-            const int less = raised == -INFINITY ? 0 : (int)fmaxf(m - raised, -252.0f);
-            m = raised;
-            const float alpha = __builtin_amdgcn_ldexpf(1.0f, less);
+        if (__any(ref.exponent(c, best) > kMostP)) {
+            const float top = fmaxf(best, __shfl_xor(best, 32));
+            const Reference now = ref.exponent(c, top) > kMostP ? reference(c, top) : ref;
+            const float less = ref.to(c, now);
+            const bool was = far;
+            far = __any(now.a != 0.0f);
+            // near zero a power of two, exact for the weights of the 32 keys before as well
+            const float alpha = ref.a != 0.0f || now.a != 0.0f
+                                    ? __builtin_amdgcn_exp2f(less)
+                                    : __builtin_amdgcn_ldexpf(1.0f, (int)fmaxf(less, -252.0f));
+            if (was || far) {
+                weigh(slot1, hf1);
+                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+            }
+            pend0 = times(pend0, alpha);
+            pend1 = times(pend1, alpha);
             l *= alpha;
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) o[dt] *= alpha;
-            pend0 = times(pend0, alpha);
-            pend1 = times(pend1, alpha);
+            ref = now;
         }
         // O of a row is held times 2^scale, the power of the tile that it saw last
-        float shift = kPShift - (m == -INFINITY ? 0.0f : m), share = 1.0f;
+        float shift = ref.b, share = 1.0f;
         if (__any(scale != s && (!decltype(masked)::value || at < limit))) {
             // the weights of the 32 keys before go first: they are of the power of two before
             weigh(slot1, hf1);
             pend0 = pend1 = make_uint4(0, 0, 0, 0);
-            const int above = follow(o, scale, s,
-                                     fmaxf(best, __shfl_xor(best, 32)) > m - kNothing);
+            const float top = fmaxf(best, __shfl_xor(best, 32));
+            const int above = follow(o, scale, s, ref.exponent(c, top) > kNothing);
             if (__any(above)) {                    // the sum takes exponentials of its own
                 float apart = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) apart += __builtin_amdgcn_exp2f(fmaf(c, z[j], shift));
+                for (int j = 0; j < 16; ++j)
+                    apart += __builtin_amdgcn_exp2f(ref.exponent(c, z[j]));
                 l += above ? apart : 0.0f;
                 share = above ? 0.0f : 1.0f;
                 shift -= (float)above;
             }
+        }
+        if (far) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] -= ref.a;
         }
         const f32x16_acc zn = scores(slot2, hf2);
         weigh(slot1, hf1);
