@@ -54,7 +54,8 @@ rudder_status_t rudder_norm(const uint16_t* X, const uint16_t* R, const float* g
  * rudder_norm followed by rudder_quant_act; without one every row has a step
  * size of its own:
  *   u          = y[m][k] * inv_smooth[k]
- *   D          = act_scale[stream_id[m]], or fl32(max_k |u| / Qa)  (fp64 divide)
+ *   D          = act_scale[stream_id[m]], or fl32(max_k |u| / Qa)  (fp64 divide),
+ *                0 in place of 2^-128 and below, whose reciprocal passes 32 bits
  *   q[m][k]    = rne(clamp(u * fl32(1 / D), -Qa, Qa)),  row_scale[m] = D
  * One launch.
  *

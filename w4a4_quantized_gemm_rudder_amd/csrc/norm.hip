@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(64 * WAVES * ROWS) norm_kernel(const Norm a) {
                 for (int w = 0; w < WAVES; ++w) top = max(top, tops[in_group][w]);
             }
             step = (float)((double)__uint_as_float(top) / (double)kMost);
+            // its reciprocal would pass 32 bits, and zeros times that are no numbers
+            if (step <= 0x1p-128f) step = 0.0f;
         }
         const float inv = step_reciprocal(step);
         if (live && part == 0 && lane == 0) a.row_scale[row] = step;
