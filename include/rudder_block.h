@@ -119,8 +119,9 @@ typedef enum {
  * for RUDDER_ROTARY_PLAIN.
  * Errors: INVALID_ARG for a null freq, rotary_dim <= 0 or odd, base not above 0
  * or not finite, an unknown scaling, factor below 1 or not finite, trained not
- * above 0 or not finite, low negative, high not above low or not finite;
- * UNSUPPORTED for rotary_dim > 2^16.
+ * above 0 or not finite, low negative, high not above low or not finite, a
+ * raised base or a frequency that is not finite; UNSUPPORTED for rotary_dim >
+ * 2^16.
  */
 rudder_status_t rudder_rotary_frequencies(int rotary_dim, double base, int scaling, double factor,
                                           double trained, double low, double high, double* freq);
@@ -130,8 +131,9 @@ rudder_status_t rudder_rotary_frequencies(int rotary_dim, double base, int scali
  * sequence b has position pos[b] + i; with a = position * freq[j],
  *   (x, y) -> (x c - y s, y c + x s),  c = magnitude * cos(a), s = magnitude * sin(a)
  * for each pair j of the first rotary_dim channels of each head; the others are
- * copied.  a is right to 2^-25 turns for every position, c and s and the sums
- * are fp32, one rounding to bf16.  One launch.
+ * copied.  a is right to 2^-25 turns for every position and frequencies of up to
+ * 2^24 in magnitude, c and s and the sums are fp32, one rounding to bf16.  One
+ * launch.
  *
  *   Q, K      bf16 bits [T][Hq][D], [T][Hkv][D], row distances ldq, ldk: e.g.
  *             two parts of a QKV linear's output

@@ -4,8 +4,9 @@
 //
 // The angle is formed in turns, as the sum of two 64-bit numbers: the product
 // position * freq and its rounding error, times 1 / (2 pi) in two parts.  What
-// is left of it behind the whole turns is right to 2^-60 for every int32
-// position, and is rounded to 32 bits only then (2^-26 turns).
+// is left of it behind the whole turns is at most 3/4 and right to 2^-50 for
+// every int32 position and frequencies of up to 2^24, and is rounded to 32 bits
+// only then (2^-25 turns).
 #include "rudder_block_launch.h"
 
 namespace rudder {

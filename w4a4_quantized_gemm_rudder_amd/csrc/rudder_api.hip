@@ -717,6 +717,10 @@ rudder_status_t rudder_rotary_frequencies(int rotary_dim, double base, int scali
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: rotary_dim=%d exceeds %d", f, rotary_dim, 1 << 16);
     const int n = rotary_dim / 2;
     if (scaling == RUDDER_ROTARY_BASE && n > 1) base *= pow(factor, (double)n / (n - 1));
+    // from the first pair, of 1, on they rise or fall: the last one's is the largest or the smallest
+    if (!(base <= most && pow(base, -(double)(n - 1) / n) <= most))
+        return fail(RUDDER_ERR_INVALID_ARG, "%s: base, or what factor raises it to, is so far from 1 "
+                    "that it or a frequency passes 64 bits", f);
     for (int i = 0; i < n; ++i) {
         double x = pow(base, -(double)i / n);
         if (scaling == RUDDER_ROTARY_LINEAR) x /= factor;
