@@ -165,3 +165,26 @@ def test_large_values_of_no_weight_in_a_long_prompt(rudder, power):
         bound += 2.0 ** -32 * (p @ tops)[:, None]
         bound = bound + aref.BF16 * (want.abs() + bound) + 2.0 ** -134
         aref.assert_within(f"head {h}", got[:, h], want.cpu(), bound.cpu())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,among", KERNELS)
+@pytest.mark.parametrize("step", [12, 16, 24, 25, 26, 31])
+def test_a_maximum_that_jumps(rudder, D, rows, among, step):
+    """Every 32, 64 or 96 keys the scores go up by 2^step, and the values down by as much: the weights in
+    front of a jump count as those behind it."""
+    log(f"case prompt maximum that jumps D={D} rows={rows}/{among} 2^{step}")
+    g = torch.Generator().manual_seed(step)
+    for keys in (32, 64, 96):
+        level = torch.clamp(torch.arange(rows) // keys, max=3).float()
+        q = torch.randn(rows, 2, D, generator=g) * 0.1
+        k = torch.randn(rows, 1, D, generator=g) * 0.1
+        v = torch.rand(rows, 1, D, generator=g) + 0.5
+        q[:, :, 0] = 16.0
+        k[:, :, 0] = (level * step * math.log(2) / 16.0)[:, None]
+        v *= (2.0 ** (-level * step))[:, None, None]
+        q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+        got = _run(rudder, q, k, v, 1.0, among)
+        some = torch.cat([torch.arange(24, rows if rows < 300 else 300, 8), torch.tensor([rows - 1])])
+        want, bound = _by_tiles(q, k, v, 1.0, some)
+        aref.assert_within(f"{keys}", got[some], want, bound)

@@ -752,7 +752,9 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
             const float alpha = ref.a != 0.0f || now.a != 0.0f
                                     ? __builtin_amdgcn_exp2f(less)
                                     : __builtin_amdgcn_ldexpf(1.0f, (int)fmaxf(less, -252.0f));
-            if (was || far) {
+            // these have a factor in fp16; below its range, or where it is not a power of two, they go
+            // first (in front of a row's first key there are none)
+            if (was || far || __any(less < -14.0f && less > -1e30f)) {
                 weigh(slot1, hf1);
                 pend0 = pend1 = make_uint4(0, 0, 0, 0);
             }
