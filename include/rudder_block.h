@@ -173,14 +173,14 @@ size_t rudder_prompt_attention_workspace_bytes(int B, int T, int max_rows, int H
  *   o = sum_j softmax_j(sm * q . k_j) v_j,  j <= i
  * Products of q and k in bf16 with fp32 sums; the softmax is in fp32 and goes by
  * the differences of these sums, however far from zero they are, its weights
- * rounded to fp16 (2^-11; 2^-33 of the largest below 2^-22 of it); v
- * enters with an absolute error of at most 2^-32 of the largest magnitude of its
- * head among the 64 tokens (counted from the prompt's first) around it; fp32
- * sums, one rounding to bf16.  A row sees nothing of the rows behind it, whatever
- * they hold: infinities and NaN there leave it alone.  A query row that is not
- * finite gives NaN in its row and head, a key or value that is not finite in
- * the rows that see it and the heads that read it (a score of -inf is a weight
- * of 0).
+ * rounded to fp16 (2^-11; 2^-33 of the largest below 2^-22 of it); v enters with
+ * an absolute error of at most 2^-32 of the largest magnitude of its head in its
+ * tile (64 tokens, counted from the prompt's first), or, where the row sees only
+ * part of that tile, of at most 2^-24 of the largest of its own token and head;
+ * fp32 sums, one rounding to bf16.  A row sees nothing of the rows behind it,
+ * whatever they hold.  A query row that is not finite gives NaN in its row and
+ * head, a key or value that is not finite in the rows that see it and the heads
+ * that read it (a score of -inf is a weight of 0).
  *
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   K, V     bf16 bits [T][Hkv][D], row distances ldk, ldv

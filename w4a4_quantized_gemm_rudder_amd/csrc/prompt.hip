@@ -18,6 +18,8 @@
 // most 2^-32 of it below.  The power is a multiple of 8, so that tiles of like
 // values share one; where one differs, a row's O is brought to it in 32 bits
 // (see follow()), so that no tile's values or weights lose bits to another's.
+// A tile that a row sees only part of, whose tokens are of very different sizes,
+// takes a slow way (uneven_values()): nothing behind a row takes bits from it.
 #include <cmath>
 #include <type_traits>
 
@@ -145,17 +147,23 @@ __device__ __forceinline__ int value_keys(int tid) { return tid / 4 % 16; }
 __device__ __forceinline__ int value_channels(int tid) { return tid % 4 + tid / 64 * 4; }
 
 // N times four rows of eight bf16 values: those that are not finite made zero; `bad` becomes the first
-// such row (of four) where it is below.  Returns the largest magnitude bits of the others.
+// such row (of four) where it is below.  Returns the largest magnitude bits of the others, `tops` each
+// row's.
 template <int N>
-__device__ __forceinline__ uint32_t finite_top(uint4 (&x)[N][4], int& bad) {
-    u16x2_t most = {0, 0};
+__device__ __forceinline__ uint32_t finite_top(uint4 (&x)[N][4], int& bad, uint32_t (&tops)[4]) {
+    uint32_t top = 0;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int i = 0; i < 4; ++i) {
+        u16x2_t most = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, top_of(x[n][i]));
-    uint32_t top = max((uint32_t)most[0], (uint32_t)most[1]);
+        for (int n = 0; n < N; ++n) most = __builtin_elementwise_max(most, top_of(x[n][i]));
+        tops[i] = max((uint32_t)most[0], (uint32_t)most[1]);
+        top = max(top, tops[i]);
+    }
     if (!__any(top >= 0x7F80u)) return top;
     top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tops[i] = 0;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -167,11 +175,23 @@ __device__ __forceinline__ uint32_t finite_top(uint4 (&x)[N][4], int& bad) {
                 const bool low = a >= 0x7F80u, high = b >= 0x7F80u;
                 if (low || high) bad = min(bad, i);
                 w[j] &= (low ? 0u : 0xFFFFu) | (high ? 0u : 0xFFFF0000u);
-                top = max(top, max(low ? 0u : a, high ? 0u : b));
+                tops[i] = max(tops[i], max(low ? 0u : a, high ? 0u : b));
             }
             x[n][i] = make_uint4(w[0], w[1], w[2], w[3]);
+            top = max(top, tops[i]);
         }
     return top;
+}
+
+// Whether a token's largest magnitude is less than 2^-8 of the tile's: a row that sees the one and not the
+// other would lose more than 2^-24 of it to the tile's power of two.
+__device__ __forceinline__ bool uneven(uint32_t token, uint32_t tile) {
+    return token > 0 && token + (8 << 7) < tile;
+}
+// The largest of four neighbouring lanes, which hold 32 channels of a token.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 15, 15, true));   // 1 0 3 2
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 15, 15, true));  // 2 3 0 1
 }
 
 // Chunks of 16 bytes of an LDS row are exchanged so that 16 lanes reading one chunk of 16 rows find
@@ -211,6 +231,13 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
+// that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
+__device__ __forceinline__ int scale_of(uint32_t top) {
+    const int e = (int)(top >> 7) - 127;
+    return top ? min((14 - e) & ~7, 120) : 120;
+}
+
 // A row's O, held times 2^scale by the row's two lanes, for a tile whose values are times 2^s: returns
 // the power of two by which this tile's weights have to be smaller.  That is 0 but for a row whose O would
 // not stay below 2^kRoom times 2^s; there the weights' lost bits are beneath O's own.  A row to which the
@@ -233,6 +260,86 @@ __device__ __forceinline__ int follow(f32x16_acc (&o)[DT], int& scale, int s, bo
     return counts ? s - scale : 0;
 }
 
+// 32 values of a tile that a row sees only part of, and that are uneven: straight from memory, in bf16,
+// with every row at the power of two of what it sees of them, so that nothing behind a row takes bits from
+// it.  The fp16 weights w (16 keys each) are sums of two bf16 numbers; a key's power of two goes from its
+// values to its weights.  `v`: the first key's channels; `there`: how many of the keys there are; `seen`:
+// how many this lane's row sees.
+// Rare, and slow (two-byte loads, twice the products): where every prompt's last tile is such a one, 77
+// tokens 16.0 us against 9.4, 2 x 4192 207 against 175.
+template <int D>
+__device__ __forceinline__ void uneven_values(f32x16_acc (&o)[D / 32], int& scale,
+                                              const uint16_t* v, size_t ldv, int there, int seen,
+                                              uint4 w0, uint4 w1) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane), "+s"(ldv));      // keeps the addresses out of the loop around this
+    const int half = lane >> 5;
+    auto of_lane = [](int from, int x) { return __builtin_amdgcn_ds_bpermute(from * 4, x); };
+    // a key a lane: its largest magnitude, that of the keys up to it, and what the lane's row sees
+    int top = 0;
+    if ((lane & 31) < there) {
+        const uint4* row = reinterpret_cast<const uint4*>(v + (size_t)(lane & 31) * ldv + half * (D / 2));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint4 x = row[i];
+            const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int a = word[j] & 0x7FFFu, b = word[j] >> 16 & 0x7FFFu;
+                top = max(top, max(a >= 0x7F80 ? 0 : a, b >= 0x7F80 ? 0 : b));
+            }
+        }
+    }
+    top = max(top, of_lane(lane ^ 32, top));
+    const int key_power = min(max((top >> 7) - 127, -120), 120);
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+        const int before = of_lane(lane - off, top);
+        if ((lane & 31) >= off) top = max(top, before);
+    }
+    top = of_lane(min(max(seen, 1), 32) - 1, top);
+    int any = w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w;
+    any |= of_lane(lane ^ 32, any);
+    follow(o, scale, scale_of(top), seen > 0 && any != 0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const uint4 w = x ? w1 : w0;
+        const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+        uint32_t upper[4], lower[4], y[D / 32][4];             // two keys a word
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            __builtin_amdgcn_sched_barrier(0);     // few loads at a time: registers are full
+            const int key = 16 * x + 8 * (j >> 1) + 4 * half + 2 * (j & 1);
+            const int power0 = of_lane(key, key_power), power1 = of_lane(key + 1, key_power);
+            union { uint32_t u; f16x2_t h; } p;
+            p.u = word[j];
+            const float e0 = __builtin_amdgcn_ldexpf((float)p.h[0], scale + power0);
+            const float e1 = __builtin_amdgcn_ldexpf((float)p.h[1], scale + power1);
+            upper[j] = pack_bf16(e0, e1);
+            lower[j] = pack_bf16(e0 - __uint_as_float(upper[j] << 16),
+                                 e1 - __uint_as_float(upper[j] & 0xFFFF0000u));
+            const uint16_t* from0 = v + (size_t)min(key, there - 1) * ldv + (lane & 31);
+            const uint16_t* from1 = v + (size_t)min(key + 1, there - 1) * ldv + (lane & 31);
+            const float f0 = __uint_as_float((uint32_t)(127 - power0) << 23);
+            const float f1 = __uint_as_float((uint32_t)(127 - power1) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t b0 = from0[i * 32], b1 = from1[i * 32];
+                const bool good0 = key < there && (b0 & 0x7FFFu) < 0x7F80u;
+                const bool good1 = key + 1 < there && (b1 & 0x7FFFu) < 0x7F80u;
+                y[i][j] = pack_bf16(good0 ? __uint_as_float(b0 << 16) * f0 : 0.0f,
+                                    good1 ? __uint_as_float(b1 << 16) * f1 : 0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 z = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            o[i] = mma_bf16(z, make_uint4(upper[0], upper[1], upper[2], upper[3]), o[i]);
+            o[i] = mma_bf16(z, make_uint4(lower[0], lower[1], lower[2], lower[3]), o[i]);
+        }
+    }
+}
+
 // What a row's weights are relative to: P = exp2(c (z - a) + b).  Near zero a is 0 and b a whole number,
 // so that a new maximum is a power of two on all that was summed; far from it, where c z and a number
 // beside it have no bits left for b, a is the largest score and the difference is taken first.
@@ -249,13 +356,6 @@ struct Reference {
 __device__ __forceinline__ Reference reference(float c, float z) {
     const float t = c * z;
     return fabsf(t) < kFar ? Reference{0.0f, kPShift - ceilf(t)} : Reference{z, kPShift};
-}
-
-// The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so
-// that 2^s is a number.  A tile of zeros takes that: it must not lower the others'.
-__device__ __forceinline__ int scale_of(uint32_t top) {
-    const int e = (int)(top >> 7) - 127;
-    return top ? min((14 - e) & ~7, 120) : 120;
 }
 
 // ---------------------------------------------------------------------------
@@ -364,6 +464,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
     bool far = false;                              // of a row of the wave
     int scale = 0, first_bad = 1 << 30;            // O of the lane's row is held times 2^scale
     uint8_t* values = lds + wave * kBytes;
+    uint4 w[4];
+    int uneven_at = -1;
     for (int tile = wave; tile < tiles; tile += kWaves) {
         const int at = tile * kTile;
         f32x16_acc z[2];
@@ -387,7 +489,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
             }
         }
         int bad = 4;
-        uint32_t top = finite_top(x, bad);
+        uint32_t tops[4], top = finite_top(x, bad, tops);
         bad = bad < 4 ? value_keys(lane) * 4 + bad : kTile;
 #pragma unroll
         for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
@@ -397,12 +499,20 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
             first_bad = min(first_bad, at + bad);
         }
         const int s = __builtin_amdgcn_readfirstlane(scale_of(top));
+        const bool part = at + kTile > least;      // some rows see only part of the tile
+        bool apart = false;
+        if (part) {                                // four lanes hold a token's channels
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= uneven(quad_max(tops[i]), top);
+            apart = __any(any);
+        }
         const float f = __uint_as_float((uint32_t)(127 + s) << 23);
 #pragma unroll
         for (int it = 0; it < kIts; ++it)
             store_values(values, x[it], f, value_keys(lane), value_channels(lane + it * 64));
         // the weights
-        if (at + kTile > least) {
+        if (part) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -431,7 +541,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
         int above = 0;
         if (tile < kWaves)
             scale = s;
-        else if (__any(scale != s && at < limit))
+        else if (!apart && __any(scale != s && at < limit))
             above = follow(o, scale, s, ref.exponent(c, best) > kNothing);
         if (far) {
 #pragma unroll
@@ -439,7 +549,6 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll
                 for (int j = 0; j < 16; ++j) z[kb][j] -= ref.a;
         }
-        uint4 w[4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t y[4];
@@ -458,6 +567,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) w[ks] = times(w[ks], down);
         }
+        if (apart) {                               // the wave's last tile: no row sees one four on
+            uneven_at = at;
+            break;
+        }
         wave_sync();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
@@ -468,6 +581,15 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
                                w[ks], o[i]);
         wave_sync();
         if (tile + kWaves < tiles) load_values(tile + kWaves);
+    }
+    if (uneven_at >= 0) {
+#pragma unroll 1
+        for (int key = uneven_at; key < min(uneven_at + kTile, n); key += 32) {
+            uneven_values<D>(o, scale, p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D, p.ldv,
+                             n - key, limit - key, w[0], w[1]);
+            w[0] = w[2];
+            w[1] = w[3];
+        }
     }
     // the waves' results side by side
     l += __shfl_xor(l, 32);
@@ -528,6 +650,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
     }
 }
 
+constexpr int kUneven = 1 << 15;                   // in a tile's note
+
 // A prompt's tiles are kept at slots of their own: floor((r0 + n) / 64) + 1 >= floor(r0 / 64) +
 // ceil(n / 64), so that those of sequence b end before those of b + 1 begin.
 __device__ __forceinline__ int first_slot(int r0, int b) { return r0 / kTile + b; }
@@ -542,7 +666,7 @@ __device__ __forceinline__ int first_slot(int r0, int b) { return r0 / kTile + b
 template <int D>
 __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     constexpr int kChunks = D / 8, kVThreads = 16 * kChunks;
-    __shared__ uint32_t tops[4];
+    __shared__ uint32_t tops[4], tokens[4][kTile];
     __shared__ int first_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int b = blockIdx.z, h = blockIdx.y, at = blockIdx.x * kTile;
@@ -562,8 +686,15 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
                                                       (size_t)h * D + chunk * 8);
     }
     int bad = 4;
-    uint32_t top = finite_top(x, bad);
+    uint32_t shares[4], top = finite_top(x, bad, shares);
     if (bad < 4) atomicMin(&first_bad, quad * 4 + bad);
+    uint32_t token = 0;                            // four lanes' tokens, one a lane
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t share = quad_max(shares[i]);
+        token = (lane & 3) == i ? share : token;
+    }
+    tokens[wave][lane] = token;
 #pragma unroll
     for (int off = 32; off; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
     if (lane == 0) tops[wave] = top;
@@ -571,7 +702,12 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
     const int s = scale_of(top);
     const int slot = first_slot(r0, b) + (int)blockIdx.x;
-    if (tid == 0) p.notes[(size_t)h * p.slots + slot] = s + 128 + (first_bad << 8);
+    if (wave == 0) {                               // a token a lane
+        token = max(max(tokens[0][lane], tokens[1][lane]), max(tokens[2][lane], tokens[3][lane]));
+        const int apart = __any(uneven(token, top)) ? kUneven : 0;
+        if (lane == 0)
+            p.notes[(size_t)h * p.slots + slot] = s + 128 + (first_bad << 8) + apart;
+    }
     if (tid >= kVThreads) return;
     const float f = __uint_as_float((uint32_t)(127 + s) << 23);
     store_values(p.images + ((size_t)slot * p.Hkv + h) * (kTile * D * 2), x[0], f, quad, chunk);
@@ -730,6 +866,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
                                 x ? pend1 : pend0, o[dt]);
     };
     int s = 0;                                     // the tile's power of two
+    bool apart = false;                            // whether its values are uneven
     // z, the scores of half hf of the tile at `at`, become weights, while the matrix cores work on
     // the scores of half hf2 in place slot2 and the values of half hf1 in place slot1
     auto step = [&](auto masked, int at, int hf, int slot2, int hf2, int slot1, int hf1) RUDDER_INLINE {
@@ -767,7 +904,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
         }
         // O of a row is held times 2^scale, the power of the tile that it saw last
         float shift = ref.b, share = 1.0f;
-        if (__any(scale != s && (!decltype(masked)::value || at < limit))) {
+        if (!apart && __any(scale != s && (!decltype(masked)::value || at < limit))) {
             // the weights of the 32 keys before go first: they are of the power of two before
             weigh(slot1, hf1);
             pend0 = pend1 = make_uint4(0, 0, 0, 0);
@@ -801,6 +938,14 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
         l = fmaf(sum, share, l);
         pend0 = make_uint4(w[0], w[1], w[2], w[3]);
         pend1 = make_uint4(w[4], w[5], w[6], w[7]);
+        if constexpr (decltype(masked)::value) {
+            const int key = at + 32 * hf;
+            if (apart && key < most) {             // not in a half in front of which all has been seen
+                uneven_values<D>(o, scale, p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D, p.ldv,
+                                 n - key, limit - key, pend0, pend1);
+                pend0 = pend1 = make_uint4(0, 0, 0, 0);
+            }
+        }
         z = zn;
     };
     // Tile i in place SLOT, known when compiled: LDS addresses are then a register and a constant.
@@ -814,7 +959,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
             if (i > 0 && (i & 63) == 0) note = notes_from(i);
             const int word = __builtin_amdgcn_readlane(note, i & 63);
             s = (word & 255) - 128;
-            const int bad = word >> 8;
+            apart = decltype(masked)::value && (word & kUneven);
+            const int bad = word >> 8 & 127;
             if (bad < kTile) first_bad = min(first_bad, at + bad);
             step(masked, at, 0, SLOT, 1, kBefore, 1);
         }
