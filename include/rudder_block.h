@@ -40,8 +40,9 @@ extern "C" {
  * Errors: INVALID_ARG for a null X, gamma or Y, R without H or H without R,
  * M < 0, K <= 0 or not a multiple of 8, a row distance below K or not a
  * multiple of 8 (those of NULL are not looked at), eps negative or not finite,
- * X, R, H, gamma or Y not 16-byte aligned, Y the same buffer as H; UNSUPPORTED
- * for K > RUDDER_MAX_K, M > 2^25 or M * K > 2^35.
+ * X, R, H, gamma or Y not 16-byte aligned, Y the same buffer as H, H or Y in the
+ * place of X or R at another row distance; UNSUPPORTED for K > RUDDER_MAX_K, M >
+ * 2^25 or M * K > 2^35.
  */
 rudder_status_t rudder_norm(const uint16_t* X, const uint16_t* R, const float* gamma, float eps,
                             int M, int K, int ldx, int ldr, int ldh, int ldy, uint16_t* H,
@@ -148,8 +149,9 @@ rudder_status_t rudder_rotary_frequencies(int rotary_dim, double base, int scali
  * Errors: INVALID_ARG for a null pointer, negative sizes, Hq <= 0, an unknown
  * layout, rotary_dim <= 0, above D or not a multiple of 16, a row distance
  * below its heads' channels or not a multiple of 8, magnitude not finite, Q, K,
- * Qo or Ko not 16-byte aligned; UNSUPPORTED for D other than 64 or 128, B >
- * 65535, Hq or Hkv > 4096, more than 2^25 rows.
+ * Qo or Ko not 16-byte aligned, Qo or Ko in the place of Q or K at another row
+ * distance; UNSUPPORTED for D other than 64 or 128, B > 65535, Hq or Hkv > 4096,
+ * more than 2^25 rows.
  */
 rudder_status_t rudder_rotary(const uint16_t* Q, const uint16_t* K, const int32_t* row_start,
                               const int32_t* pos, const double* freq, float magnitude, int B,

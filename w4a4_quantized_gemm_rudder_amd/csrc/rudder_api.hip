@@ -611,6 +611,14 @@ rudder_status_t check_codes(const char* f, int K, int abits, int codes) {
     return RUDDER_OK;
 }
 
+// Rows written in the place of rows read: at other distances a row would overwrite others.
+rudder_status_t check_place(const char* f, const void* out, int ld_out, const char* name_out,
+                            const void* in, int ld_in, const char* name_in) {
+    if (!out || out != in || ld_out == ld_in) return RUDDER_OK;
+    return fail(RUDDER_ERR_INVALID_ARG, "%s: %s is %s, with rows %d and %d elements apart", f,
+                name_out, name_in, ld_out, ld_in);
+}
+
 rudder_status_t check_norm(const char* f, const void* X, const void* R, const void* gamma,
                            float eps, int M, int K, int ldx, int ldr, int ldh, const void* H) {
     if (!X || !gamma) return fail(RUDDER_ERR_INVALID_ARG, "%s: null pointer argument", f);
@@ -643,6 +651,13 @@ rudder_status_t rudder_norm(const uint16_t* X, const uint16_t* R, const float* g
     if (Y == H) return fail(RUDDER_ERR_INVALID_ARG, "%s: Y and H are one buffer", f);
     if ((st = check_rows(f, M, K)) != RUDDER_OK) return st;
     if (M == 0) return ok();
+    if (M > 1) {
+        st = check_place(f, H, ldh, "H", X, ldx, "X");
+        if (st == RUDDER_OK) st = check_place(f, H, ldh, "H", R, ldr, "R");
+        if (st == RUDDER_OK) st = check_place(f, Y, ldy, "Y", X, ldx, "X");
+        if (st == RUDDER_OK) st = check_place(f, Y, ldy, "Y", R, ldr, "R");
+        if (st != RUDDER_OK) return st;
+    }
     return from_hip(rudder::launch_norm(X, R, nullptr, gamma, nullptr, nullptr, eps, M, K, ldx,
                                         ldr, ldh, ldy, 0, 0, H, Y, nullptr, nullptr,
                                         static_cast<hipStream_t>(stream)),
@@ -670,6 +685,11 @@ rudder_status_t rudder_norm_quant(const uint16_t* X, const uint16_t* R, const ui
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: 8-bit E2M3 codes are not built for this path", f);
     if ((st = check_rows(f, M, K)) != RUDDER_OK) return st;
     if (M == 0) return ok();
+    if (M > 1) {
+        st = check_place(f, H, ldh, "H", X, ldx, "X");
+        if (st == RUDDER_OK) st = check_place(f, H, ldh, "H", R, ldr, "R");
+        if (st != RUDDER_OK) return st;
+    }
     return from_hip(rudder::launch_norm(X, R, stream_id, gamma, inv_smooth, act_scale, eps, M, K,
                                         ldx, ldr, ldh, 0, abits, codes, H, nullptr, Xq, row_scale,
                                         static_cast<hipStream_t>(stream)),
@@ -770,6 +790,11 @@ rudder_status_t rudder_rotary(const uint16_t* Q, const uint16_t* K, const int32_
         return fail(RUDDER_ERR_UNSUPPORTED, "%s: max_rows=%d exceeds %d", f, max_rows,
                     kMaxBlockRows);
     if (B == 0 || T == 0 || max_rows == 0) return ok();
+    if (T > 1) {
+        st = check_place(f, Qo, ldqo, "Qo", Q, ldq, "Q");
+        if (st == RUDDER_OK && Hkv) st = check_place(f, Ko, ldko, "Ko", K, ldk, "K");
+        if (st != RUDDER_OK) return st;
+    }
     return from_hip(rudder::launch_rotary(Q, K, row_start, pos, freq, magnitude, B, T, max_rows,
                                           Hq, Hkv, D, rotary_dim, layout, ldq, ldk, ldqo, ldko, Qo,
                                           Ko, static_cast<hipStream_t>(stream)),
