@@ -188,3 +188,16 @@ def test_a_maximum_that_jumps(rudder, D, rows, among, step):
         some = torch.cat([torch.arange(24, rows if rows < 300 else 300, 8), torch.tensor([rows - 1])])
         want, bound = _by_tiles(q, k, v, 1.0, some)
         aref.assert_within(f"{keys}", got[some], want, bound)
+
+
+@pytest.mark.parametrize("rows", [640, 641])
+def test_sizes_beside_a_limit(rudder, rows):
+    """16 heads of 128 channels: 320 work units of the few rows' kernel, and one more."""
+    log(f"case prompt values beside a limit rows={rows}")
+    g = torch.Generator().manual_seed(rows)
+    q, k, v = (torch.randn(rows, 16, 128, generator=g).to(torch.bfloat16) for _ in range(3))
+    got = _run(rudder, q, k, v, 0.09)
+    some = torch.cat([torch.arange(0, rows, 61), torch.arange(rows - 3, rows)])
+    pick = lambda x: x[:, [0, 7, 15]].contiguous()  # noqa: E731
+    want, bound = _by_tiles(pick(q), pick(k), pick(v), 0.09, some)
+    aref.assert_within("O", pick(got)[some], want, bound)

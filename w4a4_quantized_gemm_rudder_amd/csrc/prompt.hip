@@ -265,8 +265,8 @@ __device__ __forceinline__ int follow(f32x16_acc (&o)[DT], int& scale, int s, bo
 // it.  The fp16 weights w (16 keys each) are sums of two bf16 numbers; a key's power of two goes from its
 // values to its weights.  `v`: the first key's channels; `there`: how many of the keys there are; `seen`:
 // how many this lane's row sees.
-// Rare, and slow (two-byte loads, twice the products): where every prompt's last tile is such a one, 77
-// tokens 16.0 us against 9.4, 2 x 4192 207 against 175.
+// Rare, and slow (two-byte loads, twice the products): where every tile is such a one, 77 tokens 16.0 us
+// against 9.4, 2 x 4192 207 against 175.
 template <int D>
 __device__ __forceinline__ void uneven_values(f32x16_acc (&o)[D / 32], int& scale,
                                               const uint16_t* v, size_t ldv, int there, int seen,
@@ -364,13 +364,14 @@ __device__ __forceinline__ Reference reference(float c, float z) {
 // Short prompts are a matter of latency: no launch goes in front, keys come from memory straight to
 // registers as the first product's operand, every wave turns the values of its own tiles to fp16 and
 // transposes them through its own part of LDS, and the four waves meet once, at the end.  One workgroup
-// a compute unit, two of 64 channels (2 x 256 rows of 24 heads 8.9 us, one 12.1; three spill): a wave's
+// a compute unit, two of 64 channels (2 x 256 rows of 24 heads 8.6 us, one 12.1; three spill): a wave's
 // keys and values on their way take half of its registers.  16 heads of 128
-// channels, one token 7.4 us, 77 8.6, 200 10.4; with 128 rows a workgroup and a tile after the other
+// channels, one token 7.7 us, 77 8.8, 200 10.4; with 128 rows a workgroup and a tile after the other
 // 7.1, 10.7 and 15.4.  The next tile's keys are asked for as soon as the products have read these, its
 // values once the registers are free of the last ones (both at once: 600 tokens 20.0 us against 18.9).
-// What is left is the way from lengths to rows (two trips to memory; waves wait for two thirds of
-// their time at 77 tokens) and a tile's instructions, one wave a vector unit.
+// What is left is the way from lengths to rows (two trips to memory), code that is met cold, and a tile's
+// 960 vector instructions: waves wait for 64% of their time at 77 tokens, for 70% at one, vector units
+// are busy for 2%.
 template <int D>
 __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const Prompt p) {
     constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;
@@ -727,12 +728,14 @@ __device__ __forceinline__ void wait_barrier() {
 // tile i stands between its halves: K of i and V of i - 1 have been read then, their places are
 // asked for K of i + RING and V of i + RING - 1; K of i + 1 and V of i have landed.
 // 32 rows meet 32 keys in D / 8 products of 32 cycles; beside them stand, a lane, 16 exponentials and
-// about 60 vector instructions.  16576 tokens of 32 heads (eight key heads) of 128 channels 2035 to
-// 2080 us with the launch in front, 1085 to 1107 TFLOP/s, where a library product of 8192^3 reaches 1208
-// to 1379 card by card: matrix cores busy 54% of the time, vector units 47%, LDS 27%, no bank
-// conflicts; the card lowers its clock to 1.96 GHz for it (on zeros 1637 us).  2 x 4192 of 16 heads 170
-// to 178 (matrix cores 46%), twelve prompts up to 4801 of 32 heads 740 (50%), 3 x 1500 of 24 heads of 64
-// channels 34 (18%, vector units 36%: the longest unit's 24 tiles one after the other).  Two phases
+// about 60 vector instructions.  16576 tokens of 32 heads (eight key heads) of 128 channels 2025 to
+// 2190 us card by card with the launch in front, 1028 to 1112 TFLOP/s, where a library product of 8192^3
+// reaches 1208 to 1379: matrix cores busy 57% of the time, vector units 52%, LDS 29%, bank conflicts in
+// 1% of its cycles; the card lowers its clock for it (on zeros 1555 us where it takes 2190).  2 x 4192 of
+// 16 heads 169 to 178 (matrix cores 46%), twelve prompts up to 4801 of 32 heads 725 to 750 (51%), 3 x
+// 1500 of 24 heads of 64 channels 35 (17%, vector units 35%: the longest unit's 24 tiles one after the
+// other), 16576 of 32 heads of 64 channels 1215: as many exponentials for half the products, vector units
+// busy 80% of the time and matrix cores 49%.  Two phases
 // apart with a barrier each, as in the cache's kernel for very many rows, 2304 us; 64 rows a wave, whose
 // operands from LDS serve two products, 2360 (one wave a vector unit hides nothing); hints to the
 // scheduler 2128 against 2097; a wave's priority raised for its products the same.
@@ -1038,25 +1041,27 @@ int64_t few_units(int B, int T, int max_rows, int G, int Hkv) {
     return (rows + kWaveRows - 1) / kWaveRows * B * Hkv;
 }
 
-// The kernel for few rows where its workgroups make one round, or, of 128 channels, two and the prompts
-// are long: there a round beside the launch in front costs less.  us, few | many rows, 128 channels: 4 x
-// 77 rows of 16 heads (192 units) 9.6 | 12.9, 2 x 256 (256) 11.4 | 17.8, 4 x 130 (320) 17.1 | 15.7, 2 x
-// 400 (416, 7 tiles) 22.8 | 21.3, 1 x 600 (304, 10 tiles) 18.9 | 23.6, 1 x 1000 (512) 34.6 | 36.0, 2 x
-// 600 (608) 36.6 | 26.0; 64 channels, 24 heads of eight key heads: 2 x 256 (384) 8.8 | 11.5, 1 x 600
-// (456) 12.9 | 15.9, 8 x 77 (512) 8.0 | 10.1, 2 x 400 (608) 13.4 | 13.1, 12 x 77 (768) 11.2 | 10.5, 1 x
-// 1000 (752) 21.3 | 20.8; 8 heads of two, 1 x 2000 (500) 22.2 | 31.3.
+// The kernel for few rows where its workgroups make one round, or, of 128 channels, one and a quarter and
+// the prompts are long: there the rest of a round beside the launch in front costs less.  us, few | many
+// rows, 128 channels, 16 heads: 4 x 77 rows (192 units) 9.1 | 12.9, 2 x 256 (256) 11.2 | 15.3, 4 x 130
+// (320, 3 tiles) 16.4 | 13.7, 1 x 520 (272, 9 tiles) 17.1 | 18.9, 1 x 600 (304) 18.5 | 21.0, 1 x 700
+// (352) 22.1 | 21.4, 1 x 800 (416) 26.6 | 23.3, 1 x 1000 (512) 31.1 | 27.8, 2 x 400 (416) 21.5 | 17.8, 2
+// x 600 (608) 33.4 | 22.9, 8 heads, 1 x 2000 (504, 32 tiles) 44.9 | 43.0 (with inputs out of the caches 1
+// to 2 more on both sides); 64 channels, 24 heads of eight key heads: 2 x 256 (384) 8.7 | 11.8, 1 x 600
+// (456) 12.8 | 16.4, 8 x 77 (512) 8.1 | 10.7, 2 x 400 (608) 13.8 | 13.8, 12 x 77 (768) 11.9 | 10.9, 1 x
+// 1000 (752) 22.0 | 21.5; 8 heads of two, 1 x 2000 (500) 23.3 | 32.8.
 bool few_rows(int64_t units, int max_rows, int D) {
     const int tiles = (max_rows + kTile - 1) / kTile;
-    return units <= round_of(D) || (D == 128 && units <= 512 && tiles >= 9);
+    return units <= round_of(D) || (D == 128 && units <= 320 && tiles >= 9);
 }
 
 // Waves of the kernel for many rows, eight or four.  Four make rounds of workgroups that end more
 // evenly, two of them a compute unit go through their barriers apart; eight read every tile half as
-// often.  us, eight | four; 128 channels: 2 x 1500 rows of 16 heads 53.9 | 45.6, 1 x 5000 of 8
-// (two key heads) 125.8 | 98.3, 2 x 6000 of 16 320 | 311, 1 x 12000 of 8 (376 units of 256 rows) 335
-// | 301, 1 x 8192 of 16 (512) 303 | 315, 1 x 16576 of 16 1055 | 1072, of 32 (eight key heads) 2032 |
-// 2078.  64 channels, whose registers leave room for a third: 3 x 1500 of 24 43.4 | 39.4, 1 x 16576
-// of 32 1255 | 1177.
+// often.  us, eight | four; 128 channels: 2 x 1500 rows of 16 heads 55.5 | 49.2, 1 x 5000 of 8
+// (two key heads) 121.6 | 97.5, 2 x 6000 of 16 352 | 335, 1 x 12000 of 8 (376 units of 256 rows) 350
+// | 321, of 16 616 | 612, 1 x 8192 of 16 (512) 293 | 313, 1 x 16576 of 16 1110 | 1127, of 32 (eight key
+// heads) 2130 | 2175.  64 channels, whose registers leave room for a third (an earlier form of the
+// kernel): 3 x 1500 of 24 43.4 | 39.4, 1 x 16576 of 32 1255 | 1177.
 bool eight_waves(int pairs, int max_rows, int G, int D) {
     const int64_t units = ((int64_t)max_rows * G + 255) / 256 * pairs;
     return D == 128 && units >= 512 && max_rows >= 128 * kTile;
