@@ -120,7 +120,8 @@ size_t rudder_attention_workspace_bound(int B, int T, int max_rows, int max_kv, 
  *   Q, O     bf16 bits [T][Hq][D], row distances ldq, ldo
  *   kv_len   int32 [B]; max_kv an upper bound on them (larger ones are cut)
  *   sm       the softmax scale, e.g. 1 / sqrt(D); sm times a row's largest element
- *            stays below 2^127
+ *            stays below 2^127, and sm * q . k_j below 2^23 in magnitude (beyond,
+ *            32 bits do not hold a score beside its weight's exponent)
  *   workspace, workspace_bytes  at least rudder_attention_workspace_bytes(...)
  *            bytes (NULL if 0)
  *   B, T, max_rows, max_kv >= 0 (B, T or max_rows 0 is a no-op), Hq a multiple

@@ -11,10 +11,12 @@
 // the codes are those of the norm's rows through rudder_quant_act.
 //
 // One pass: a row's elements stay in registers, as bf16, between the sum and
-// the outputs.  Bound by memory: 16576 x 4096 with the residual to E2M3 codes 97
-// us (459 MB, 4.7 TB/s; a plain copy moves 5.1), 8384 x 2048 to 8 bits 16 (51 MB,
-// 3.2 TB/s: a thousand workgroups that load, sum, round and store once each); a
-// single row 2.2, a launch and the way to memory and back.
+// the outputs.  Bound by memory: 16576 x 4096 with the residual to bf16 rows 102 us
+// (5.3 TB/s, what a plain copy moves), to E2M3 codes 95 to 100 (459 MB, 4.6 TB/s) and
+// to the 4-bit int ones 95; 8384 x 2048 to bf16 rows 12 (5.6 TB/s), to 8 bits 16 (51
+// MB, 3.2 TB/s) and to 4 bits 16, the launch of a wave for one row each, whose
+// loads, sum, codes and stores follow one another beside no other row's; a single
+// row 2.3, a launch and the way to memory and back.
 #include "rudder_block_launch.h"
 
 namespace rudder {
@@ -330,6 +332,9 @@ hipError_t start(const Norm& a, hipStream_t stream) {
 // rows of 2048 channels 5.4 | 6.1, 1024 7.4 | 6.6; 1024 of 4096 9.7 | 10.6 (bf16 rows 6.6 | 7.8, 1536
 // E2M3 13.6 | 13.5); 1536 of 8192 21.4 | 27.4; 16576 of 4096, E2M3 137 | 103.  Eight rows a workgroup
 // 107, 16576 of 4096 8-bit 114 against 106; two rows 110.
+// Wider rows than 8192 channels are rare and take one shape for all widths, eight waves a row and up to
+// sixteen pieces a lane, of which narrow ones leave most unused: 2048 x 65536 with the residual to bf16
+// rows 212 us (5.1 TB/s), 8384 x 12288 252 (3.3 TB/s; 8384 x 8192 110 with 5.0) and to 8 bits 358.
 template <int OUT>
 hipError_t launch(const Norm& a, hipStream_t stream) {
     if (a.K > 8192) return start<OUT, 8, 1, 16>(a, stream);

@@ -370,8 +370,7 @@ __device__ __forceinline__ Reference reference(float c, float z) {
 // 7.1, 10.7 and 15.4.  The next tile's keys are asked for as soon as the products have read these, its
 // values once the registers are free of the last ones (both at once: 600 tokens 20.0 us against 18.9).
 // What is left is the way from lengths to rows (two trips to memory), code that is met cold, and a tile's
-// 960 vector instructions: waves wait for 64% of their time at 77 tokens, for 70% at one, vector units
-// are busy for 2%.
+// 960 vector instructions: waves wait for 64% of their time at 77 tokens, for 70% at one.
 template <int D>
 __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const Prompt p) {
     constexpr int kKS = D / 16, kDT = D / 32, kIts = D / 32, kBytes = kTile * D * 2;

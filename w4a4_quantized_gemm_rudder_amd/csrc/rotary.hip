@@ -55,7 +55,7 @@ __device__ __forceinline__ float turns(int64_t position, double freq) {
 
 // A wave takes a row (or, with SPLIT, four waves a quarter of its heads each); a lane 16 channels of
 // every fourth or eighth head.  A row's cosines and sines are formed once, one a lane.  Bound by memory:
-// 8384 rows of 32 heads of 128 channels move 137 MB at 5.8 TB/s; 48 single tokens of 40 heads 3.4 us,
+// 8384 rows of 32 heads of 128 channels move 137 MB at 5.9 TB/s; 48 single tokens of 40 heads 3.3 us,
 // a launch and the way from lengths to rows to outputs.
 template <int D, bool PAIRS, bool SPLIT, bool TURNS>
 __global__ void __launch_bounds__(256) rotary_kernel(const Rotary a) {
