@@ -31,6 +31,7 @@
 // unrounded values.  Products with bf16 states take P as the sum of two bf16 numbers.
 #include <cmath>
 
+#include "rudder_device.h"
 #include "rudder_operators.h"
 
 namespace rudder {
@@ -80,11 +81,6 @@ struct Problem {
     float* part_o;      // [pieces][units - whole][rows of a unit][D]
     float2* part_ml;    // [pieces][units - whole][rows of a unit]
 };
-
-// a / b of wave-uniform values, back in a scalar register (the division runs on the vector units)
-__device__ __forceinline__ int quotient(int a, int b) {
-    return __builtin_amdgcn_readfirstlane(a / b);
-}
 
 // Unit number -> row tile of a pair.  Workgroups go round robin to the eight dies: where the pairs
 // divide by eight, the units of a pair, which read the same keys, are kept on one (dies = 8, else
@@ -144,19 +140,6 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 // Bits 2 and 3 exchanged: key number <-> accumulator row (its own inverse).
 __device__ __forceinline__ int swap23(int r) {
     return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    union { bf16x2_t v; uint32_t u; } r;
-    r.v = (bf16x2_t){(__bf16)a, (__bf16)b};
-    return r.u;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    union { f16x2_t v; uint32_t u; } r;
-    r.v = (f16x2_t){(_Float16)a, (_Float16)b};
-    return r.u;
 }
 
 // Weights as operands: for the cache in fp16.  For states in bf16, whose 8 bits alone would put as
@@ -413,13 +396,6 @@ __device__ __forceinline__ void interleave() {
 // The running maximum is raised only where a score passes it by more than 2^6 (P has room for it):
 // most tiles then need no exchange between lanes and no rescaling of O.
 constexpr float kLazy = 6.0f;
-
-// Orders a wave's LDS accesses of different lanes (the hardware keeps their order; this keeps the
-// compiler's).
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
 
 // The 32 query rows of a wave pass through LDS, so that global memory sees whole rows: a lane's
 // share of its row is 16 bytes in 32 (loads) or 8 in 16 (stores).  2 x 4192 rows of 16 heads over

@@ -18,6 +18,7 @@
 // result is off by a few 2^-19 * sum |x|, whatever its own size.  A code is
 // off by up to a half, which makes that a few 2^-18 of what the weights'
 // rounding may cost; results far below sum |x| have it relative to that.
+#include "rudder_device.h"
 #include "rudder_operators.h"
 
 namespace rudder {
@@ -69,13 +70,6 @@ __global__ void quantize_weights_grouped_kernel(const uint16_t* __restrict__ W, 
 // ---------------------------------------------------------------------------
 // The product.
 // ---------------------------------------------------------------------------
-// Orders a wave's LDS accesses of different lanes (the hardware keeps their order; this keeps the
-// compiler's).
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 __device__ __forceinline__ bf16x8_t widen_codes(uint32_t w, uint32_t magic) {
     union { uint32_t u[4]; bf16x8_t v; } r;
 #pragma unroll

@@ -18,6 +18,7 @@
 // loads, sum, codes and stores follow one another beside no other row's; a single
 // row 2.3, a launch and the way to memory and back.
 #include "rudder_block_launch.h"
+#include "rudder_device.h"
 
 namespace rudder {
 namespace {
@@ -36,16 +37,6 @@ struct Norm {
     float* row_scale;
 };
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    union { bf16x2_t v; uint32_t u; } r;
-    r.v = (bf16x2_t){(__bf16)a, (__bf16)b};
-    return r.u;
-}
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 // Two bf16 values a word, added in 32 bits and rounded.
 __device__ __forceinline__ uint32_t add_bf16(uint32_t a, uint32_t b) {
     return pack_bf16(low(a) + low(b), high(a) + high(b));
@@ -63,13 +54,9 @@ __device__ __forceinline__ void load8(const float* from, float (&to)[8]) {
     to[7] = v.w;
 }
 
-// A store past the caches, for what is not read again soon: the residual stream, which the next norm
-// wants, several linears later (16576 x 4096 rows, with their values read back, 150 us, through the
-// caches 152), and values (152, 190).  Rows and codes go to the next call and stay.
-__device__ __forceinline__ void stream16(void* to, uint4 x) {
-    typedef unsigned v4u __attribute__((ext_vector_type(4)));
-    __builtin_nontemporal_store(v4u{x.x, x.y, x.z, x.w}, static_cast<v4u*>(to));
-}
+// Stored past the caches: the residual stream, which the next norm wants, several linears later (16576 x
+// 4096 rows, with their values read back, 150 us, through the caches 152), and values (152, 190).  Rows and
+// codes go to the next call and stay.
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "rudder_block_launch.h"
+#include "rudder_device.h"
 
 namespace rudder {
 namespace {
@@ -31,7 +32,6 @@ namespace {
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_acc __attribute__((ext_vector_type(16)));
 
 // Lambdas that hold registers of the kernel around them: a call would put those into memory.
@@ -68,19 +68,6 @@ struct Prompt {
     int slots;
 };
 
-__device__ __forceinline__ int quotient(int a, int b) {
-    return __builtin_amdgcn_readfirstlane(a / b);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    union { bf16x2_t v; uint32_t u; } r;
-    r.v = (bf16x2_t){(__bf16)a, (__bf16)b};
-    return r.u;
-}
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    union { f16x2_t v; uint32_t u; } r;
-    r.v = (f16x2_t){(_Float16)a, (_Float16)b};
-    return r.u;
-}
 __device__ __forceinline__ f32x16_acc mma_bf16(uint4 a, uint4 b, f32x16_acc c) {
     union { uint4 u; bf16x8_t v; } x, y;
     x.u = a;
@@ -222,13 +209,6 @@ __device__ __forceinline__ void store_values(uint8_t* image, const uint4 (&x)[4]
         *reinterpret_cast<uint2*>(image + place<8>(ch + 1, to >> 1) + (to & 1) * 8) =
             make_uint2(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]));
     }
-}
-
-// Orders a wave's LDS accesses of different lanes (the hardware keeps their order; this keeps the
-// compiler's).
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 // The multiple of 8 that brings a largest magnitude of these bits into [2^7, 2^15); at most 120, so

@@ -8,6 +8,7 @@
 // every int32 position and frequencies of up to 2^24, and is rounded to 32 bits
 // only then (2^-25 turns).
 #include "rudder_block_launch.h"
+#include "rudder_device.h"
 
 namespace rudder {
 namespace {
@@ -22,29 +23,13 @@ struct Rotary {
     uint16_t *Qo, *Ko;
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    union { bf16x2_t v; uint32_t u; } r;
-    r.v = (bf16x2_t){(__bf16)a, (__bf16)b};
-    return r.u;
-}
-
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // A pair in one word, turned.
 __device__ __forceinline__ uint32_t turn(uint32_t w, float c, float s) {
     const float x = low(w), y = high(w);
     return pack_bf16(fmaf(x, c, -(y * s)), fmaf(y, c, x * s));
 }
-// A store past the caches: into buffers of their own 8384 rows of 32 heads of 128 channels 23.7 us,
-// through the caches 31; in place, behind the linear that wrote them and in front of attention or an
-// append, the same.
-__device__ __forceinline__ void stream16(uint16_t* to, const uint32_t (&x)[4]) {
-    typedef unsigned v4u __attribute__((ext_vector_type(4)));
-    __builtin_nontemporal_store(v4u{x[0], x[1], x[2], x[3]}, reinterpret_cast<v4u*>(to));
-}
 
-// position * freq in turns, in [-1/2, 1/2]
+// position * freq in turns, at most 3/4 in magnitude
 __device__ __forceinline__ float turns(int64_t position, double freq) {
     constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;   // 1 / (2 pi)
     const double p = (double)position, a = p * freq, da = __builtin_fma(p, freq, -a);
@@ -122,8 +107,11 @@ __global__ void __launch_bounds__(256) rotary_kernel(const Rotary a) {
                     y[j] = pack_bf16(fmaf(f0, c0, e0 * s0), fmaf(f1, c1, e1 * s1));
                 }
             }
-            stream16(to + at0, x);
-            stream16(to + at1, y);
+            // past the caches: into buffers of their own 8384 rows of 32 heads of 128 channels 23.7 us,
+            // through the caches 31; in place, behind the linear that wrote them and in front of
+            // attention or an append, the same
+            stream16(to + at0, make_uint4(x[0], x[1], x[2], x[3]));
+            stream16(to + at1, make_uint4(y[0], y[1], y[2], y[3]));
         }
         i += gridDim.x * 4;
     } while (TURNS && i < n);
