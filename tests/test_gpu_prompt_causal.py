@@ -131,6 +131,31 @@ def test_values_that_are_not_finite_among_uneven_ones(rudder, D, rows, among):
             aref.assert_within(f"{at} {bad}", got[:at], want, bound + 2.0 ** -24 * bound)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,among", KERNELS)
+def test_large_values_of_no_weight_beside_small_ones(rudder, D, rows, among):
+    """A row's own tile holds a token of large values and no weight, and small values of a small weight
+    beside a zero that takes the rest: the small ones are the output."""
+    log(f"case prompt causal no weight D={D} rows={rows}/{among}")
+    g = torch.Generator().manual_seed(rows + 4)
+    for large, small in ((72, -66), (100, -30), (30, -100)):
+        for at in (0, 30, 63):
+            power, weight = torch.full((rows,), float(small) - 4), torch.full((rows,), -60.0)
+            i = torch.arange(rows) % TILE
+            power[i == at], weight[i == at] = large, -(large - small + 60.0)
+            power[i == 4], weight[i == 4] = small, -20.0
+            weight[i == 7] = 0.0
+            q, k, v = (torch.randn(rows, h, D, generator=g) * 0.1 for h in (2, 1, 1))
+            q[:, :, 0], k[:, :, 0] = 8.0, (weight * math.log(2) / 8.0)[:, None]
+            v = (v + 1.0).double() * (2.0 ** power.double())[:, None, None]
+            v[i == 7] = 0
+            q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+            got = _run(rudder, q, k, v, 1.0, among)
+            some = torch.cat([torch.arange(min(rows, 70)), torch.arange(70, rows, 9)])
+            want, bound = _bounds(q, k, v, 1.0, some)
+            aref.assert_within(f"{large} {small} {at}", got[some], want, bound)
+
+
 def test_tokens_of_every_size_in_a_long_prompt(rudder):
     """The same on the kernel of eight waves, all rows of two heads."""
     log("case long prompt causal sizes")

@@ -241,22 +241,21 @@ __device__ __forceinline__ int follow(f32x16_acc (&o)[DT], int& scale, int s, bo
 }
 
 // 32 values of a tile that a row sees only part of, and that are uneven: straight from memory, in bf16,
-// with every row at the power of two of what it sees of them, so that nothing behind a row takes bits from
-// it.  The fp16 weights w (16 keys each) are sums of two bf16 numbers; a key's power of two goes from its
-// values to its weights.  `v`: the first key's channels; `there`: how many of the keys there are; `seen`:
-// how many this lane's row sees.
+// with every row at the power of two of those that it weighs, so that nothing behind a row takes bits from
+// it, nor what it sees and does not weigh.  The fp16 weights w (16 keys each) are sums of two bf16 numbers;
+// a key's power of two goes from its values to its weights.  `v`: the first key's channels; `there`: how
+// many of the keys there are.
 // Rare, and slow (two-byte loads, twice the products): where every tile is such a one, 77 tokens 16.0 us
 // against 9.4, 2 x 4192 207 against 175.
 template <int D>
 __device__ __forceinline__ void uneven_values(f32x16_acc (&o)[D / 32], int& scale,
-                                              const uint16_t* v, size_t ldv, int there, int seen,
-                                              uint4 w0, uint4 w1) {
+                                              const uint16_t* v, size_t ldv, int there, uint4 w0,
+                                              uint4 w1) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane), "+s"(ldv));      // keeps the addresses out of the loop around this
     const int half = lane >> 5;
     auto of_lane = [](int from, int x) { return __builtin_amdgcn_ds_bpermute(from * 4, x); };
-    // a key a lane: its largest magnitude, that of the keys up to it, and what the lane's row sees
-    int top = 0;
+    int top = 0;                                   // a key a lane: its largest magnitude
     if ((lane & 31) < there) {
         const uint4* row = reinterpret_cast<const uint4*>(v + (size_t)(lane & 31) * ldv + half * (D / 2));
 #pragma unroll
@@ -271,16 +270,18 @@ __device__ __forceinline__ void uneven_values(f32x16_acc (&o)[D / 32], int& scal
         }
     }
     top = max(top, of_lane(lane ^ 32, top));
-    const int key_power = min(max((top >> 7) - 127, -120), 120);
-#pragma unroll 1
-    for (int off = 1; off < 32; off <<= 1) {
-        const int before = of_lane(lane - off, top);
-        if ((lane & 31) >= off) top = max(top, before);
+    // the lane's two keys of word j of weights x, and the largest that its row weighs
+    auto key_of = [&](int x, int j) { return 16 * x + 8 * (j >> 1) + 4 * half + 2 * (j & 1); };
+    int most = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 w = i < 4 ? w0 : w1;
+        const uint32_t word = i % 4 == 0 ? w.x : i % 4 == 1 ? w.y : i % 4 == 2 ? w.z : w.w;
+        const int t0 = of_lane(key_of(i / 4, i % 4), top), t1 = of_lane(key_of(i / 4, i % 4) + 1, top);
+        most = max(most, max(word & 0xFFFFu ? t0 : -1, word >> 16 ? t1 : -1));
     }
-    top = of_lane(min(max(seen, 1), 32) - 1, top);
-    int any = w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w;
-    any |= of_lane(lane ^ 32, any);
-    follow(o, scale, scale_of(top), seen > 0 && any != 0);
+    most = max(most, of_lane(lane ^ 32, most));
+    follow(o, scale, scale_of(max(most, 0)), most >= 0);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const uint4 w = x ? w1 : w0;
@@ -289,8 +290,9 @@ __device__ __forceinline__ void uneven_values(f32x16_acc (&o)[D / 32], int& scal
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             __builtin_amdgcn_sched_barrier(0);     // few loads at a time: registers are full
-            const int key = 16 * x + 8 * (j >> 1) + 4 * half + 2 * (j & 1);
-            const int power0 = of_lane(key, key_power), power1 = of_lane(key + 1, key_power);
+            const int key = key_of(x, j);
+            const int power0 = min(max((of_lane(key, top) >> 7) - 127, -120), 120);
+            const int power1 = min(max((of_lane(key + 1, top) >> 7) - 127, -120), 120);
             union { uint32_t u; f16x2_t h; } p;
             p.u = word[j];
             const float e0 = __builtin_amdgcn_ldexpf((float)p.h[0], scale + power0);
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
 #pragma unroll 1
         for (int key = uneven_at; key < min(uneven_at + kTile, n); key += 32) {
             uneven_values<D>(o, scale, p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D, p.ldv,
-                             n - key, limit - key, w[0], w[1]);
+                             n - key, w[0], w[1]);
             w[0] = w[2];
             w[1] = w[3];
         }
@@ -924,7 +926,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 64 ? 3 : 2) prompt_wide_kerne
             const int key = at + 32 * hf;
             if (apart && key < most) {             // not in a half in front of which all has been seen
                 uneven_values<D>(o, scale, p.V + (size_t)(r0 + key) * p.ldv + (size_t)h * D, p.ldv,
-                                 n - key, limit - key, pend0, pend1);
+                                 n - key, pend0, pend1);
                 pend0 = pend1 = make_uint4(0, 0, 0, 0);
             }
         }
