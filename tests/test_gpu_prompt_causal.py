@@ -156,6 +156,26 @@ def test_large_values_of_no_weight_beside_small_ones(rudder, D, rows, among):
             aref.assert_within(f"{large} {small} {at}", got[some], want, bound)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,among", KERNELS)
+def test_zeros_in_front_of_large_values(rudder, D, rows, among):
+    """Tiles of small values, then tiles of large ones whose first tokens are zeros: rows that see of these
+    only the zeros have what the small ones give."""
+    log(f"case prompt causal zeros D={D} rows={rows}/{among}")
+    g = torch.Generator().manual_seed(rows + 5)
+    q, k = (torch.randn(rows, h, D, generator=g).to(torch.bfloat16) for h in (2, 1))
+    i = torch.arange(rows)
+    for small, large in ((-90, 100), (-100, 20), (0, 120)):
+        v = torch.randn(rows, 1, D, generator=g) + 2.0
+        v = v.double() * (2.0 ** torch.where(i // TILE % 2 > 0, large, small).double())[:, None, None]
+        v[i % (2 * TILE) // 10 == 6] = 0               # 60 .. 69 of every 128
+        v = v.to(torch.bfloat16)
+        got = _run(rudder, q, k, v, 0.1, among)
+        some = torch.cat([torch.arange(50, min(rows, 90)), torch.arange(min(180, rows), rows, 5)])
+        want, bound = _bounds(q, k, v, 0.1, some)
+        aref.assert_within(f"{small} {large}", got[some], want, bound)
+
+
 def test_tokens_of_every_size_in_a_long_prompt(rudder):
     """The same on the kernel of eight waves, all rows of two heads."""
     log("case long prompt causal sizes")

@@ -171,9 +171,10 @@ __device__ __forceinline__ uint32_t finite_top(uint4 (&x)[N][4], int& bad, uint3
 }
 
 // Whether a token's largest magnitude is less than 2^-8 of the tile's: a row that sees the one and not the
-// other would lose more than 2^-24 of it to the tile's power of two.
+// other would lose more than 2^-24 of it to the tile's power of two, or, where it is 0, bits of what
+// it has summed.
 __device__ __forceinline__ bool uneven(uint32_t token, uint32_t tile) {
-    return token > 0 && token + (8 << 7) < tile;
+    return token + (8 << 7) < tile;
 }
 // The largest of four neighbouring lanes, which hold 32 channels of a token.
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) prompt_few_kernel(const 
         if (part) {                                // four lanes hold a token's channels
             bool any = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) any |= uneven(quad_max(tops[i]), top);
+            for (int i = 0; i < 4; ++i)
+                any |= uneven(quad_max(tops[i]), top) && at + value_keys(lane) * 4 + i < n;
             apart = __any(any);
         }
         const float f = __uint_as_float((uint32_t)(127 + s) << 23);
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(256) prompt_values_kernel(const Prompt p) {
     const int slot = first_slot(r0, b) + (int)blockIdx.x;
     if (wave == 0) {                               // a token a lane
         token = max(max(tokens[0][lane], tokens[1][lane]), max(tokens[2][lane], tokens[3][lane]));
-        const int apart = __any(uneven(token, top)) ? kUneven : 0;
+        const int apart = __any(uneven(token, top) && at + lane < n) ? kUneven : 0;
         if (lane == 0)
             p.notes[(size_t)h * p.slots + slot] = s + 128 + (first_bad << 8) + apart;
     }
