@@ -715,7 +715,7 @@ __device__ __forceinline__ void wait_barrier() {
 // 2190 us card by card with the launch in front, 1028 to 1112 TFLOP/s, where a library product of 8192^3
 // reaches 1208 to 1379: matrix cores busy 57% of the time, vector units 52%, LDS 29%, bank conflicts in
 // 1% of its cycles; the card lowers its clock for it (on zeros 1555 us where it takes 2190).  2 x 4192 of
-// 16 heads 169 to 178 (matrix cores 46%), twelve prompts up to 4801 of 32 heads 725 to 750 (51%), 3 x
+// 16 heads 169 to 181 (matrix cores 46%), twelve prompts up to 4801 of 32 heads 725 to 773 (51%), 3 x
 // 1500 of 24 heads of 64 channels 35 (17%, vector units 35%: the longest unit's 24 tiles one after the
 // other), 16576 of 32 heads of 64 channels 1215: as many exponentials for half the products, vector units
 // busy 80% of the time and matrix cores 49%.  Two phases
